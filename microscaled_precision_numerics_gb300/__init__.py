@@ -1,10 +1,10 @@
 """Python binding of libmxnum.so (block-scaled microscaling numerics on GB300, sm_103a).
 
 Argument marshalling only: every function passes ``tensor.data_ptr()`` values, sizes, seeds and the
-current CUDA stream to the C ABI declared in ``include/mxnum.h`` and raises ``MXError`` on a non-OK
+current CUDA stream to the C ABI declared in ``include/mxnum.h`` (and ``mxnum_generate.h``) and raises ``MXError`` on a non-OK
 status.  No arithmetic happens here and there is no CPU fallback: if the CUDA library is missing or
 a tensor is not on a CUDA device, the call raises.  ``alloc_*`` helpers only create output tensors
-of the right sizes (``torch.empty`` on the input's device).
+of the right sizes (``torch.empty`` on the input's device; the key/value cache cleared).
 """
 from __future__ import annotations
 
@@ -72,6 +72,14 @@ def lib() -> ctypes.CDLL:
                 "mx_wgrad_bf16_dq_nvfp4": (I32, [P, P, P, P, I32, I64, I64, I64, P, I64, P]),
                 "mx_fp8_blockwise_gemm": (I32, [P, P, P, P, I64, I64, I64, P, I64, P]),
                 "mx_fp8_blockwise_gemm_wgrad": (I32, [P, P, P, P, I64, I64, I64, P, I64, P]),
+                "mx_kv_page_bytes": (I64, [I64, I64, I64]),
+                "mx_kv_slots": (I32, [P, P, I64, I64, P, I64, I64, P, I64, P, P, P, P, P, I64, P, P, P]),
+                "mx_nvfp4_kv_append": (I32, [P, I64, I64, P, I64, I64, P, I64, P, P, P, I64, I64, I64, I64, P]),
+                "mx_nvfp4_kv_gather": (I32, [P, I64, I64, I64, I64, P, I64, P, P, P, I64, I64, P, I64, I64, P]),
+                "mx_kv_attention_workspace_bytes": (SZ, [I64]),
+                "mx_nvfp4_kv_attention": (I32, [P, I64, I64, I64, I64, P, P, I64, I64, P, I64, I64, P, I64, I64, I64,
+                                                I64, P, P, ctypes.c_float, I64, P, I64, I64, P, P, SZ, P]),
+                "mx_nvfp4_matvec": (I32, [P, I64, P, P, P, I32, I64, I64, I64, P, I64, I32, P]),
                 "mx_check_device_status": (I32, []),
                 "mx_check_stream_status": (I32, [P]),
                 "mx_watchdog_selftest": (I32, [I32, U64, P]),
@@ -500,6 +508,155 @@ def mx_grouped_scaled_gemm(fmt: int, group_offsets, a, sa, alpha_a_rows, b, sb, 
         N, K, _p(d), _stream(stream)))
 
 
+# ------------------------------------------------------------------------------------------------
+# generation: NVFP4 key/value cache, attention over it, products of a few tokens with NVFP4 weights
+# ------------------------------------------------------------------------------------------------
+
+MX_KV_MAX_REQUESTS = 4096
+MX_MATVEC_MAX_TOKENS = 64
+
+
+def _ptrs(*tensors):
+    """The device pointers of the tensors (None stays None), all on the current device: _p() for the calls of a
+    generation step, which are many and short."""
+    if not tensors[0].is_cuda:
+        _p(tensors[0])                                  # raises
+    cur = torch.cuda.current_device()
+    return [t.data_ptr() if t is not None and t.is_cuda and t.get_device() == cur else _p(t) for t in tensors]
+
+
+def _i32(fn: str, name: str, t, n: int):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{fn}: {name} must be int32, got {t.dtype}")
+    _need(fn, name, t, 4 * n)
+
+
+def _f32(fn: str, name: str, t, n: int):
+    if t.dtype != torch.float32:
+        raise TypeError(f"{fn}: {name} must be float32, got {t.dtype}")
+    _need(fn, name, t, 4 * n)
+
+
+def _block_table(fn: str, t, requests: int):
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] < requests or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{fn}: block_table must be int32 [requests, pages] with unit column stride")
+    return t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _kv_cache(fn: str, cache, s_k, s_v):
+    """(pages, page size, kv heads, head dimension) of a cache [pages, kv heads, page_size / 16, 18 * head_dim]."""
+    if cache.dtype != torch.uint8 or cache.dim() != 4 or cache.shape[3] % 18 or not cache.is_contiguous():
+        raise ValueError(f"{fn}: cache must be a contiguous uint8 [pages, kv_heads, page_size / 16, 18 * head_dim]")
+    pages, heads, groups, record = cache.shape
+    _f32(fn, "s_k", s_k, heads)
+    _f32(fn, "s_v", s_v, heads)
+    return pages, 16 * groups, heads, record // 18
+
+
+def _heads_bf16(fn: str, name: str, t, heads, dim: int, tokens=None):
+    """A BF16 [tokens, heads, dim] view with unit element stride; its token and head strides."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads) or (
+            tokens is not None and t.shape[0] != tokens) or t.stride(2) != 1:
+        raise ValueError(f"{fn}: {name} must be bfloat16 [{tokens if tokens is not None else 'tokens'}, "
+                         f"{heads if heads is not None else 'heads'}, {dim}] with unit element stride, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    T, H = t.shape[0], t.shape[1]
+    head = t.stride(1) if H > 1 else dim
+    return (t.stride(0) if T > 1 else H * head), head
+
+
+def kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().mx_kv_page_bytes(page_size, kv_heads, head_dim))
+
+
+def kv_attention_workspace_bytes(head_dim: int) -> int:
+    return int(lib().mx_kv_attention_workspace_bytes(head_dim))
+
+
+def mx_kv_slots(seq_lens, new_lens, page_size: int, block_table, free_pages, free_count, q_start, total_lens, slots,
+                positions, free_left, unplaced, stream=None):
+    """Page and slot maps of a step (see include/mxnum_generate.h).  total_lens may be seq_lens, free_left may be free_count."""
+    fn, R, T = "mx_kv_slots", seq_lens.numel(), slots.numel()
+    width, row = _block_table(fn, block_table, R)
+    for name, t, n in (("seq_lens", seq_lens, R), ("new_lens", new_lens, R), ("free_pages", free_pages, 0),
+                       ("free_count", free_count, 1), ("q_start", q_start, R + 1), ("total_lens", total_lens, R),
+                       ("slots", slots, T), ("positions", positions, T), ("free_left", free_left, 1),
+                       ("unplaced", unplaced, 1)):
+        _i32(fn, name, t, n)
+    p = _ptrs(seq_lens, new_lens, block_table, free_pages, free_count, q_start, total_lens, slots, positions, free_left, unplaced)
+    _check(fn, lib().mx_kv_slots(p[0], p[1], R, page_size, p[2], width, row, p[3], free_pages.numel(), p[4], p[5], p[6],
+                                 p[7], p[8], T, p[9], p[10], _stream(stream)))
+
+
+def mx_nvfp4_kv_append(k, v, slots, s_k, s_v, cache, stream=None):
+    """Quantize keys and values [T, kv_heads, head_dim] (BF16, any token and head stride) into the cache at slots [T]."""
+    fn = "mx_nvfp4_kv_append"
+    pages, page, heads, dim = _kv_cache(fn, cache, s_k, s_v)
+    kt, kh = _heads_bf16(fn, "k", k, heads, dim)
+    T = k.shape[0]
+    vt, vh = _heads_bf16(fn, "v", v, heads, dim, T)
+    _i32(fn, "slots", slots, T)
+    p = _ptrs(k, v, slots, s_k, s_v, cache)
+    _check(fn, lib().mx_nvfp4_kv_append(p[0], kt, kh, p[1], vt, vh, p[2], T, p[3], p[4], p[5], pages, page, heads, dim,
+                                        _stream(stream)))
+
+
+def mx_nvfp4_kv_gather(cache, slots, s_k, s_v, k, v, stream=None):
+    """Read the cached tokens at slots [T] back into k, v [T, kv_heads, head_dim] (BF16, any token and head stride)."""
+    fn = "mx_nvfp4_kv_gather"
+    pages, page, heads, dim = _kv_cache(fn, cache, s_k, s_v)
+    kt, kh = _heads_bf16(fn, "k", k, heads, dim)
+    T = k.shape[0]
+    vt, vh = _heads_bf16(fn, "v", v, heads, dim, T)
+    _i32(fn, "slots", slots, T)
+    p = _ptrs(cache, slots, s_k, s_v, k, v)
+    _check(fn, lib().mx_nvfp4_kv_gather(p[0], pages, page, heads, dim, p[1], T, p[2], p[3], p[4], kt, kh, p[5], vt, vh,
+                                        _stream(stream)))
+
+
+def mx_nvfp4_kv_attention(q, q_start, seq_lens, block_table, cache, s_k, s_v, scale: float, max_q: int, out, workspace,
+                          lse=None, window: int = 0, stream=None):
+    """Attention of a step's new tokens q [T, heads, head_dim] over the cache into out (and lse [T, heads], FP32)."""
+    fn = "mx_nvfp4_kv_attention"
+    pages, page, kv_heads, dim = _kv_cache(fn, cache, s_k, s_v)
+    qt, qh = _heads_bf16(fn, "q", q, None, dim)
+    T, heads = q.shape[0], q.shape[1]
+    ot, oh = _heads_bf16(fn, "out", out, heads, dim, T)
+    R = seq_lens.numel()
+    width, row = _block_table(fn, block_table, R)
+    _i32(fn, "seq_lens", seq_lens, R)
+    _i32(fn, "q_start", q_start, R + 1)
+    if lse is not None:
+        _f32(fn, "lse", lse, T * heads)
+    if not workspace.is_contiguous():
+        raise ValueError(f"{fn}: workspace must be contiguous")
+    p = _ptrs(q, q_start, seq_lens, block_table, cache, s_k, s_v, out, lse, workspace)
+    _check(fn, lib().mx_nvfp4_kv_attention(p[0], qt, qh, T, heads, p[1], p[2], R, max_q, p[3], width, row, p[4], pages, page,
+                                           kv_heads, dim, p[5], p[6], scale, window, p[7], ot, oh, p[8], p[9],
+                                           workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mx_nvfp4_matvec(x, q, s, s2, s2_scope: int, y, stream=None):
+    """y = s2 * x @ W^T for x BF16 [M, K] (M <= MX_MATVEC_MAX_TOKENS, any row stride) and W given as NVFP4 codes q [N, K/2],
+    GEMM-layout scales s and FP32 second-level scales s2; y BF16 or FP32 [M, N] (any row stride)."""
+    fn = "mx_nvfp4_matvec"
+    x = _bf16_bits(x)
+    M, K = x.shape
+    if q.dim() != 2 or 2 * q.shape[1] != K:
+        raise ValueError(f"{fn}: q must be [N, {K // 2}], got {tuple(q.shape)}")
+    N = q.shape[0]
+    if y.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{fn}: y must be bfloat16 or float32")
+    if y.shape[0] != M or y.shape[1] != N or (N > 1 and y.stride(1) != 1):
+        raise ValueError(f"{fn}: y must be [{M}, {N}] with unit column stride")
+    _need(fn, "q", q, N * K // 2)
+    _need(fn, "s", s, (N + 127) // 128 * ((K // 16 + 3) // 4) * 512)
+    _f32(fn, "s2", s2, _alpha_count(s2_scope, N))
+    p = _ptrs(x, q, s, s2, y)
+    _check(fn, lib().mx_nvfp4_matvec(p[0], x.stride(0) if M > 1 else K, p[1], p[2], p[3], s2_scope, M, N, K, p[4],
+                                     y.stride(0) if M > 1 else N, int(y.dtype == torch.float32), _stream(stream)))
+
+
 def mx_count_mismatch(x, y, count, stream=None):
     n = x.numel() * x.element_size()
     if y.numel() * y.element_size() != n:
@@ -534,6 +691,13 @@ def alloc_nvfp4_rows(rows: int, k: int, device):
     return {"q": torch.empty((rows, k // 2), dtype=torch.uint8, device=device),
             "s": _u8(scale_bytes(rows, k, 16), device),
             "s2": torch.empty(rows, dtype=torch.float32, device=device)}
+
+
+def alloc_nvfp4_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device):
+    """An empty NVFP4 key/value cache [pages, kv_heads, page_size / 16, 18 * head_dim]."""
+    if kv_page_bytes(page_size, kv_heads, head_dim) == 0:
+        raise ValueError("page_size must be a multiple of 16 and head_dim 64, 128 or 256")
+    return torch.zeros((pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8, device=device)
 
 
 def alloc_nvfp4_rows_grouped(rows: int, G: int, k: int, device):

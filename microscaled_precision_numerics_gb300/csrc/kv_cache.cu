@@ -1,0 +1,325 @@
+// kv_cache.cu -- the NVFP4 key/value cache of a generation step: page and slot maps from the requests' lengths,
+// the write of new keys and values, and the reading back of cached ones as BF16.
+//
+// 4-bit RL pages: rollout engines run on NVFP4 (Miles page), and a key/value cache in few bits has scales that are
+// calibrated ahead (NeMo RL FP8 page, "FP8 KV cache"); here the second-level scale S is one FP32 per kv head.
+#include "mx_internal.h"
+#include "mx_kv.cuh"
+
+namespace mxk {
+
+namespace {
+
+// ------------------------------------------------------------------------------------------------
+// Page and slot maps.
+//
+// For request r with L_r cached and N_r new tokens and pages of P tokens: had_r = ceil(L_r / P), have_r =
+// max(had_r, min(ceil((L_r + N_r) / P), W)), W the table's width.  The new pages, in request order, pop the free stack from
+// its top: new page k is free[F - 1 - k], or -1 once the stack is empty.  New token t of request r (t counted
+// over all requests) sits at position L_r + t - start_r in page table[r][position / P].
+//
+// Two exclusive sums over the requests (tokens and pages) and then independent look-ups: a few kilobytes, bound by
+// latency.  Every CTA of the one cluster sums all requests for itself (R / 1024 steps a thread) rather
+// than wait for another launch; the outputs are shared out afterwards.
+// ------------------------------------------------------------------------------------------------
+constexpr int SLOT_THREADS = 1024;
+
+struct SlotArgs {
+    const int32_t* seq_lens;
+    const int32_t* new_lens;
+    int R;
+    uint32_t page;
+    int32_t* table;
+    int64_t width, stride;
+    const int32_t* free_pages;
+    int64_t free_capacity;
+    const int32_t* free_count;
+    int32_t *q_start, *total_lens, *slots, *positions;
+    int64_t max_tokens;
+    int32_t *free_left, *unplaced;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Largest i in [0, n) with v[i] <= x (v[0] = 0 <= x, v non-decreasing).
+__device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a) {
+    extern __shared__ int sm[];
+    int* s_start = sm;                         // [R + 1] first new token of each request
+    int* s_pages = s_start + a.R + 1;          // [R + 1] first new page of each request
+    int* s_seq = s_pages + a.R + 1;            // [R] cached tokens
+    __shared__ int2 s_warp[32];
+    __shared__ int s_placed[32];
+    __shared__ int s_total_placed;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int per = (a.R + SLOT_THREADS - 1) / SLOT_THREADS, r0 = tid * per;
+    const uint32_t P = a.page;
+    const int64_t n_free = max64(0, min64(__ldg(a.free_count), a.free_capacity));
+
+    auto lengths = [&](int r, int& seq, int& fresh, int& pages) {
+        seq = max(0, a.seq_lens[r]);
+        fresh = max(0, a.new_lens[r]);
+        const int64_t had = ((int64_t)seq + P - 1) / P, want = ((int64_t)seq + fresh + P - 1) / P;
+        pages = (int)max64(0, min64(want, a.width) - had);
+    };
+    int2 sum = make_int2(0, 0);
+    for (int r = r0; r < min(a.R, r0 + per); ++r) {
+        int seq, fresh, pages;
+        lengths(r, seq, fresh, pages);
+        s_seq[r] = seq;
+        sum.x += fresh;
+        sum.y += pages;
+    }
+    int2 incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, incl.x, o), y = __shfl_up_sync(0xFFFFFFFFu, incl.y, o);
+        if (lane >= o) {
+            incl.x += x;
+            incl.y += y;
+        }
+    }
+    if (lane == 31) s_warp[wid] = incl;
+    __syncthreads();
+    int2 run = make_int2(incl.x - sum.x, incl.y - sum.y);
+    for (int w = 0; w < wid; ++w) {
+        run.x += s_warp[w].x;
+        run.y += s_warp[w].y;
+    }
+    for (int r = r0; r < min(a.R, r0 + per); ++r) {
+        int seq, fresh, pages;
+        lengths(r, seq, fresh, pages);
+        s_start[r] = run.x;
+        s_pages[r] = run.y;
+        run.x += fresh;
+        run.y += pages;
+        if (r == a.R - 1) {
+            s_start[a.R] = run.x;
+            s_pages[a.R] = run.y;
+        }
+    }
+    // every read of seq_lens and free_count is done before any CTA writes total_lens or free_left, which
+    // may be the same arrays
+    __syncthreads();
+    cluster_sync();
+
+    const int nthr = SLOT_THREADS * (int)cluster_size(), me = (int)cluster_rank() * SLOT_THREADS + tid;
+    const int tokens = s_start[a.R], fresh_pages = s_pages[a.R];
+    for (int r = me; r <= a.R; r += nthr) {
+        a.q_start[r] = s_start[r];
+        if (r < a.R) a.total_lens[r] = s_seq[r] + (s_start[r + 1] - s_start[r]);
+    }
+    for (int k = me; k < fresh_pages; k += nthr) {
+        const int r = last_not_above(s_pages, a.R, k);
+        const int64_t col = ((int64_t)s_seq[r] + P - 1) / P + (k - s_pages[r]);
+        if (col < a.width) a.table[r * a.stride + col] = k < n_free ? __ldg(a.free_pages + (n_free - 1 - k)) : -1;
+    }
+    int placed = 0;
+    for (int64_t t = me; t < a.max_tokens; t += nthr) {
+        int slot = -1, pos = -1;
+        if (t < tokens) {
+            const int r = last_not_above(s_start, a.R, (int)t);
+            pos = s_seq[r] + ((int)t - s_start[r]);
+            const int64_t col = (uint32_t)pos / P, had = ((int64_t)s_seq[r] + P - 1) / P;
+            int page = -1;
+            if (pos >= 0 && col < a.width) {
+                if (col < had) {
+                    page = a.table[r * a.stride + col];               // an older page: not written by this call
+                } else {
+                    const int64_t k = s_pages[r] + (col - had);
+                    if (k < n_free) page = __ldg(a.free_pages + (n_free - 1 - k));
+                }
+            }
+            const int64_t s = (int64_t)page * P + (uint32_t)pos % P;
+            if (page >= 0 && s <= INT32_MAX) slot = (int)s;
+            placed += slot >= 0;
+        }
+        a.slots[t] = slot;
+        a.positions[t] = pos;
+    }
+    placed = __reduce_add_sync(0xFFFFFFFFu, placed);
+    if (lane == 0) s_placed[wid] = placed;
+    __syncthreads();
+    if (wid == 0) {
+        placed = __reduce_add_sync(0xFFFFFFFFu, s_placed[lane]);
+        if (lane == 0) s_total_placed = placed;
+    }
+    cluster_sync();                                                     // every CTA's count is in its shared memory
+    if (me == 0) {
+        int all = 0;
+        const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&s_total_placed);
+        for (uint32_t c = 0; c < cluster_size(); ++c) {
+            uint32_t there;
+            int v;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(c));
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(there) : "memory");
+            all += v;
+        }
+        *a.unplaced = tokens - all;
+        *a.free_left = (int)max64(0, n_free - fresh_pages);
+    }
+    cluster_sync();                                                     // nobody leaves while CTA 0 reads its count
+}
+
+// ------------------------------------------------------------------------------------------------
+// Write and read of cached tokens: one thread per 16-element block, as the quantizers and dequantizers of
+// the framework, with the same arithmetic and S per head.  Both are bound by memory (2.5625 bytes a value).
+// ------------------------------------------------------------------------------------------------
+
+// The record of (slot, head), or null when the slot is outside the cache.
+template <typename T>
+__device__ __forceinline__ T* record_of(T* cache, int64_t slot, int h, const KvShape& c, int& token) {
+    if (slot < 0 || slot >= c.pages * c.page) return nullptr;
+    const uint32_t s = (uint32_t)slot, page = divu32(s, c.dv_page), off = s - page * (uint32_t)c.page;
+    token = (int)(off & (KV_GROUP - 1));
+    const int64_t rec = ((int64_t)page * c.heads + h) * (c.page / KV_GROUP) + off / KV_GROUP;
+    return cache + rec * kv_record_bytes(c.dim);
+}
+
+__global__ void __launch_bounds__(256)
+kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_token, int64_t k_head,
+                 int64_t v_token, int64_t v_head, const int32_t* __restrict__ slots, int64_t T,
+                 const float* __restrict__ s_k, const float* __restrict__ s_v, uint8_t* __restrict__ cache, KvShape c) {
+    const bool is_v = blockIdx.y != 0;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int nb = c.dim / 16, per = nb * c.heads;
+    const int64_t t = i / per;
+    if (t >= T) return;
+    const int e = (int)(i - t * per), h = e / nb, b = e - h * nb;
+    int token;
+    uint8_t* rec = record_of(cache, __ldg(slots + t), h, c, token);
+    if (!rec) return;
+    const uint4* src = reinterpret_cast<const uint4*>((is_v ? v + t * v_token + h * v_head : k + t * k_token + h * k_head) + b * 16);
+    const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+    const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m2 = absmax_bf16x2_int(m2, w[j]);     // integer maximum: a NaN is the largest
+    const float S = __ldg((is_v ? s_v : s_k) + h);
+    const uint32_t bs = nvfp4_block_scale_fast(__uint_as_float(fold_halves(m2) << 16), S, nvfp4_fast_rs(S));
+    const float r = nvfp4_block_recip(bs, S);
+    uint2 out;
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __fmul_rn(bf16_lo(w[j]), r);
+        f[2 * j + 1] = __fmul_rn(bf16_hi(w[j]), r);
+    }
+    out.x = cvt_e2m1x8(f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __fmul_rn(bf16_lo(w[4 + j]), r);
+        f[2 * j + 1] = __fmul_rn(bf16_hi(w[4 + j]), r);
+    }
+    out.y = cvt_e2m1x8(f);
+    if (r == 0.0f) {                                                  // zeros for infinities too (infinity * 0)
+        out.x &= 0x88888888u;
+        out.y &= 0x88888888u;
+    }
+    *reinterpret_cast<uint2*>(rec + (is_v ? kv_v_codes(c.dim) : 0) + token * (c.dim / 2) + b * 8) = out;
+    if (is_v) rec[kv_v_scales(c.dim) + b * 16 + kv_token_of_row(token)] = (uint8_t)bs;
+    else rec[kv_k_scales(c.dim) + token * nb + b] = (uint8_t)bs;
+}
+
+__global__ void __launch_bounds__(256)
+kv_gather_kernel(const uint8_t* __restrict__ cache, const int32_t* __restrict__ slots, int64_t T,
+                 const float* __restrict__ s_k, const float* __restrict__ s_v, uint16_t* __restrict__ k,
+                 uint16_t* __restrict__ v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, KvShape c) {
+    const bool is_v = blockIdx.y != 0;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int nb = c.dim / 16, per = nb * c.heads;
+    const int64_t t = i / per;
+    if (t >= T) return;
+    const int e = (int)(i - t * per), h = e / nb, b = e - h * nb;
+    uint32_t out[8] = {};
+    int token;
+    const uint8_t* rec = record_of(cache, __ldg(slots + t), h, c, token);
+    if (rec) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(rec + (is_v ? kv_v_codes(c.dim) : 0) + token * (c.dim / 2) + b * 8));
+        const uint32_t bs = __ldg(is_v ? rec + kv_v_scales(c.dim) + b * 16 + kv_token_of_row(token)
+                                       : rec + kv_k_scales(c.dim) + token * nb + b);
+        const float S = __ldg((is_v ? s_v : s_k) + h), f = e4m3_to_f32(bs);
+        const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t p = e2m1x2_to_f16x2((w[j >> 2] >> (8 * (j & 3))) & 0xFFu);
+            // the product with the block scale is exact, so the value is rounded by S and once to BF16
+            const float v0 = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(p & 0xFFFFu))), f);
+            const float v1 = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(p >> 16))), f);
+            out[j] = pack_bf16x2(__fmul_rn(v0, S), __fmul_rn(v1, S));
+        }
+    }
+    uint4* dst = reinterpret_cast<uint4*>((is_v ? v + t * v_token + h * v_head : k + t * k_token + h * k_head) + b * 16);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_slots(const int32_t* seq_lens, const int32_t* new_lens, int64_t R, int64_t page, int32_t* table,
+                            int64_t width, int64_t stride, const int32_t* free_pages, int64_t free_capacity,
+                            const int32_t* free_count, int32_t* q_start, int32_t* total_lens, int32_t* slots,
+                            int32_t* positions, int64_t max_tokens, int32_t* free_left, int32_t* unplaced,
+                            cudaStream_t stream) {
+    static PerDevice pd;
+    int unused = 0;
+    cudaError_t e = per_device_once(pd, unused, [](int&) {
+        return cudaFuncSetAttribute(kv_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (3 * (int)KV_MAX_REQUESTS + 2) * (int)sizeof(int));
+    });
+    if (e != cudaSuccess) return e;
+    const SlotArgs a{seq_lens, new_lens, (int)R, (uint32_t)page, table, width, stride, free_pages, free_capacity,
+                     free_count, q_start, total_lens, slots, positions, max_tokens, free_left, unplaced};
+    cudaLaunchConfig_t cfg{};
+    const unsigned ctas = max_tokens > 2 * SLOT_THREADS ? 8 : 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(SLOT_THREADS);
+    cfg.dynamicSmemBytes = (size_t)(3 * R + 2) * sizeof(int);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {ctas, 1, 1};
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_slots_kernel, a);
+}
+
+cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token,
+                             int64_t v_head, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
+                             uint8_t* cache, const KvShape& c, cudaStream_t stream) {
+    const int64_t blocks = (T * c.heads * (c.dim / 16) + 255) / 256;
+    kv_append_kernel<<<dim3((unsigned)blocks, 2), 256, 0, stream>>>(k, v, k_token, k_head, v_token, v_head, slots, T,
+                                                                    s_k, s_v, cache, c);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_gather(const uint8_t* cache, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
+                             uint16_t* k, uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                             const KvShape& c, cudaStream_t stream) {
+    const int64_t blocks = (T * c.heads * (c.dim / 16) + 255) / 256;
+    kv_gather_kernel<<<dim3((unsigned)blocks, 2), 256, 0, stream>>>(cache, slots, T, s_k, s_v, k, v, k_token, k_head,
+                                                                    v_token, v_head, c);
+    return cudaGetLastError();
+}
+
+}  // namespace mxk

@@ -153,6 +153,48 @@ uint32_t read_and_clear_mxfp8_status_on(cudaStream_t stream);
 cudaError_t launch_watchdog_selftest(unsigned long long limit_ns, cudaStream_t stream);
 cudaError_t launch_mxfp8_watchdog_selftest(unsigned long long limit_ns, cudaStream_t stream);
 
+// NVFP4 key/value cache (layout in mx_kv.cuh): pages x heads x page / 16 records; slots number its tokens.
+constexpr int64_t KV_MAX_REQUESTS = 4096;
+struct KvShape {
+    int64_t pages, page;
+    int heads, dim;
+    DivU32 dv_page;
+};
+cudaError_t launch_kv_slots(const int32_t* seq_lens, const int32_t* new_lens, int64_t R, int64_t page, int32_t* table,
+                            int64_t width, int64_t stride, const int32_t* free_pages, int64_t free_capacity,
+                            const int32_t* free_count, int32_t* q_start, int32_t* total_lens, int32_t* slots,
+                            int32_t* positions, int64_t max_tokens, int32_t* free_left, int32_t* unplaced,
+                            cudaStream_t stream);
+cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token,
+                             int64_t v_head, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
+                             uint8_t* cache, const KvShape& c, cudaStream_t stream);
+cudaError_t launch_kv_gather(const uint8_t* cache, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
+                             uint16_t* k, uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                             const KvShape& c, cudaStream_t stream);
+struct KvAttentionArgs {
+    const uint16_t* q; int64_t q_token, q_head;          // [T, kv_heads * group, dim] BF16, strides in elements
+    const int32_t *q_start, *seq_lens;
+    int R; int64_t T;
+    const int32_t* table; int64_t width, stride;
+    const uint8_t* cache; int64_t pages; int page, kv_heads, group, dim;
+    const float *s_k, *s_v;
+    float scale; int max_q, window;
+    uint16_t* out; int64_t o_token, o_head;
+    float* lse;                                          // [T, kv_heads * group] or null
+    void* workspace;
+};
+size_t kv_attention_workspace_bytes(int64_t dim);
+cudaError_t launch_kv_attention(const KvAttentionArgs& a, int num_sms, cudaStream_t stream);
+
+// Products of M tokens with NVFP4 weights [N, K].
+struct MatvecArgs {
+    const uint16_t* x; int64_t ldx;
+    const uint8_t *q, *s; const float* s2; bool s2_per_row;
+    int M; int64_t N, K;
+    void* y; int64_t ldy; bool y_fp32;
+};
+cudaError_t launch_matvec_nvfp4(const MatvecArgs& a, int num_sms, cudaStream_t stream);
+
 int device_sm_count();
 
 }  // namespace mxk

@@ -1,6 +1,8 @@
-// mxnum_api.cu -- the C ABI of libmxnum.so: argument validation and launches (see include/mxnum.h).
+// mxnum_api.cu -- the C ABI of libmxnum.so: argument validation and launches (see include/mxnum.h and include/mxnum_generate.h).
 #include "../../include/mxnum.h"
+#include "../../include/mxnum_generate.h"
 #include "mx_internal.h"
+#include "mx_kv.cuh"
 
 #include <mutex>
 
@@ -31,6 +33,8 @@ int device_sm_count() {
 namespace {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 inline mx_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MX_OK : MX_ERR_CUDA; }
 
@@ -417,6 +421,143 @@ mx_status mx_count_mismatch(const uint8_t* x, const uint8_t* y, int64_t nbytes, 
     if (!aligned16(x) || !aligned16(y)) return MX_ERR_ALIGNMENT;
     if (nbytes == 0) return MX_OK;
     return from_cuda(mxk::launch_mismatch(x, y, nbytes, count, mxk::device_sm_count(), stream));
+}
+
+mx_status mx_kv_slots(const int32_t* seq_lens, const int32_t* new_lens, int64_t requests, int64_t page_size,
+                      int32_t* block_table, int64_t table_width, int64_t table_stride, const int32_t* free_pages,
+                      int64_t free_capacity, const int32_t* free_count, int32_t* q_start, int32_t* total_lens,
+                      int32_t* slots, int32_t* positions, int64_t max_tokens, int32_t* free_left, int32_t* unplaced,
+                      cudaStream_t stream) {
+    static_assert(MX_KV_MAX_REQUESTS == mxk::KV_MAX_REQUESTS, "request limit");
+    if (!seq_lens || !new_lens || !block_table || !free_pages || !free_count || !q_start || !total_lens || !slots ||
+        !positions || !free_left || !unplaced)
+        return MX_ERR_INVALID_ARG;
+    if (requests <= 0 || table_width <= 0 || table_stride < table_width || free_capacity < 0 || max_tokens <= 0 ||
+        page_size <= 0)
+        return MX_ERR_INVALID_ARG;
+    if (!aligned4(seq_lens) || !aligned4(new_lens) || !aligned4(block_table) || !aligned4(free_pages) ||
+        !aligned4(free_count) || !aligned4(q_start) || !aligned4(total_lens) || !aligned4(slots) ||
+        !aligned4(positions) || !aligned4(free_left) || !aligned4(unplaced))
+        return MX_ERR_ALIGNMENT;
+    if (requests > MX_KV_MAX_REQUESTS || (page_size % 16) != 0 || page_size > (1 << 20) || max_tokens > INT32_MAX ||
+        table_width > INT32_MAX / requests)
+        return MX_ERR_UNSUPPORTED;
+    return from_cuda(mxk::launch_kv_slots(seq_lens, new_lens, requests, page_size, block_table, table_width, table_stride,
+                                          free_pages, free_capacity, free_count, q_start, total_lens, slots, positions,
+                                          max_tokens, free_left, unplaced, stream));
+}
+
+int64_t mx_kv_page_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim) {
+    if (page_size <= 0 || (page_size % 16) != 0 || kv_heads <= 0) return 0;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    return page_size / mxk::KV_GROUP * kv_heads * mxk::kv_record_bytes((int)head_dim);
+}
+
+static mx_status check_kv_cache(const void* cache, int64_t pages, int64_t page_size, int64_t heads, int64_t dim,
+                                const float* s_k, const float* s_v) {
+    if (!cache || !s_k || !s_v || pages <= 0 || page_size <= 0 || heads <= 0 || dim <= 0) return MX_ERR_INVALID_ARG;
+    if (!aligned16(cache) || !aligned4(s_k) || !aligned4(s_v)) return MX_ERR_ALIGNMENT;
+    if ((page_size % 16) != 0 || page_size > (1 << 20) || pages > INT32_MAX / page_size || heads > 65535 ||
+        (dim != 64 && dim != 128 && dim != 256))
+        return MX_ERR_UNSUPPORTED;
+    return MX_OK;
+}
+
+// A [tokens, heads, dim] BF16 tensor with unit element stride whose rows start on 16 bytes.
+static mx_status check_heads_tensor(const void* x, int64_t token_stride, int64_t head_stride, int64_t dim) {
+    if (!x || head_stride < dim || token_stride < dim) return MX_ERR_INVALID_ARG;
+    if (!aligned16(x) || (token_stride % 8) != 0 || (head_stride % 8) != 0) return MX_ERR_ALIGNMENT;
+    return MX_OK;
+}
+
+static mxk::KvShape kv_shape(int64_t pages, int64_t page_size, int64_t heads, int64_t dim) {
+    return mxk::KvShape{pages, page_size, (int)heads, (int)dim, mxk::make_divu32((uint64_t)page_size)};
+}
+
+mx_status mx_nvfp4_kv_append(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                             int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots, int64_t T,
+                             const float* s_k, const float* s_v, uint8_t* cache, int64_t pages, int64_t page_size,
+                             int64_t kv_heads, int64_t head_dim, cudaStream_t stream) {
+    mx_status st = check_kv_cache(cache, pages, page_size, kv_heads, head_dim, s_k, s_v);
+    if (st == MX_OK && (!slots || T <= 0)) st = MX_ERR_INVALID_ARG;
+    if (st == MX_OK) st = check_heads_tensor(k, k_token_stride, k_head_stride, head_dim);
+    if (st == MX_OK) st = check_heads_tensor(v, v_token_stride, v_head_stride, head_dim);
+    if (st == MX_OK && !aligned4(slots)) st = MX_ERR_ALIGNMENT;
+    if (st == MX_OK && T > INT32_MAX / (kv_heads * (head_dim / 16))) st = MX_ERR_UNSUPPORTED;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_kv_append(static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_token_stride,
+                                           k_head_stride, v_token_stride, v_head_stride, slots, T, s_k, s_v, cache,
+                                           kv_shape(pages, page_size, kv_heads, head_dim), stream));
+}
+
+mx_status mx_nvfp4_kv_gather(const uint8_t* cache, int64_t pages, int64_t page_size, int64_t kv_heads, int64_t head_dim,
+                             const int32_t* slots, int64_t T, const float* s_k, const float* s_v, void* k,
+                             int64_t k_token_stride, int64_t k_head_stride, void* v, int64_t v_token_stride,
+                             int64_t v_head_stride, cudaStream_t stream) {
+    mx_status st = check_kv_cache(cache, pages, page_size, kv_heads, head_dim, s_k, s_v);
+    if (st == MX_OK && (!slots || T <= 0)) st = MX_ERR_INVALID_ARG;
+    if (st == MX_OK) st = check_heads_tensor(k, k_token_stride, k_head_stride, head_dim);
+    if (st == MX_OK) st = check_heads_tensor(v, v_token_stride, v_head_stride, head_dim);
+    if (st == MX_OK && !aligned4(slots)) st = MX_ERR_ALIGNMENT;
+    if (st == MX_OK && T > INT32_MAX / (kv_heads * (head_dim / 16))) st = MX_ERR_UNSUPPORTED;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_kv_gather(cache, slots, T, s_k, s_v, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v),
+                                           k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+                                           kv_shape(pages, page_size, kv_heads, head_dim), stream));
+}
+
+size_t mx_kv_attention_workspace_bytes(int64_t head_dim) {
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    return mxk::kv_attention_workspace_bytes(head_dim);
+}
+
+mx_status mx_nvfp4_kv_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t T, int64_t heads,
+                                const int32_t* q_start, const int32_t* seq_lens, int64_t requests, int64_t max_q,
+                                const int32_t* block_table, int64_t table_width, int64_t table_stride,
+                                const uint8_t* cache, int64_t pages, int64_t page_size, int64_t kv_heads,
+                                int64_t head_dim, const float* s_k, const float* s_v, float scale, int64_t window,
+                                void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    mx_status st = check_kv_cache(cache, pages, page_size, kv_heads, head_dim, s_k, s_v);
+    if (st == MX_OK && (!q_start || !seq_lens || !block_table || !workspace || T <= 0 || heads <= 0 || requests <= 0 ||
+                        max_q <= 0 || window < 0 || table_width <= 0 || table_stride < table_width ||
+                        heads % kv_heads != 0 || !(scale == scale) ||
+                        workspace_bytes < mx_kv_attention_workspace_bytes(head_dim)))
+        st = MX_ERR_INVALID_ARG;
+    if (st == MX_OK) st = check_heads_tensor(q, q_token_stride, q_head_stride, head_dim);
+    if (st == MX_OK) st = check_heads_tensor(out, out_token_stride, out_head_stride, head_dim);
+    if (st == MX_OK && (!aligned4(q_start) || !aligned4(seq_lens) || !aligned4(block_table) || !aligned4(lse) ||
+                        !aligned16(workspace)))
+        st = MX_ERR_ALIGNMENT;
+    if (st == MX_OK && (requests > MX_KV_MAX_REQUESTS || T > INT32_MAX || heads > 65535 || max_q > INT32_MAX / heads ||
+                        table_width > INT32_MAX / page_size || window > INT32_MAX))
+        st = MX_ERR_UNSUPPORTED;
+    if (st != MX_OK) return st;
+    mxk::KvAttentionArgs a{};
+    a.q = static_cast<const uint16_t*>(q); a.q_token = q_token_stride; a.q_head = q_head_stride;
+    a.q_start = q_start; a.seq_lens = seq_lens; a.R = (int)requests; a.T = T;
+    a.table = block_table; a.width = table_width; a.stride = table_stride;
+    a.cache = cache; a.pages = pages; a.page = (int)page_size;
+    a.kv_heads = (int)kv_heads; a.group = (int)(heads / kv_heads); a.dim = (int)head_dim;
+    a.s_k = s_k; a.s_v = s_v; a.scale = scale; a.max_q = (int)max_q; a.window = (int)window;
+    a.out = static_cast<uint16_t*>(out); a.o_token = out_token_stride; a.o_head = out_head_stride;
+    a.lse = lse; a.workspace = workspace;
+    return from_cuda(mxk::launch_kv_attention(a, mxk::device_sm_count(), stream));
+}
+
+mx_status mx_nvfp4_matvec(const void* x, int64_t ldx, const uint8_t* q, const uint8_t* s, const float* s2,
+                          mx_scope s2_scope, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, int y_fp32,
+                          cudaStream_t stream) {
+    if (!x || !q || !s || !s2 || !y || M <= 0 || N <= 0 || K <= 0 || ldx < K || ldy < N) return MX_ERR_INVALID_ARG;
+    if ((s2_scope != MX_SCOPE_TENSOR && s2_scope != MX_SCOPE_ROW) || (y_fp32 != 0 && y_fp32 != 1)) return MX_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(q) || !aligned16(s) || !aligned4(s2) || !aligned16(y) || (ldx % 8) != 0)
+        return MX_ERR_ALIGNMENT;
+    if (M > MX_MATVEC_MAX_TOKENS || (K % 16) != 0 || K > (int64_t(1) << 24) || N >= (int64_t(1) << 31)) return MX_ERR_UNSUPPORTED;
+    mxk::MatvecArgs a{};
+    a.x = static_cast<const uint16_t*>(x); a.ldx = ldx;
+    a.q = q; a.s = s; a.s2 = s2; a.s2_per_row = s2_scope == MX_SCOPE_ROW;
+    a.M = (int)M; a.N = N; a.K = K; a.y = y; a.ldy = ldy; a.y_fp32 = y_fp32 != 0;
+    return from_cuda(mxk::launch_matvec_nvfp4(a, mxk::device_sm_count(), stream));
 }
 
 mx_status mx_check_device_status(void) {
