@@ -1,9 +1,25 @@
 // kv_attention.cu -- attention of a generation step over the NVFP4 key/value cache.
 //
-//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale * q_i . k_j - m_i),  k_j = val(code) * val(block scale) * S_k
-//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = 2^(c q_i . k_j - m_i),  c = scale * log2(e),
+//   k_j = val(code) * val(block scale) * S_k, v_j alike with S_v,
 // over the cached positions j in (pos_i - window, pos_i], pos_i = L - N + i for new token i of a request with L
 // cached tokens of which N are new.
+//
+// Bound: the cache is read once, 1.125 D bytes a token and kv head, and with G q heads to a kv head every byte meets
+// G query rows: 4 G D / (1.125 D) = 3.6 G operations a byte, far below the tensor cores' balance.  The work is
+// turning 4-bit codes into matrix operands fast enough: a record of 16 tokens (2304 bytes for D = 128) may cost
+// one quarter of an SM at most 396 clocks at the measured copy rate.
+//
+// Tokens are the rows (M) of both products and query rows the columns (N = 8), so eight query rows fill a fragment:
+//   scores  S^T[16 tokens, 8 NQ rows] = K[16, D] Q^T:  K's codes become the A fragment of mma.m16n8k16 in registers.  A
+//           thread of the quad owns D / 4 contiguous elements of a token, a run of bytes; the contraction index may
+//           be permuted freely as long as Q's fragment follows.  Block scales multiply the FP16 pairs exactly (2 + 4
+//           significant bits), so the only roundings of a score are FP32 sums.
+//   output  O^T[D, 8 NQ] += V^T[D, 16] P:  A is V with two neighbouring tokens in a register.  The nibbles of two tokens
+//           are interleaved as packed codes (4 logic instructions for 32 codes), after which one conversion gives
+//           the pair (token, next token) of a dimension.  P^T comes out of S^T's accumulators by one 8x8 transpose.
+// Q enters as FP16, scaled by a power of two per row so that its largest element lies in [2^15, 2^16): every BF16 value
+// down to 2^-29 of it stays exact.  P enters as FP16: 2^-12 relative rounding, against 2^-9 of the BF16 output.
 #include "mx_internal.h"
 #include "mx_kv.cuh"
 
@@ -11,91 +27,662 @@ namespace mxk {
 
 namespace {
 
-// One CTA for each (new token, q head): its four warps take every fourth cached token, a lane D / 32 elements
-// of it, with a running maximum and sum each, and join at the end.
-template <int D>
-__global__ void __launch_bounds__(128) kv_attention_simple_kernel(const KvAttentionArgs a) {
-    constexpr int E = D / 32;
-    const int t = blockIdx.x, hq = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int lo = 0, hi = a.R;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.q_start + mid) <= t) lo = mid; else hi = mid;
-    }
-    const int r = lo, first = __ldg(a.q_start + r), count = __ldg(a.q_start + r + 1) - first, len = __ldg(a.seq_lens + r);
-    const int pos = len - count + (t - first);
-    const int begin = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    const int h = hq / a.group;
-    const float S_k = __ldg(a.s_k + h), S_v = __ldg(a.s_v + h);
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.0f;
+constexpr int ATT_WARPS = 4;
+constexpr int ATT_THREADS = 32 * ATT_WARPS;
+constexpr int ATT_TILE = 32;                 // tokens of a warp's step: two records
+constexpr int ATT_MIN_TILES = 4;             // smallest share of a CTA: one step a warp
+constexpr float ATT_SLACK = 8.0f;            // the running maximum may lag by 2^8 (P stays below 2^8 in FP16)
+
+__host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 6 : (D == 128 ? 3 : 2); }
+// Resident CTAs per SM: by registers (O holds D / 4 * NQ of them) and by shared memory.
+__host__ __device__ constexpr int att_ctas(int D, int NQ) { return D == 256 ? (NQ == 1 ? 3 : 2) : (NQ == 1 ? 4 : (NQ == 2 ? 3 : 2)); }
+__host__ __device__ constexpr int att_ring_bytes(int D) { return ATT_WARPS * att_stages(D) * 2 * kv_record_bytes(D); }
+constexpr int ATT_MAX_CTAS_PER_SM = 4;
+
+// Workspace: partial results of the work items that several CTAs share.  Each CTA has two places: 0 for an item
+// that began in an earlier CTA, 1 for one that goes on in the next.
+struct Piece {
+    int first_cta, count;                    // CTAs first_cta (place 1), first_cta + 1 .. (place 0); count 0: not shared
+    int token0, kv_head, col0, cols;         // where its query rows go
+};
+
+struct AttParams {
+    KvAttentionArgs a;
+    DivU32 dv_group, dv_page_groups;         // q heads per kv head; records per page
+    int page_groups;
+    float* part_ml;                          // [CTAs][2][8 NQ][2]
+    float* part_o;                           // [CTAs][2][8 NQ][D]
+    Piece* pieces;
+    int n_pieces;                            // entries of pieces
+    bool by_item;                            // they are numbered by item (else by CTA)
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Four code bytes -> four FP16 pairs (low nibble in the low half).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&f)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(w));
+}
+// The two E4M3 bytes in the low half of w as an FP16 pair (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void copy_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// Words of a thread's run of codes in shared memory.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x; w[1] = v.y;
+    } else {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const uint32_t b = __ldg(a.q + t * a.q_token + hq * a.q_head + lane * E + e);
-        q[e] = __uint_as_float(b << 16) * S_k;
-    }
-    const int nb = D / 16, blk = lane * E / 16;
-    for (int j = begin + warp; j <= pos; j += 4) {
-        const int64_t col = j / a.page;
-        const int page = col < a.width ? __ldg(a.table + r * a.stride + col) : -1;
-        if (page < 0 || page >= a.pages) continue;
-        const int off = j % a.page, tok = off & 15;
-        const uint8_t* rec = a.cache + (((int64_t)page * a.kv_heads + h) * (a.page / KV_GROUP) + off / KV_GROUP) * kv_record_bytes(D);
-        const float ks = e4m3_to_f32(rec[kv_k_scales(D) + tok * nb + blk]);
-        const float vs = e4m3_to_f32(rec[kv_v_scales(D) + blk * 16 + kv_token_of_row(tok)]);
-        float dot = 0.0f, v[E];
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const int at = tok * (D / 2) + (lane * E + e) / 2;
-            const uint32_t kw = e2m1x2_to_f16x2(rec[at]), vw = e2m1x2_to_f16x2(rec[kv_v_codes(D) + at]);
-            const __half2 kp = *reinterpret_cast<const __half2*>(&kw), vp = *reinterpret_cast<const __half2*>(&vw);
-            dot = fmaf(q[e], __low2float(kp) * ks, dot);
-            dot = fmaf(q[e + 1], __high2float(kp) * ks, dot);
-            v[e] = __low2float(vp) * vs;
-            v[e + 1] = __high2float(vp) * vs;
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
         }
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, s);
-        dot *= a.scale;
-        const float mn = fmaxf(m, dot), c = expf(m - mn), p = expf(dot - mn);
-        l = fmaf(l, c, p);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(o[e], c, p * v[e]);
-        m = mn;
     }
-    __shared__ float s_m[4], s_l[4], s_o[4][D];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+}
+
+// What request r asks for: tiles of its context, items (kv head x column tile) and the first tile's position.
+struct Request {
+    int first, count, len, tile0, tiles, col_tiles;
+};
+template <int NQ>
+__device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r) {
+    Request q;
+    q.first = __ldg(a.q_start + r);
+    // (offsets outside [0, T] are invalid input; the clamps keep every access inside q and out all the same)
+    q.count = q.first < 0 ? 0 : (int)min64(min64(__ldg(a.q_start + r + 1), a.T) - q.first, a.max_q);
+    q.count = max(0, q.count);
+    q.len = max(0, __ldg(a.seq_lens + r));
+    const int64_t lo = a.window > 0 ? max64(0, (int64_t)q.len - q.count + 1 - a.window) : 0;
+    q.tile0 = (int)(lo / ATT_TILE);
+    q.tiles = max(1, (int)(((uint32_t)q.len + ATT_TILE - 1) / ATT_TILE) - q.tile0);
+    q.col_tiles = (q.count * a.group + 8 * NQ - 1) / (8 * NQ);
+    return q;
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_kernel(const __grid_constant__ AttParams p) {
+    constexpr int STAGES = att_stages(D), REC = kv_record_bytes(D), STAGE_BYTES = 2 * REC;
+    constexpr int KS = D / 16;               // k-steps of the scores
+    constexpr int MT = D / 16;               // 16-row tiles of the output
+    constexpr int KW = D / 32, VW = D / 64;  // words of a thread's run of K and V codes
+    constexpr int CHUNKS = REC / 16;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t s_warp_sum[ATT_WARPS];
+    __shared__ int s_warp_items[ATT_WARPS];
+    __shared__ int64_t s_off;
+    __shared__ int s_r, s_item;
+    __shared__ float s_m[ATT_WARPS][8 * NQ], s_l[ATT_WARPS][8 * NQ];
+
+    const KvAttentionArgs& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+
+    // ---- the CTA's share of all tiles: equal runs over (request, kv head, column tile, context tile)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int per = (a.R + ATT_THREADS - 1) / ATT_THREADS, r0 = tid * per;
+    int64_t mine = 0;
+    int my_items = 0;
+    for (int r = r0; r < min(a.R, r0 + per); ++r) {
+        const Request q = request_of<NQ>(a, r);
+        mine += (int64_t)q.tiles * q.col_tiles * a.kv_heads;
+        my_items += q.col_tiles * a.kv_heads;
     }
+    int64_t incl = mine;
+    int incl_items = my_items;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        const int y = __shfl_up_sync(0xFFFFFFFFu, incl_items, o);
+        if (lane >= o) {
+            incl += x;
+            incl_items += y;
+        }
+    }
+    if (lane == 31) {
+        s_warp_sum[warp] = incl;
+        s_warp_items[warp] = incl_items;
+    }
     __syncthreads();
-    float top = -INFINITY, sum = 0.0f;
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[w]);
-    float c[4];
-    for (int w = 0; w < 4; ++w) {
-        c[w] = s_l[w] > 0.0f ? expf(s_m[w] - top) : (s_l[w] == 0.0f ? 0.0f : s_l[w]);
-        sum += c[w] * s_l[w];
+    int64_t total = 0, excl = incl - mine;
+    int excl_items = incl_items - my_items, items = 0;
+    for (int w = 0; w < ATT_WARPS; ++w) {
+        items += s_warp_items[w];
+        if (w < warp) {
+            excl += s_warp_sum[w];
+            excl_items += s_warp_items[w];
+        }
+        total += s_warp_sum[w];
     }
-    for (int d = threadIdx.x; d < D; d += 128) {
-        float x = 0.0f;
-        for (int w = 0; w < 4; ++w) x += c[w] * s_o[w][d];
-        x = sum == 0.0f ? 0.0f : x * S_v / sum;
-        a.out[t * a.o_token + hq * a.o_head + d] = (uint16_t)pack_bf16x2(x, 0.0f);
+    const int64_t share = max64(ATT_MIN_TILES, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t begin = min64(total, blockIdx.x * share), end = min64(total, begin + share);
+    if (mine > 0 && begin >= excl && begin < excl + mine && begin < end) {
+        int64_t at = excl;
+        int r = r0, it = excl_items;
+        for (;; ++r) {
+            const Request q = request_of<NQ>(a, r);
+            const int64_t w = (int64_t)q.tiles * q.col_tiles * a.kv_heads;
+            if (begin < at + w) break;
+            at += w;
+            it += q.col_tiles * a.kv_heads;
+        }
+        s_r = r;
+        s_off = begin - at;
+        s_item = it;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)t * gridDim.y + hq] = sum == 0.0f ? -INFINITY : top + logf(sum);
+    // every entry is written in every call: by the item's first CTA, or here
+    if (!p.by_item) {
+        if (tid == 0) p.pieces[blockIdx.x].count = 0;
+    } else {
+        for (int i = items + blockIdx.x * ATT_THREADS + tid; i < p.n_pieces; i += gridDim.x * ATT_THREADS) p.pieces[i].count = 0;
+    }
+    __syncthreads();
+    if (begin >= end) return;
+
+    int r = s_r, item0 = s_item;             // request; number of its first item
+    int64_t off = s_off;                     // tile inside the request
+    Request rq = request_of<NQ>(a, r);
+    uint8_t* ring = smem + warp * (STAGES * STAGE_BYTES);
+    const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
+
+    for (int64_t at = begin; at < end;) {
+        while (off >= (int64_t)rq.tiles * rq.col_tiles * a.kv_heads) {     // next request with work
+            off -= (int64_t)rq.tiles * rq.col_tiles * a.kv_heads;
+            item0 += rq.col_tiles * a.kv_heads;
+            rq = request_of<NQ>(a, ++r);
+        }
+        const int item = (int)(off / rq.tiles), first_tile = (int)(off - (int64_t)item * rq.tiles);
+        const int n_tiles = (int)min64(rq.tiles - first_tile, end - at);
+        const int h = item / rq.col_tiles, col0 = (item - h * rq.col_tiles) * 8 * NQ;
+        const int cols = rq.count * a.group;                               // query rows of this kv head
+        const int base_pos = rq.len - rq.count;                            // position of new token 0
+
+        // ---- Q^T fragments: column g of each eight, elements [t4 * D / 4, + D / 4), as FP16 scaled by a power of two
+        uint32_t qf[NQ][KS][2];
+        float mul[NQ][2];                                                  // score -> exponent of two, columns 2 t4, 2 t4 + 1
+        int pos[NQ][2];                                                    // last position they attend to (-1: none)
+        const float S_k = __ldg(a.s_k + h);
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            const int col = col0 + nq * 8 + g;
+            const bool real = col < cols;
+            const int i = real ? (int)divu32((uint32_t)col, p.dv_group) : 0;
+            const int hq = real ? h * a.group + (col - i * a.group) : 0;
+            const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(rq.first + i) * a.q_token + (int64_t)hq * a.q_head + t4 * (D / 4));
+            uint32_t w[D / 8];
+            uint32_t amax = 0;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (real) v = __ldg(src + k);
+                w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+            }
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+                const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+                amax = max(amax, lo < 0x7F80u ? lo : 0u);                  // infinities and NaN go through as they are
+                amax = max(amax, hi < 0x7F80u ? hi : 0u);
+            }
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            // x * 2^(142 - e) with e the biased exponent of the largest element (27 at least: the factor stays finite)
+            const int e = max((int)(amax >> 7), 27);
+            const float up = __uint_as_float((uint32_t)(127 + 142 - e) << 23);
+            const float c = a.scale * 1.4426950408889634f * S_k * __uint_as_float((uint32_t)max(e - 15, 1) << 23);
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) qf[nq][k >> 1][k & 1] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                mul[nq][j] = __shfl_sync(0xFFFFFFFFu, c, 4 * (2 * t4 + j));
+                const int cj = col0 + nq * 8 + 2 * t4 + j;
+                pos[nq][j] = cj < cols ? base_pos + (int)divu32((uint32_t)cj, p.dv_group) : -1;
+            }
+        }
+        // positions that every column of the tile attends to
+        const int last_col = min(cols, col0 + 8 * NQ) - 1;
+        const int64_t all_hi = base_pos + (int64_t)divu32((uint32_t)col0, p.dv_group) + 1;
+        const int64_t all_lo = a.window > 0 ? base_pos + (int64_t)divu32((uint32_t)last_col, p.dv_group) + 1 - a.window : 0;
+
+        float o[NQ][MT][4] = {};
+        float m[NQ][2], l[NQ][2];
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m[nq][j] = -INFINITY;
+                l[nq][j] = 0.0f;
+            }
+
+        // ---- the warp's tiles: first_tile + warp, + 4, ...; lane i looks up record i & 1 of step 16 b + i / 2
+        const int steps = n_tiles > warp ? (n_tiles - warp + ATT_WARPS - 1) / ATT_WARPS : 0;
+        auto look_up = [&](int b) -> int64_t {
+            const int k = 16 * b + (lane >> 1);
+            if (k >= steps) return -1;
+            const int64_t grp = 2 * (int64_t)(rq.tile0 + first_tile + warp + ATT_WARPS * k) + (lane & 1);
+            if (grp * KV_GROUP >= rq.len) return -1;
+            const uint32_t col = divu32((uint32_t)grp, p.dv_page_groups);
+            if (col >= a.width) return -1;
+            const int page = __ldg(a.table + r * a.stride + col);
+            if (page < 0 || page >= a.pages) return -1;
+            return (((int64_t)page * a.kv_heads + h) * p.page_groups + ((uint32_t)grp - col * (uint32_t)p.page_groups)) * REC;
+        };
+        int64_t now = look_up(0), next = look_up(1);
+        uint32_t there = 0;                                                // two bits a stage: its records hold data
+        auto issue = [&](int k) {
+            if (k < steps) {
+                const int s = k % STAGES;
+                if ((k & 15) == 0 && k > 0) {
+                    now = next;
+                    next = look_up((k >> 4) + 1);
+                }
+                const int64_t a0 = __shfl_sync(0xFFFFFFFFu, now, 2 * (k & 15)), a1 = __shfl_sync(0xFFFFFFFFu, now, 2 * (k & 15) + 1);
+                there = (there & ~(3u << (2 * s))) | ((a0 >= 0 ? 1u : 0u) << (2 * s)) | ((a1 >= 0 ? 2u : 0u) << (2 * s));
+                const uint32_t dst = ring_u32 + s * STAGE_BYTES;
+#pragma unroll
+                for (int i = 0; i < (2 * CHUNKS + 31) / 32; ++i) {
+                    const int c = lane + 32 * i;
+                    const int64_t from = c < CHUNKS ? a0 : a1;
+                    if (c < 2 * CHUNKS && from >= 0) copy_async_16(dst + 16 * c, a.cache + from + 16 * (c < CHUNKS ? c : c - CHUNKS));
+                }
+            }
+            copy_async_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < STAGES - 1; ++k) issue(k);
+
+        for (int k = 0; k < steps; ++k) {
+            copy_async_wait<STAGES - 2>();
+            __syncwarp();
+            issue(k + STAGES - 1);
+            const uint8_t* st = ring + (k % STAGES) * STAGE_BYTES;
+            const uint32_t have = (there >> (2 * (k % STAGES))) & 3u;
+            const int64_t tok0 = (int64_t)(rq.tile0 + first_tile + warp + ATT_WARPS * k) * ATT_TILE;
+            const bool full = have == 3u && tok0 + ATT_TILE <= all_hi && tok0 >= all_lo;
+
+            // scores
+            float s[2][NQ][4] = {};
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) {
+                const uint8_t* rec = st + gr * REC;
+                uint32_t kw[2][KW], ksc[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int tok = kv_token_of_row(g) + 8 * x;
+                    load_words<KW>(rec + tok * (D / 2) + t4 * (D / 8), kw[x]);
+                    const uint8_t* sc = rec + kv_k_scales(D) + tok * (D / 16) + t4 * (D / 64);
+                    if constexpr (D == 64) ksc[x] = *sc;
+                    else if constexpr (D == 128) ksc[x] = *reinterpret_cast<const uint16_t*>(sc);
+                    else ksc[x] = *reinterpret_cast<const uint32_t*>(sc);
+                }
+#pragma unroll
+                for (int w = 0; w < KW; ++w) {
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        e2m1x8_to_f16(kw[x][w], f[x]);
+                        const uint32_t sc = e4m3x2_to_f16x2(__byte_perm(ksc[x], 0u, 0x1111u * (w >> 1)));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) f[x][i] = mul_f16x2(f[x][i], sc);
+                    }
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq) {
+                        mma_16816(s[gr][nq], f[0][0], f[1][0], f[0][1], f[1][1], qf[nq][2 * w][0], qf[nq][2 * w][1]);
+                        mma_16816(s[gr][nq], f[0][2], f[1][2], f[0][3], f[1][3], qf[nq][2 * w + 1][0], qf[nq][2 * w + 1][1]);
+                    }
+                }
+            }
+
+            // softmax: fragment row g of half x of record gr is token gr * 16 + 8 x + token_of_row(g)
+            float top[NQ][2];
+            bool raise = false;
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+                top[nq][0] = top[nq][1] = -INFINITY;
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float v = s[gr][nq][2 * x + j] * mul[nq][j];
+                            if (!full) {
+                                const int64_t tok = tok0 + gr * 16 + 8 * x + kv_token_of_row(g);
+                                const bool in = ((have >> gr) & 1u) && tok <= pos[nq][j] && (a.window == 0 || tok > (int64_t)pos[nq][j] - a.window);
+                                v = in ? v : -INFINITY;
+                            }
+                            s[gr][nq][2 * x + j] = v;
+                            top[nq][j] = fmaxf(top[nq][j], v);
+                        }
+                raise |= top[nq][0] > m[nq][0] + ATT_SLACK || top[nq][1] > m[nq][1] + ATT_SLACK;
+            }
+            if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+                for (int nq = 0; nq < NQ; ++nq) {
+                    float f[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float v = fmaxf(top[nq][j], m[nq][j]);
+                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+                        f[j] = v == -INFINITY ? 1.0f : ex2(m[nq][j] - v);
+                        m[nq][j] = v;
+                        l[nq][j] *= f[j];
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[nq][mt][e] *= f[e & 1];
+                }
+            }
+            uint32_t pf[2][NQ][2];                                         // P as B fragments
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) {
+                const float m0 = m[nq][0] == -INFINITY ? 0.0f : m[nq][0], m1 = m[nq][1] == -INFINITY ? 0.0f : m[nq][1];
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float p0 = ex2(s[gr][nq][2 * x] - m0), p1 = ex2(s[gr][nq][2 * x + 1] - m1);
+                        l[nq][0] += p0;
+                        l[nq][1] += p1;
+                        pf[gr][nq][x] = transpose_8x8(pack_f16x2(p0, p1));
+                    }
+            }
+
+            // output: dimensions [g * D / 8, + D / 8) of each pair of tokens; byte i of the interleaved words is a dimension
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr) {
+                const uint8_t* rec = st + gr * REC;
+                uint32_t vw[2][2][VW], vsc[2][(D + 127) / 128];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        load_words<VW>(rec + kv_v_codes(D) + (8 * x + kv_token_of_row(2 * t4 + y)) * (D / 2) + g * (D / 16), vw[x][y]);
+#pragma unroll
+                    for (int b = 0; b < (D + 127) / 128; ++b) {
+                        const int blk = D == 64 ? g >> 1 : (D == 128 ? g : 2 * g + b);
+                        uint32_t sc = *reinterpret_cast<const uint16_t*>(rec + kv_v_scales(D) + blk * 16 + 8 * x + 2 * t4);
+                        if (!full) {                                       // bytes beyond the context may be anything
+                            const int64_t tok = tok0 + gr * 16 + 8 * x;
+                            const bool hv = (have >> gr) & 1u;
+                            if (!hv || tok + kv_token_of_row(2 * t4) >= rq.len) sc &= 0xFF00u;
+                            if (!hv || tok + kv_token_of_row(2 * t4 + 1) >= rq.len) sc &= 0x00FFu;
+                        }
+                        vsc[x][b] = e4m3x2_to_f16x2(sc);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    uint32_t f[2][2][4];                                   // [half][even / odd dimension][byte]
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t wa = vw[x][0][w], wb = vw[x][1][w];
+                        e2m1x8_to_f16((wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u), f[x][0]);
+                        e2m1x8_to_f16(((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u), f[x][1]);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) f[x][y][i] = mul_f16x2(f[x][y][i], vsc[x][w >> 1]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq)
+                            mma_16816(o[nq][4 * w + i], f[0][0][i], f[0][1][i], f[1][0][i], f[1][1][i], pf[gr][nq][0], pf[gr][nq][1]);
+                }
+            }
+        }
+        copy_async_wait<0>();
+
+        // ---- join the four warps
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float v = l[nq][j];
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+                v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+                if (g == 0) {
+                    s_m[warp][nq * 8 + 2 * t4 + j] = m[nq][j];
+                    s_l[warp][nq * 8 + 2 * t4 + j] = v;
+                }
+            }
+        const bool whole = first_tile == 0 && n_tiles == rq.tiles;
+        const int place = first_tile > 0 ? 0 : 1;
+        const int64_t part = ((int64_t)blockIdx.x * 2 + place) * (8 * NQ);
+        float* buf = reinterpret_cast<float*>(smem);                       // [warp][8][D + 4]
+        constexpr int LD = D + 4;
+        static_assert(ATT_WARPS * 8 * LD * 4 <= att_ring_bytes(D), "the join fits in the ring");
+        const float S_v = __ldg(a.s_v + h);
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            __syncthreads();                                               // ring (or buffer) no longer read; s_m, s_l written
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = nq * 8 + 2 * t4 + j;
+                float M = s_m[0][c];
+#pragma unroll
+                for (int w = 1; w < ATT_WARPS; ++w) M = fmaxf(M, s_m[w][c]);
+                const float f = m[nq][j] == -INFINITY ? 0.0f : ex2(m[nq][j] - M);
+                float* dst = buf + (warp * 8 + 2 * t4 + j) * LD + g * (D / 8);
+#pragma unroll
+                for (int mt = 0; mt < MT; mt += 2)
+                    *reinterpret_cast<float4*>(dst + 2 * mt) = make_float4(o[nq][mt][j] * f, o[nq][mt][2 + j] * f, o[nq][mt + 1][j] * f, o[nq][mt + 1][2 + j] * f);
+            }
+            __syncthreads();
+            for (int e = tid; e < 8 * (D / 4); e += ATT_THREADS) {
+                const int c = e / (D / 4), d = (e - c * (D / 4)) * 4, cc = nq * 8 + c, col = col0 + cc;
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float M = -INFINITY, L = 0.0f;
+#pragma unroll
+                for (int w = 0; w < ATT_WARPS; ++w) M = fmaxf(M, s_m[w][cc]);
+#pragma unroll
+                for (int w = 0; w < ATT_WARPS; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(buf + (w * 8 + c) * LD + d);
+                    x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
+                    L = __fmaf_rn(s_l[w][cc], s_m[w][cc] == -INFINITY ? 0.0f : ex2(s_m[w][cc] - M), L);
+                }
+                if (!whole) {
+                    *reinterpret_cast<float4*>(p.part_o + (part + cc) * D + d) = x;
+                    if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (part + cc) * 2) = make_float2(M, L);
+                } else if (col < cols) {
+                    const int i = (int)divu32((uint32_t)col, p.dv_group), hq = h * a.group + (col - i * a.group);
+                    const int64_t t = rq.first + i;
+                    const float f = L == 0.0f ? 0.0f : S_v / L;
+                    *reinterpret_cast<uint2*>(a.out + t * a.o_token + (int64_t)hq * a.o_head + d) =
+                        make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+                    if (a.lse && d == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
+                }
+            }
+        }
+        if (first_tile == 0 && tid == 0 && (p.by_item || !whole)) {
+            Piece pc{(int)blockIdx.x, 0, rq.first, h, col0, cols};
+            if (!whole) pc.count = (int)((at + rq.tiles - 1) / share) - (int)blockIdx.x + 1;
+            p.pieces[p.by_item ? item0 + item : (int)blockIdx.x] = pc;
+        }
+        __syncthreads();                                                   // buffer free for the next item's ring
+        at += n_tiles;
+        off += n_tiles;
+    }
+}
+
+// Join of the pieces of an item, in the order of the CTAs.  A CTA takes the columns y, y + gridDim.y, ... of piece x.
+// With one column a CTA (few items, many pieces) its warps share the pieces; else each warp takes columns.
+template <int D>
+__global__ void __launch_bounds__(256) kv_attention_join_kernel(const __grid_constant__ AttParams p, int columns) {
+    constexpr int V = D / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const Piece pc = p.pieces[blockIdx.x];
+    if (pc.count <= 0) return;
+    const KvAttentionArgs& a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool one = gridDim.y == (unsigned)columns;
+    __shared__ float s_o[8][D], s_ml[8][2];
+    for (int c = one ? (int)blockIdx.y : warp; c < columns; c += one ? columns : 8) {
+        const int col = pc.col0 + c;
+        if (col >= pc.cols) break;
+        float M = -INFINITY, L = 0.0f, o[V] = {};
+        const int w0 = one ? warp : 0, dw = one ? 8 : 1;
+        for (int k0 = w0; k0 < pc.count; k0 += 4 * dw) {
+            float x[4][V], ml[4][2];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int k = k0 + u * dw;
+                ml[u][0] = -INFINITY;
+                ml[u][1] = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[u][v] = 0.0f;
+                if (k < pc.count) {
+                    const int64_t at = ((int64_t)(pc.first_cta + k) * 2 + (k == 0 ? 1 : 0)) * columns + c;
+                    ml[u][0] = p.part_ml[at * 2];
+                    ml[u][1] = p.part_ml[at * 2 + 1];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) x[u][v] = p.part_o[at * D + v * 32 + lane];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float Mn = fmaxf(M, ml[u][0]);
+                const float f0 = M == -INFINITY ? 0.0f : ex2(M - Mn), f1 = ml[u][0] == -INFINITY ? 0.0f : ex2(ml[u][0] - Mn);
+                L = __fmaf_rn(L, f0, ml[u][1] * f1);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = __fmaf_rn(o[v], f0, x[u][v] * f1);
+                M = Mn;
+            }
+        }
+        if (one) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s_o[warp][v * 32 + lane] = o[v];
+            if (lane == 0) {
+                s_ml[warp][0] = M;
+                s_ml[warp][1] = L;
+            }
+            __syncthreads();
+            if (warp != 0) return;
+            M = -INFINITY;
+            for (int w = 0; w < 8; ++w) M = fmaxf(M, s_ml[w][0]);
+            L = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = 0.0f;
+            for (int w = 0; w < 8; ++w) {
+                const float f = s_ml[w][0] == -INFINITY ? 0.0f : ex2(s_ml[w][0] - M);
+                L = __fmaf_rn(s_ml[w][1], f, L);
+#pragma unroll
+                for (int v = 0; v < V; ++v) o[v] = __fmaf_rn(s_o[w][v * 32 + lane], f, o[v]);
+            }
+        }
+        const int i = (int)divu32((uint32_t)col, p.dv_group), hq = pc.kv_head * a.group + (col - i * a.group);
+        const int64_t t = pc.token0 + i;
+        const float f = L == 0.0f ? 0.0f : __ldg(a.s_v + pc.kv_head) / L;
+#pragma unroll
+        for (int v = 0; v < V; ++v) a.out[t * a.o_token + (int64_t)hq * a.o_head + v * 32 + lane] = (uint16_t)pack_bf16x2(o[v] * f, 0.0f);
+        if (a.lse && lane == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
+    }
+}
+
+constexpr int att_max_columns(int D) { return D == 256 ? 16 : 32; }
+
+template <int D, int NQ>
+cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
+    static PerDevice pd;
+    int unused = 0;
+    cudaError_t e = per_device_once(pd, unused, [](int&) {
+        return cudaFuncSetAttribute(kv_attention_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, att_ring_bytes(D));
+    });
+    if (e != cudaSuccess) return e;
+    const KvAttentionArgs& a = p.a;
+    const int ctas = num_sms * att_ctas(D, NQ);
+    const int64_t items = (int64_t)a.R * a.kv_heads * ((a.max_q * (int64_t)a.group + 8 * NQ - 1) / (8 * NQ));
+    p.by_item = items <= ctas;
+    p.n_pieces = (int)(p.by_item ? items : ctas);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    p.pieces = reinterpret_cast<Piece*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + (int64_t)num_sms * ATT_MAX_CTAS_PER_SM * sizeof(Piece));
+    p.part_o = p.part_ml + (int64_t)ctas * 2 * (8 * NQ) * 2;
+    kv_attention_kernel<D, NQ><<<ctas, ATT_THREADS, att_ring_bytes(D), stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // the join starts while the last CTAs finish and waits for them on the device
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.n_pieces, p.by_item && items * 8 <= ctas ? 8 * NQ : 1);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D>, p, 8 * NQ);
+}
+
+template <int D>
+cudaError_t launch_d(AttParams& p, int num_sms, cudaStream_t stream) {
+    const int64_t rows = (int64_t)p.a.max_q * p.a.group;
+    if (rows <= 8) return launch_nq<D, 1>(p, num_sms, stream);
+    if (D != 64 || rows <= 16) return launch_nq<D, 2>(p, num_sms, stream);
+    if constexpr (D == 64) return launch_nq<D, 4>(p, num_sms, stream);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t kv_attention_workspace_bytes(int64_t) { return 16; }
+size_t kv_attention_workspace_bytes(int64_t D) {
+    const int64_t ctas = (int64_t)device_sm_count() * ATT_MAX_CTAS_PER_SM;
+    return (size_t)(ctas * ((int64_t)sizeof(Piece) + 2 * att_max_columns((int)D) * (D + 2) * 4));
+}
 
-cudaError_t launch_kv_attention(const KvAttentionArgs& a, int, cudaStream_t stream) {
-    const dim3 grid((unsigned)a.T, (unsigned)(a.kv_heads * a.group));
-    if (a.dim == 64) kv_attention_simple_kernel<64><<<grid, 128, 0, stream>>>(a);
-    else if (a.dim == 128) kv_attention_simple_kernel<128><<<grid, 128, 0, stream>>>(a);
-    else kv_attention_simple_kernel<256><<<grid, 128, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_kv_attention(const KvAttentionArgs& a, int num_sms, cudaStream_t stream) {
+    AttParams p{};
+    p.a = a;
+    p.page_groups = a.page / KV_GROUP;
+    p.dv_group = make_divu32((uint64_t)a.group);
+    p.dv_page_groups = make_divu32((uint64_t)p.page_groups);
+    if (a.dim == 64) return launch_d<64>(p, num_sms, stream);
+    if (a.dim == 128) return launch_d<128>(p, num_sms, stream);
+    return launch_d<256>(p, num_sms, stream);
 }
 
 }  // namespace mxk
