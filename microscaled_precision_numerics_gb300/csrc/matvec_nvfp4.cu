@@ -8,15 +8,20 @@
 // leaves a quarter of an SM for the 2304 bytes of a warp's step.
 //
 // Weight rows are the rows (M) of mma.m16n8k16 and tokens its columns, eight to a fragment.  val(q) * val(bs) has at
-// most 6 significant bits and is exact in FP16.  x enters as FP16 scaled by a power of two per token (its largest
-// element of the stretch in [2^15, 2^16)): exact down to 2^-29 of that, an absolute error of 2^-40 of it below.
+// most 6 significant bits and is exact in FP16.  x enters as FP16 scaled by a power of two per token and step, its largest
+// element there in [2^15, 2^16): exact down to 2^-29 of that, an absolute error of 2^-40 of it below.  The product of
+// a step is scaled back as it joins the sum.
 //
 // A warp takes 32 rows, 8 consecutive ones in each of the four 32-row bands of a 128-row scale tile: the 16 bytes that the
 // GEMM scale layout holds for a row of the first band are the four bands' scales of the same four columns, so no
 // scale sector is fetched for a quarter of its bytes.  In a step of 128 values a thread reads 16 bytes of codes from
-// each of its four rows (a quad: 64 contiguous bytes) and one 16-byte piece of scales.
-// CTA: 128 rows, four warps across them and two along K.  The CTAs of a cluster split K further and add up through
-// distributed shared memory in rank order: no workspace, no second launch, and the sum does not depend on timing.
+// each of its four rows (a quad: 64 contiguous bytes) and one 16-byte piece of scales, through a cp.async
+// ring of its warp's: what keeps HBM busy is bytes in flight, and the ring holds 110 to 147 KB an SM without registers.  It
+// runs on across the rows that a CTA takes in turn, while x stays where it is.
+// A CTA has 16 warps, WK of them along K for each group of 32 rows: 1 where there are rows enough for every warp of the
+// GPU, which then never wait for each other, up to all 16 where there are few.  Partial sums meet in shared memory,
+// and across the CTAs of a cluster, which split K further, through distributed shared memory; always in the same order,
+// so a result does not depend on timing.
 #include "mx_internal.h"
 #include "mx_fragment.cuh"
 
@@ -24,264 +29,387 @@ namespace mxk {
 
 namespace {
 
-constexpr int MV_THREADS = 256;
-constexpr int MV_ROWS = 128;
+constexpr int MV_ROWS = 32;                           // of a warp
 constexpr int MV_STEP = 128;                          // values of K a step
-__host__ __device__ constexpr int mv_chunk(int NQ) { return NQ <= 2 ? 2048 : 4096 / NQ; }            // values of K staged at once
-__host__ __device__ constexpr int mv_row_bytes(int NQ) { return mv_chunk(NQ) * 2 + 64; }            // 64: odd and even tokens on both bank halves
-__host__ __device__ constexpr int mv_smem(int NQ) { return 8 * NQ * mv_row_bytes(NQ); }
+constexpr int MV_SLOT = 4 * 512 + 256;                // a warp's step in the ring: codes of four rows a lane, scales
+constexpr int MV_MAX_SPLIT = 8;                       // CTAs of a cluster
+constexpr int MV_SMEM = 225 * 1024;                   // dynamic shared memory of a CTA, which has its SM to itself
+constexpr int MV_WARPS = 16;
+__host__ __device__ constexpr int mv_stages(int NQ) { return NQ == 1 ? 4 : 3; }
+__host__ __device__ constexpr int mv_ring(int NQ) { return MV_WARPS * mv_stages(NQ) * MV_SLOT; }
+// Bytes of a staged token: a stretch of `steps` steps, and 64 so that odd and even tokens lie on both bank halves.
+__host__ __device__ constexpr int mv_row_bytes(int steps) { return steps * MV_STEP * 2 + 64; }
+// Partial sums, FP32 [warp][token][row]; staged x; its scales, FP32 [token][step].
+__host__ __device__ constexpr int mv_sums(int M) { return MV_WARPS * M * MV_ROWS * 4; }
+__host__ __device__ constexpr int mv_x(int M, int steps) { return M * (mv_row_bytes(steps) + steps * 4); }
 
-struct Step {
-    uint4 q[4];                                       // codes of the four rows
-    uint4 s;                                          // scales: word b of band b, four columns
+struct MvPlan {
+    int wk;                                           // warps along K (a power of two)
+    int stretch;                                      // steps of x staged at once: all of the CTA's, or a multiple of wk
 };
 
-template <bool A16>
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p, int left) {
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (A16) {
-        if (left > 0) v = __ldcs(reinterpret_cast<const uint4*>(p));
-    } else {                                          // rows on 8 bytes only: K % 32 == 16
-        uint2 a = make_uint2(0u, 0u), b = a;
-        if (left > 0) a = __ldcs(reinterpret_cast<const uint2*>(p));
-        if (left > 16) b = __ldcs(reinterpret_cast<const uint2*>(p) + 1);
-        v = make_uint4(a.x, a.y, b.x, b.y);
-    }
-    return v;
+__device__ __forceinline__ void copy_async_16z(uint32_t dst, const void* src, int bytes) {      // the rest of 16 is zero
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_async_8z(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" :: "r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-template <int NQ, bool A16>
-__global__ void __launch_bounds__(MV_THREADS, NQ <= 2 ? 2 : 1) matvec_kernel(const __grid_constant__ MatvecArgs a) {
+// TAIL: K is not a multiple of the step.  A16: rows start on 16 bytes (K % 32 == 0).
+template <int NQ, bool TAIL, bool A16>
+__global__ void __launch_bounds__(32 * MV_WARPS, 1)
+matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
+    constexpr int WARPS = MV_WARPS, THREADS = 32 * WARPS, STAGES = mv_stages(NQ);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int s_e[8 * NQ];                       // biased exponent that the tokens are scaled by
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-    const int wr = warp & 3, wk = warp >> 2;
+    const int WK = plan.wk, wk = warp & (WK - 1), groups_cta = WARPS / WK, row_bytes = mv_row_bytes(plan.stretch);
+    float* sums = reinterpret_cast<float*>(smem + mv_ring(NQ));                 // [warp][M][MV_ROWS]
+    float* xscale = sums + WARPS * a.M * MV_ROWS;                               // [M][stretch]
+    uint8_t* xs = smem + (MV_SMEM - a.M * row_bytes) / 16 * 16;
     uint32_t rank, ranks;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
-    const int64_t band = blockIdx.x / ranks;
+    // row groups in the order of the scale tiles: group r is rows 128 (r / 4) + 8 (r % 4) + {0..7} + {0, 32, 64, 96}
+    const int groups = (int)((a.N + 127) / 128 * 4), turns = (groups + groups_cta - 1) / groups_cta;
+    const int turn0 = (int)(blockIdx.x / ranks), turn_step = (int)(gridDim.x / ranks);
     const int steps = (int)((a.K + MV_STEP - 1) / MV_STEP);
     const int cta0 = (int)((int64_t)steps * rank / ranks), cta1 = (int)((int64_t)steps * (rank + 1) / ranks);
     const int64_t nct = sf_col_tiles(a.K, 16);
 
-    const uint8_t* row[4];
+    // ---- x of a stretch as FP16: a quad takes a (token, step) pair, 32 values a lane as the fragments have them, finds the largest
+    // element and scales by it.  The loads of the first stretch go ahead of the weights'.
+    uint4 x[4];
+    auto load_x = [&](int c0, int n_steps, int task) {
+        const int pair = task >> 2, m = pair / n_steps, st = pair - m * n_steps;
+        const int64_t k = (int64_t)(c0 + st) * MV_STEP + t4 * 32;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) row[b] = a.q + min64(a.N - 1, band * MV_ROWS + 32 * b + 8 * wr + g) * (a.K / 2) + t4 * 16;
-    const uint8_t* scales = a.s + (band * nct << 9) + ((8 * wr + g) << 4);
-    auto fetch = [&](int step, Step& st) {
-        const int left = (int)(a.K - (int64_t)step * MV_STEP) - t4 * 32;         // valid values of the thread's 32
-#pragma unroll
-        for (int b = 0; b < 4; ++b) st.q[b] = load_codes<A16>(row[b] + (int64_t)step * (MV_STEP / 2), left);
-        st.s = make_uint4(0u, 0u, 0u, 0u);
-        if (left > 0) st.s = __ldcs(reinterpret_cast<const uint4*>(scales + ((2 * (int64_t)step + (t4 >> 1)) << 9)));
-        if (left == 16) {                             // the second block's scale is padding
-            const uint32_t keep = (t4 & 1) ? 0x00FF0000u : 0x000000FFu;
-            st.s.x &= keep; st.s.y &= keep; st.s.z &= keep; st.s.w &= keep;
+        for (int u = 0; u < 4; ++u) {
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (m < a.M && (!TAIL || k + u * 8 < a.K)) x[u] = __ldg(reinterpret_cast<const uint4*>(a.x + m * a.ldx + k) + u);
         }
     };
-
-    float acc[2][NQ][4] = {};
-    int scaled[NQ][2];                                // exponents that acc's columns carry
-    constexpr int CH = mv_chunk(NQ) / MV_STEP;
-    for (int c0 = cta0; c0 < cta1; c0 += CH) {
-        const int c1 = min(cta1, c0 + CH), half = (c1 - c0 + 1) / 2;
-        const int k0 = c0 + wk * half, k1 = min(c1, k0 + half);
-        Step st[2];
-        if (k0 < k1) fetch(k0, st[0]);                // on their way while x is staged
-        if (k0 + 1 < k1) fetch(k0 + 1, st[1]);
-
-        // ---- x of this stretch as FP16: a warp takes a token at a time
-        if (c0 > cta0) __syncthreads();               // the previous stretch is done with
-        constexpr int UNITS = mv_chunk(NQ) / 8 / 32;  // 8-value units a lane
-        const int n_units = (c1 - c0) * (MV_STEP / 8);
-        for (int m = warp; m < 8 * NQ; m += MV_THREADS / 32) {
-            uint4 x[UNITS];
-            uint32_t amax = 0;
+    auto stage_x = [&](int c0, int n_steps, bool loaded) {
+        for (int task = tid; task - lane < 4 * a.M * n_steps; task += THREADS) {
+            if (!loaded) load_x(c0, n_steps, task);
+            loaded = false;
+            uint32_t m2 = 0;
 #pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-                const int unit = lane + 32 * u;
-                const int64_t k = (int64_t)c0 * MV_STEP + unit * 8;
-                x[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (m < a.M && unit < n_units && k < a.K) x[u] = __ldg(reinterpret_cast<const uint4*>(a.x + m * a.ldx + k));
-            }
+            for (int u = 0; u < 4; ++u) m2 = absmax_bf16x2_int(absmax_bf16x2_int(absmax_bf16x2_int(absmax_bf16x2_int(m2, x[u].x), x[u].y), x[u].z), x[u].w);
+            uint32_t amax = fold_halves(m2);
+            if (amax >= 0x7F80u) {                    // infinities and NaN go through as they are: the largest finite element
+                amax = 0;
 #pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-                    amax = max(amax, lo < 0x7F80u ? lo : 0u);                    // infinities and NaN go through as they are
-                    amax = max(amax, hi < 0x7F80u ? hi : 0u);
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t h = (w[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+                        amax = max(amax, h < 0x7F80u ? h : 0u);
+                    }
                 }
             }
-            amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-            // x * 2^(142 - e); e never falls from one stretch to the next, so the sums only ever scale down
-            const int e = max(max((int)(amax >> 7), 27), c0 > cta0 ? s_e[m] : 0);
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            // x * 2^(142 - e), e the biased exponent of the pair's largest element (27 at least: the factor stays finite)
+            const int e = max((int)(amax >> 7), 27);
             const float up = __uint_as_float((uint32_t)(127 + 142 - e) << 23);
+            const int pair = task >> 2, m = pair / n_steps, st = pair - m * n_steps;
+            if (m < a.M) {
+                // unit i of thread t4's four goes to place i * 4 + t4: a quad reads 64 contiguous bytes
+                uint8_t* to = xs + m * row_bytes + st * (MV_STEP * 2) + t4 * 16;
 #pragma unroll
-            for (int u = 0; u < UNITS; ++u) {
-                const int unit = lane + 32 * u;
-                if (unit >= n_units) break;
-                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                uint32_t f[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
-                // unit i of thread t4's four inside a step goes to place i * 4 + t4: a quad reads 64 contiguous bytes
-                const int place = (unit & ~15) + (unit & 3) * 4 + ((unit >> 2) & 3);
-                *reinterpret_cast<uint4*>(smem + m * mv_row_bytes(NQ) + place * 16) = make_uint4(f[0], f[1], f[2], f[3]);
+                for (int u = 0; u < 4; ++u)
+                    *reinterpret_cast<uint4*>(to + u * 64) =
+                        make_uint4(pack_f16x2(bf16_lo(x[u].x) * up, bf16_hi(x[u].x) * up), pack_f16x2(bf16_lo(x[u].y) * up, bf16_hi(x[u].y) * up),
+                                   pack_f16x2(bf16_lo(x[u].z) * up, bf16_hi(x[u].z) * up), pack_f16x2(bf16_lo(x[u].w) * up, bf16_hi(x[u].w) * up));
+                if (t4 == 0) xscale[m * plan.stretch + st] = __uint_as_float((uint32_t)(e - 15) << 23);
             }
-            __syncwarp();
-            if (lane == 0) s_e[m] = e;
         }
         __syncthreads();
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int e = s_e[nq * 8 + 2 * t4 + j];
-                if (c0 > cta0) {
-                    const float f = __uint_as_float((uint32_t)max(0, 127 + scaled[nq][j] - e) << 23);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        acc[t][nq][j] *= f;
-                        acc[t][nq][2 + j] *= f;
-                    }
-                }
-                scaled[nq][j] = e;
-            }
+    };
+    load_x(cta0, min(plan.stretch, cta1 - cta0), tid);
 
-        auto multiply = [&](int step, const Step& w) {
-            const uint8_t* xs = smem + g * mv_row_bytes(NQ) + (step - c0) * (MV_STEP * 2) + t4 * 16;
-            const uint32_t sw[4] = {w.s.x, w.s.y, w.s.z, w.s.w};
+    // ---- the warp's steps, cta0 + wk, + WK, ... of one row group after the other, enter the ring STAGES - 1 ahead
+    uint8_t* ring = smem + warp * (STAGES * MV_SLOT);
+    const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
+    int in_group = cta0 + wk < cta1 ? turn0 * groups_cta + warp / WK : groups;
+    int in_step = cta0 + wk, in_slot = 0;
+    const uint8_t *in_q[4], *in_s;                    // the thread's next bytes
+    auto left_of = [&](int step) { return (int)min64(32, a.K - (int64_t)step * MV_STEP - t4 * 32); };   // valid values of the thread's 32
+    auto aim = [&]() {                                // at the first step of in_group
+        const int64_t band = in_group >> 2, r0 = band * 128 + 8 * (in_group & 3) + g;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {             // 8 of the thread's 32 values: two k-steps
-                uint4 xb[NQ];
+        for (int b = 0; b < 4; ++b) in_q[b] = a.q + min64(a.N - 1, r0 + 32 * b) * (a.K / 2) + (int64_t)in_step * (MV_STEP / 2) + t4 * 16;
+        in_s = a.s + ((band * nct + 2 * (int64_t)in_step + (t4 >> 1)) << 9) + ((8 * (in_group & 3) + g) << 4);
+    };
+    if (in_group < groups) aim();
+    auto issue = [&]() {
+        if (in_group < groups) {
+            const uint32_t slot_at = ring_u32 + in_slot * MV_SLOT, dst = slot_at + lane * 16, dst_s = slot_at + 4 * 512 + (g * 2 + (t4 >> 1)) * 16;
+            if (!TAIL) {
 #pragma unroll
-                for (int nq = 0; nq < NQ; ++nq) xb[nq] = *reinterpret_cast<const uint4*>(xs + nq * 8 * mv_row_bytes(NQ) + i * 64);
-                uint32_t f[4][4];
+                for (int b = 0; b < 4; ++b) copy_async_16(dst + b * 512, in_q[b]);
+                if ((t4 & 1) == 0) copy_async_16(dst_s, in_s);
+            } else {                                  // beyond K zeros, from an address that is valid all the same
+                const int left = max(0, left_of(in_step));
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    const uint32_t codes = i == 0 ? w.q[b].x : (i == 1 ? w.q[b].y : (i == 2 ? w.q[b].z : w.q[b].w));
-                    e2m1x8_to_f16(codes, f[b]);
-                    // column 2 (t4 & 1) + i / 2 of the four, in both halves
-                    const uint32_t sc = e4m3x2_to_f16x2(__byte_perm(sw[b], 0u, 0x1111u * (2 * (t4 & 1) + (i >> 1))));
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) f[b][j] = mul_f16x2(f[b][j], sc);
-                }
-#pragma unroll
-                for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        mma_16816(acc[t][nq], f[2 * t][0], f[2 * t + 1][0], f[2 * t][1], f[2 * t + 1][1], xb[nq].x, xb[nq].y);
-                        mma_16816(acc[t][nq], f[2 * t][2], f[2 * t + 1][2], f[2 * t][3], f[2 * t + 1][3], xb[nq].z, xb[nq].w);
+                    const uint8_t* src = left > 0 ? in_q[b] : a.q;
+                    if (A16) {
+                        copy_async_16z(dst + b * 512, src, left > 0 ? 16 : 0);
+                    } else {                          // K % 32 == 16: rows start on 8 bytes only
+                        copy_async_8z(dst + b * 512, src, left > 0 ? 8 : 0);
+                        copy_async_8z(dst + b * 512 + 8, left > 16 ? src + 8 : src, left > 16 ? 8 : 0);
                     }
+                }
+                if ((t4 & 1) == 0) copy_async_16z(dst_s, left > 0 ? in_s : a.s, left > 0 ? 16 : 0);
             }
-        };
-        for (int k = k0; k < k1; k += 2) {
-            multiply(k, st[0]);
-            if (k + 2 < k1) fetch(k + 2, st[0]);
-            if (k + 1 < k1) {
-                multiply(k + 1, st[1]);
-                if (k + 3 < k1) fetch(k + 3, st[1]);
+            in_step += WK;
+            if (in_step < cta1) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) in_q[b] += WK * (MV_STEP / 2);
+                in_s += WK * 1024;
+            } else {
+                in_step = cta0 + wk;
+                in_group += turn_step * groups_cta;
+                if (in_group < groups) aim();
             }
         }
-    }
-
-    // ---- the sums: two warps along K, then the cluster's CTAs, [token][row] in shared memory
-    __syncthreads();
-    float* sum = reinterpret_cast<float*>(smem);      // [8 NQ][MV_ROWS]
+        copy_async_commit();
+        in_slot = in_slot + 1 == STAGES ? 0 : in_slot + 1;
+    };
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-        if (wk == pass) {
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+
+    int slot = 0;
+    const int sc_shift = 16 * (t4 & 1);
+    const bool once = cta1 - cta0 <= plan.stretch;    // x is staged once for all rows
+    for (int turn = turn0; turn < turns; turn += turn_step) {
+        const int group = turn * groups_cta + warp / WK;
+        float acc[2][NQ][4] = {};
+        for (int c0 = cta0; c0 < cta1; c0 += plan.stretch) {
+            const int c1 = min(cta1, c0 + plan.stretch);
+            const bool start = turn == turn0 && c0 == cta0;
+            if (start || !once) {
+                if (!start) __syncthreads();          // the previous stretch is done with
+                stage_x(c0, c1 - c0, start);
+            }
+
+            // ---- the products.  A stretch begins at a multiple of WK steps from cta0, so the warps' turns go on.
+            // Columns beyond the last token repeat it and are not stored.
+            if (group < groups) {
+                const uint8_t* xr[NQ];
+#pragma unroll
+                for (int nq = 0; nq < NQ; ++nq) xr[nq] = xs + min(a.M - 1, nq * 8 + g) * row_bytes + t4 * 16;
+                for (int step = c0 + wk; step < c1; step += WK) {
+                    copy_async_wait<STAGES - 2>();
+                    __syncwarp();                     // the scales come by other lanes; and the slot of the last step is free
+                    const uint8_t* st = ring + slot * MV_SLOT;
+                    uint4 q[4], s;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) q[b] = *reinterpret_cast<const uint4*>(st + b * 512 + lane * 16);
+                    s = *reinterpret_cast<const uint4*>(st + 4 * 512 + (g * 2 + (t4 >> 1)) * 16);
+                    if (TAIL && left_of(step) < 32) {  // scales beyond K are padding
+                        const uint32_t keep = left_of(step) < 16 ? 0u : ((t4 & 1) ? 0x00FF0000u : 0x000000FFu);
+                        s.x &= keep; s.y &= keep; s.z &= keep; s.w &= keep;
+                    }
+                    issue();
+                    slot = slot + 1 == STAGES ? 0 : slot + 1;
+                    const int x_at = (step - c0) * (MV_STEP * 2);
+                    // the two block scales of the thread's run, columns 2 (t4 & 1) and + 1 of the four
+                    const uint32_t sc[4] = {e4m3x2_to_f16x2(s.x >> sc_shift), e4m3x2_to_f16x2(s.y >> sc_shift),
+                                            e4m3x2_to_f16x2(s.z >> sc_shift), e4m3x2_to_f16x2(s.w >> sc_shift)};
+                    float part[2][NQ][4] = {};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {     // 8 of the thread's 32 values: two k-steps
+                        uint4 xb[NQ];
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq) xb[nq] = *reinterpret_cast<const uint4*>(xr[nq] + x_at + i * 64);
+                        uint32_t f[4][4];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const uint32_t codes = i == 0 ? q[b].x : (i == 1 ? q[b].y : (i == 2 ? q[b].z : q[b].w));
+                            e2m1x8_to_f16(codes, f[b]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) f[b][j] = i < 2 ? mul_f16x2_lo(f[b][j], sc[b]) : mul_f16x2_hi(f[b][j], sc[b]);
+                        }
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                mma_16816(part[t][nq], f[2 * t][0], f[2 * t + 1][0], f[2 * t][1], f[2 * t + 1][1], xb[nq].x, xb[nq].y);
+                                mma_16816(part[t][nq], f[2 * t][2], f[2 * t + 1][2], f[2 * t][3], f[2 * t + 1][3], xb[nq].z, xb[nq].w);
+                            }
+                    }
+#pragma unroll
+                    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float xsc = xscale[min(a.M - 1, nq * 8 + 2 * t4 + j) * plan.stretch + step - c0];
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                acc[t][nq][j] = __fmaf_rn(part[t][nq][j], xsc, acc[t][nq][j]);
+                                acc[t][nq][2 + j] = __fmaf_rn(part[t][nq][2 + j], xsc, acc[t][nq][2 + j]);
+                            }
+                        }
+                }
+            }
+        }
+
+        // ---- the results: row 32 b + r of the group's four runs of 8, token m
+        auto store = [&](int group, int b, int r, int m, float v) {
+            const int64_t n = (int64_t)(group >> 2) * 128 + 8 * (group & 3) + 32 * b + r;
+            if (group >= groups || n >= a.N || m >= a.M) return;
+            v *= __ldg(a.s2 + (a.s2_per_row ? n : 0));
+            if (a.y_fp32) static_cast<float*>(a.y)[m * a.ldy + n] = v;
+            else static_cast<uint16_t*>(a.y)[m * a.ldy + n] = (uint16_t)pack_bf16x2(v, 0.0f);
+        };
+        if (WK == 1 && ranks == 1) {
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int m = nq * 8 + 2 * t4 + (j & 1);
-                        float* d = sum + m * MV_ROWS + 32 * (2 * t + (j >> 1)) + 8 * wr + g;
-                        const float v = acc[t][nq][j];
-                        *d = pass == 0 ? v : (*d + v);
-                    }
+                    for (int j = 0; j < 4; ++j) store(group, 2 * t + (j >> 1), g, nq * 8 + 2 * t4 + (j & 1), acc[t][nq][j]);
+            continue;
         }
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int m = nq * 8 + 2 * t4 + (j & 1);
+                if (m < a.M) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) sums[(warp * a.M + m) * MV_ROWS + 8 * (2 * t + (j >> 1)) + g] = acc[t][nq][j];
+                }
+            }
         __syncthreads();
-    }
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-    const uint32_t sum_u32 = (uint32_t)__cvta_generic_to_shared(sum), e_u32 = (uint32_t)__cvta_generic_to_shared(s_e);
-    for (int i = tid + (int)rank * MV_THREADS; i < a.M * MV_ROWS; i += MV_THREADS * (int)ranks) {
-        const int m = i / MV_ROWS, rr = i % MV_ROWS;
-        float y = 0.0f;
-        for (uint32_t c = 0; c < ranks; ++c) {
-            uint32_t at, at_e;
-            float v;
-            int e;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(sum_u32 + 4 * i), "r"(c));
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at_e) : "r"(e_u32 + 4 * m), "r"(c));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(e) : "r"(at_e) : "memory");
-            y += v * __uint_as_float((uint32_t)(e - 15) << 23);
+        // the WK partial sums of an element lie M rows apart; with a cluster the CTA's sum takes the first one's place
+        const int per_group = a.M * MV_ROWS;
+        for (int i = tid; i < groups_cta * per_group; i += THREADS) {
+            const int gi = i / per_group, e = i - gi * per_group;
+            float* at = sums + gi * WK * per_group + e;
+            float y = 0.0f;
+#pragma unroll 4
+            for (int w = 0; w < WK; ++w) y += at[w * per_group];
+            if (ranks > 1) *at = y;
+            else store(turn * groups_cta + gi, (e % MV_ROWS) >> 3, e & 7, e / MV_ROWS, y);
         }
-        const int64_t n = band * MV_ROWS + rr;
-        if (n >= a.N) continue;
-        y *= __ldg(a.s2 + (a.s2_per_row ? n : 0));
-        if (a.y_fp32) static_cast<float*>(a.y)[m * a.ldy + n] = y;
-        else static_cast<uint16_t*>(a.y)[m * a.ldy + n] = (uint16_t)pack_bf16x2(y, 0.0f);
+        if (ranks == 1) {
+            __syncthreads();                          // the sums are read before anybody writes them again
+            continue;
+        }
+        cluster_barrier();
+        for (int i = tid + (int)rank * THREADS; i < groups_cta * per_group; i += THREADS * (int)ranks) {
+            const int gi = i / per_group, e = i - gi * per_group;
+            const uint32_t at = (uint32_t)__cvta_generic_to_shared(sums + gi * WK * per_group + e);
+            float v[MV_MAX_SPLIT];
+#pragma unroll
+            for (int c = 0; c < MV_MAX_SPLIT; ++c) {
+                uint32_t there;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(min(c, (int)ranks - 1)));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[c]) : "r"(there) : "memory");
+            }
+            float y = v[0];
+#pragma unroll
+            for (int c = 1; c < MV_MAX_SPLIT; ++c)
+                if (c < (int)ranks) y += v[c];
+            store(turn * groups_cta + gi, (e % MV_ROWS) >> 3, e & 7, e / MV_ROWS, y);
+        }
+        cluster_barrier();                            // and before anybody leaves
     }
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    copy_async_wait<0>();
 }
 
-// CTAs along K: the split whose slowest wave of CTAs is shortest, counting a CTA's fixed cost as four steps.
-int mv_split(int64_t bands, int steps, int slots) {
-    int best = 1;
+// The split of the work: warps along K and CTAs of a cluster along K, for one CTA an SM, such that the busiest warp has
+// the least to do, in steps.  Counted besides the steps: half a step for a meeting of a CTA's warps, two for one of a
+// cluster, the staging of x by its size.  clusters[c] is how many clusters of c CTAs the device runs at once (the SMs
+// of a cluster share a GPC, so it is below SMs / c).
+constexpr double MV_STAGING = 0.008, MV_MEET = 0.5, MV_MEET_CLUSTER = 2.0;
+MvPlan mv_plan(int NQ, const MatvecArgs& a, const int (&clusters)[MV_MAX_SPLIT + 1], int& ctas_k) {
+    const int steps = (int)((a.K + MV_STEP - 1) / MV_STEP), warps = MV_WARPS;
+    const int64_t groups = (a.N + 127) / 128 * 4;
+    int fits = 0;                                     // steps of x that have room
+    while (fits < steps && mv_ring(NQ) + mv_sums(a.M) + mv_x(a.M, fits + 1) + 16 <= MV_SMEM) ++fits;
+    MvPlan best{1, 1};
     double least = 1e30;
-    for (int c = 1; c <= 8 && 2 * c <= max(2, steps); ++c) {
-        const double waves = (double)((bands * c + slots - 1) / slots);
-        const double cost = waves * ((double)((steps + 2 * c - 1) / (2 * c)) + 4.0);
-        if (cost < least) {
-            least = cost;
-            best = c;
+    ctas_k = 1;
+    for (int c = 1; c <= MV_MAX_SPLIT && c <= steps; ++c) {
+        if (clusters[c] < 1) continue;
+        for (int wk = 1; warps % wk == 0 && (c * wk <= steps || wk == 1); wk *= 2) {
+            const int per_turn = warps / wk, mine = (steps + c - 1) / c;
+            const int64_t turns = (groups + per_turn - 1) / per_turn, rounds = (turns + clusters[c] - 1) / clusters[c];
+            const int stretch = mine <= fits ? mine : fits / wk * wk;
+            if (stretch < 1) continue;
+            const double staging = 0.5 + MV_STAGING * a.M * stretch;
+            const int again = mine <= fits ? 0 : (mine + stretch - 1) / stretch;
+            const double cost = (double)rounds * ((mine + wk - 1) / wk + (wk > 1 ? MV_MEET : 0.0) + (c > 1 ? MV_MEET_CLUSTER : 0.0) + staging * again) + staging;
+            if (cost < least) {
+                least = cost;
+                best = MvPlan{wk, stretch};
+                ctas_k = c;
+            }
         }
     }
     return best;
 }
 
-template <int NQ, bool A16>
-cudaError_t launch_nq(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
+template <int NQ, bool TAIL, bool A16>
+cudaError_t launch_nq(const MatvecArgs& a, cudaStream_t stream) {
     static PerDevice pd;
-    int resident = 0;
-    cudaError_t e = per_device_once(pd, resident, [](int& value) {
-        const cudaError_t s = cudaFuncSetAttribute(matvec_kernel<NQ, A16>, cudaFuncAttributeMaxDynamicSharedMemorySize, mv_smem(NQ));
-        return s != cudaSuccess ? s : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&value, matvec_kernel<NQ, A16>, MV_THREADS, mv_smem(NQ));
-    });
-    if (e != cudaSuccess) return e;
-    const int64_t bands = (a.N + MV_ROWS - 1) / MV_ROWS;
-    const int c = mv_split(bands, (int)((a.K + MV_STEP - 1) / MV_STEP), num_sms * max(1, resident));
+    static int clusters[MX_MAX_DEVICES][MV_MAX_SPLIT + 1];
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(bands * c));
-    cfg.blockDim = dim3(MV_THREADS);
-    cfg.dynamicSmemBytes = mv_smem(NQ);
-    cfg.stream = stream;
+    cfg.blockDim = dim3(32 * MV_WARPS);
+    cfg.dynamicSmemBytes = MV_SMEM;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim = {(unsigned)c, 1, 1};
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, matvec_kernel<NQ, A16>, a);
+    int dev = 0;
+    cudaError_t e = per_device_once(pd, dev, [&](int& value) {
+        cudaError_t s = cudaGetDevice(&value);
+        if (s == cudaSuccess) s = cudaFuncSetAttribute(matvec_kernel<NQ, TAIL, A16>, cudaFuncAttributeMaxDynamicSharedMemorySize, MV_SMEM);
+        for (int c = 1; c <= MV_MAX_SPLIT && s == cudaSuccess; ++c) {
+            at.val.clusterDim = {(unsigned)c, 1, 1};
+            cfg.gridDim = dim3((unsigned)c);
+            s = cudaOccupancyMaxActiveClusters(&clusters[value][c], matvec_kernel<NQ, TAIL, A16>, &cfg);
+        }
+        return s;
+    });
+    if (e != cudaSuccess) return e;
+    int c = 1;
+    const MvPlan plan = mv_plan(NQ, a, clusters[dev], c);
+    const int per_turn = MV_WARPS / plan.wk;
+    const int64_t turns = ((a.N + 127) / 128 * 4 + per_turn - 1) / per_turn;
+    at.val.clusterDim = {(unsigned)c, 1, 1};
+    cfg.gridDim = dim3((unsigned)(min64(turns, max(1, clusters[dev][c])) * c));
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, matvec_kernel<NQ, TAIL, A16>, a, plan);
 }
 
 template <int NQ>
-cudaError_t launch_aligned(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
-    return a.K % 32 == 0 ? launch_nq<NQ, true>(a, num_sms, stream) : launch_nq<NQ, false>(a, num_sms, stream);
+cudaError_t launch_aligned(const MatvecArgs& a, cudaStream_t stream) {
+    if (a.K % MV_STEP == 0) return launch_nq<NQ, false, true>(a, stream);
+    return a.K % 32 == 0 ? launch_nq<NQ, true, true>(a, stream) : launch_nq<NQ, true, false>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_matvec_nvfp4(const MatvecArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.M <= 8) return launch_aligned<1>(a, num_sms, stream);
-    if (a.M <= 16) return launch_aligned<2>(a, num_sms, stream);
-    if (a.M <= 32) return launch_aligned<4>(a, num_sms, stream);
-    return launch_aligned<8>(a, num_sms, stream);
+// Sixteen tokens a pass over the weights: a third and fourth fragment of eight columns would not fit the registers (32
+// tokens in one pass 42 us, in two 37 at 12288 x 4096), and the weights of most layers stay in L2 for the next pass.
+cudaError_t launch_matvec_nvfp4(const MatvecArgs& a, cudaStream_t stream) {
+    for (int m = 0; m < a.M; m += 16) {
+        MatvecArgs p = a;
+        p.M = a.M - m < 16 ? a.M - m : 16;
+        p.x = a.x + m * a.ldx;
+        p.y = a.y_fp32 ? static_cast<void*>(static_cast<float*>(a.y) + m * a.ldy) : static_cast<void*>(static_cast<uint16_t*>(a.y) + m * a.ldy);
+        const cudaError_t e = p.M <= 8 ? launch_aligned<1>(p, stream) : launch_aligned<2>(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace mxk

@@ -1,4 +1,4 @@
-// mx_fragment.cuh -- NVFP4 codes and scales as FP16 operands of mma.m16n8k16, in registers.
+// mx_fragment.cuh -- NVFP4 codes and scales as FP16 operands of mma.m16n8k16, in registers, and cp.async.
 #pragma once
 
 #include <cstdint>
@@ -13,6 +13,19 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// a times the low (high) half of b.
+__device__ __forceinline__ uint32_t mul_f16x2_lo(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 s;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b32 s, {lo, lo};\n\tmul.rn.f16x2 %0, %1, s;\n\t}"
+        : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2_hi(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 s;\n\tmov.b32 {lo, hi}, %2;\n\tmov.b32 s, {hi, hi};\n\tmul.rn.f16x2 %0, %1, s;\n\t}"
+        : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 // Four code bytes -> four FP16 pairs (low nibble in the low half).
@@ -36,5 +49,12 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+
+__device__ __forceinline__ void copy_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 }  // namespace mxk

@@ -193,7 +193,7 @@ struct MatvecArgs {
     int M; int64_t N, K;
     void* y; int64_t ldy; bool y_fp32;
 };
-cudaError_t launch_matvec_nvfp4(const MatvecArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_matvec_nvfp4(const MatvecArgs& a, cudaStream_t stream);
 
 int device_sm_count();
 

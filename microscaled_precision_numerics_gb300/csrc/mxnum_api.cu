@@ -557,7 +557,7 @@ mx_status mx_nvfp4_matvec(const void* x, int64_t ldx, const uint8_t* q, const ui
     a.x = static_cast<const uint16_t*>(x); a.ldx = ldx;
     a.q = q; a.s = s; a.s2 = s2; a.s2_per_row = s2_scope == MX_SCOPE_ROW;
     a.M = (int)M; a.N = N; a.K = K; a.y = y; a.ldy = ldy; a.y_fp32 = y_fp32 != 0;
-    return from_cuda(mxk::launch_matvec_nvfp4(a, mxk::device_sm_count(), stream));
+    return from_cuda(mxk::launch_matvec_nvfp4(a, stream));
 }
 
 mx_status mx_check_device_status(void) {
