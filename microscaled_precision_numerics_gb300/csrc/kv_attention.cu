@@ -31,7 +31,8 @@ namespace {
 constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_TILE = 32;                 // tokens of a warp's step: two records
-constexpr int ATT_MIN_TILES = 4;             // smallest share of a CTA: one step a warp
+constexpr int ATT_ITEM_COST = 8;             // what an item costs besides its tiles, in tiles
+constexpr int ATT_MIN_SHARE = 12;            // smallest share of a CTA: an item's fixed cost and one step a warp
 constexpr float ATT_SLACK = 8.0f;            // the running maximum may lag by 2^8 (P stays below 2^8 in FP16)
 
 __host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 6 : (D == 128 ? 3 : 2); }
@@ -88,6 +89,7 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 // What request r asks for: tiles of its context, items (kv head x column tile) and the first tile's position.
 struct Request {
     int first, count, len, tile0, tiles, col_tiles;
+    __device__ int64_t cost(int kv_heads) const { return (int64_t)(tiles + ATT_ITEM_COST) * col_tiles * kv_heads; }
 };
 template <int NQ>
 __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r) {
@@ -121,14 +123,14 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
     const KvAttentionArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
 
-    // ---- the CTA's share of all tiles: equal runs over (request, kv head, column tile, context tile)
+    // ---- the CTA's share: equal runs over (request, kv head, column tile, fixed cost and context tiles)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int per = (a.R + ATT_THREADS - 1) / ATT_THREADS, r0 = tid * per;
     int64_t mine = 0;
     int my_items = 0;
     for (int r = r0; r < min(a.R, r0 + per); ++r) {
         const Request q = request_of<NQ>(a, r);
-        mine += (int64_t)q.tiles * q.col_tiles * a.kv_heads;
+        mine += q.cost(a.kv_heads);
         my_items += q.col_tiles * a.kv_heads;
     }
     int64_t incl = mine;
@@ -157,14 +159,14 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         }
         total += s_warp_sum[w];
     }
-    const int64_t share = max64(ATT_MIN_TILES, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t share = max64(ATT_MIN_SHARE, (total + gridDim.x - 1) / gridDim.x);
     const int64_t begin = min64(total, blockIdx.x * share), end = min64(total, begin + share);
     if (mine > 0 && begin >= excl && begin < excl + mine && begin < end) {
         int64_t at = excl;
         int r = r0, it = excl_items;
         for (;; ++r) {
             const Request q = request_of<NQ>(a, r);
-            const int64_t w = (int64_t)q.tiles * q.col_tiles * a.kv_heads;
+            const int64_t w = q.cost(a.kv_heads);
             if (begin < at + w) break;
             at += w;
             it += q.col_tiles * a.kv_heads;
@@ -183,78 +185,29 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
     if (begin >= end) return;
 
     int r = s_r, item0 = s_item;             // request; number of its first item
-    int64_t off = s_off;                     // tile inside the request
+    int64_t off = s_off;                     // place inside the request
     Request rq = request_of<NQ>(a, r);
     uint8_t* ring = smem + warp * (STAGES * STAGE_BYTES);
     const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
 
     for (int64_t at = begin; at < end;) {
-        while (off >= (int64_t)rq.tiles * rq.col_tiles * a.kv_heads) {     // next request with work
-            off -= (int64_t)rq.tiles * rq.col_tiles * a.kv_heads;
+        while (off >= rq.cost(a.kv_heads)) {                               // next request with work
+            off -= rq.cost(a.kv_heads);
             item0 += rq.col_tiles * a.kv_heads;
             rq = request_of<NQ>(a, ++r);
         }
-        const int item = (int)(off / rq.tiles), first_tile = (int)(off - (int64_t)item * rq.tiles);
-        const int n_tiles = (int)min64(rq.tiles - first_tile, end - at);
+        const int per_item = rq.tiles + ATT_ITEM_COST, item = (int)(off / per_item), in_item = (int)(off - (int64_t)item * per_item);
+        const int run = (int)min64(per_item - in_item, end - at);          // of the share inside this item
+        const int first_tile = max(0, in_item - ATT_ITEM_COST), n_tiles = in_item + run - ATT_ITEM_COST - first_tile;
+        if (n_tiles <= 0) {                                                // nothing but the fixed cost: the next CTA begins the item
+            at += run;
+            off += run;
+            continue;
+        }
+        const int64_t item_at = at - in_item;                              // where the item begins
         const int h = item / rq.col_tiles, col0 = (item - h * rq.col_tiles) * 8 * NQ;
         const int cols = rq.count * a.group;                               // query rows of this kv head
         const int base_pos = rq.len - rq.count;                            // position of new token 0
-
-        // ---- Q^T fragments: column g of each eight, elements [t4 * D / 4, + D / 4), as FP16 scaled by a power of two
-        uint32_t qf[NQ][KS][2];
-        float mul[NQ][2];                                                  // score -> exponent of two, columns 2 t4, 2 t4 + 1
-        int pos[NQ][2];                                                    // last position they attend to (-1: none)
-        const float S_k = __ldg(a.s_k + h);
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-            const int col = col0 + nq * 8 + g;
-            const bool real = col < cols;
-            const int i = real ? (int)divu32((uint32_t)col, p.dv_group) : 0;
-            const int hq = real ? h * a.group + (col - i * a.group) : 0;
-            const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(rq.first + i) * a.q_token + (int64_t)hq * a.q_head + t4 * (D / 4));
-            uint32_t w[D / 8];
-            uint32_t amax = 0;
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (real) v = __ldg(src + k);
-                w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
-            }
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-                const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
-                amax = max(amax, lo < 0x7F80u ? lo : 0u);                  // infinities and NaN go through as they are
-                amax = max(amax, hi < 0x7F80u ? hi : 0u);
-            }
-            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            // x * 2^(142 - e) with e the biased exponent of the largest element (27 at least: the factor stays finite)
-            const int e = max((int)(amax >> 7), 27);
-            const float up = __uint_as_float((uint32_t)(127 + 142 - e) << 23);
-            const float c = a.scale * 1.4426950408889634f * S_k * __uint_as_float((uint32_t)max(e - 15, 1) << 23);
-#pragma unroll
-            for (int k = 0; k < D / 8; ++k) qf[nq][k >> 1][k & 1] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mul[nq][j] = __shfl_sync(0xFFFFFFFFu, c, 4 * (2 * t4 + j));
-                const int cj = col0 + nq * 8 + 2 * t4 + j;
-                pos[nq][j] = cj < cols ? base_pos + (int)divu32((uint32_t)cj, p.dv_group) : -1;
-            }
-        }
-        // positions that every column of the tile attends to
-        const int last_col = min(cols, col0 + 8 * NQ) - 1;
-        const int64_t all_hi = base_pos + (int64_t)divu32((uint32_t)col0, p.dv_group) + 1;
-        const int64_t all_lo = a.window > 0 ? base_pos + (int64_t)divu32((uint32_t)last_col, p.dv_group) + 1 - a.window : 0;
-
-        float o[NQ][MT][4] = {};
-        float m[NQ][2], l[NQ][2];
-#pragma unroll
-        for (int nq = 0; nq < NQ; ++nq)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                m[nq][j] = -INFINITY;
-                l[nq][j] = 0.0f;
-            }
 
         // ---- the warp's tiles: first_tile + warp, + 4, ...; lane i looks up record i & 1 of step 16 b + i / 2
         const int steps = n_tiles > warp ? (n_tiles - warp + ATT_WARPS - 1) / ATT_WARPS : 0;
@@ -271,51 +224,129 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         };
         int64_t now = look_up(0), next = look_up(1);
         uint32_t there = 0;                                                // two bits a stage: its records hold data
+        int in_slot = 0;
         auto issue = [&](int k) {
             if (k < steps) {
-                const int s = k % STAGES;
                 if ((k & 15) == 0 && k > 0) {
                     now = next;
                     next = look_up((k >> 4) + 1);
                 }
                 const int64_t a0 = __shfl_sync(0xFFFFFFFFu, now, 2 * (k & 15)), a1 = __shfl_sync(0xFFFFFFFFu, now, 2 * (k & 15) + 1);
-                there = (there & ~(3u << (2 * s))) | ((a0 >= 0 ? 1u : 0u) << (2 * s)) | ((a1 >= 0 ? 2u : 0u) << (2 * s));
-                const uint32_t dst = ring_u32 + s * STAGE_BYTES;
+                const uint32_t got = (a0 >= 0 ? 1u : 0u) | (a1 >= 0 ? 2u : 0u);
+                there = (there & ~(3u << (2 * in_slot))) | (got << (2 * in_slot));
+                const uint32_t dst = ring_u32 + in_slot * STAGE_BYTES + 16 * lane;
+                const uint8_t *p0 = a.cache + a0 + 16 * lane, *p1 = a.cache + a1 + 16 * (lane - CHUNKS);
 #pragma unroll
-                for (int i = 0; i < (2 * CHUNKS + 31) / 32; ++i) {
-                    const int c = lane + 32 * i;
-                    const int64_t from = c < CHUNKS ? a0 : a1;
-                    if (c < 2 * CHUNKS && from >= 0) copy_async_16(dst + 16 * c, a.cache + from + 16 * (c < CHUNKS ? c : c - CHUNKS));
+                for (int i = 0; i < (2 * CHUNKS + 31) / 32; ++i) {                // 16-byte pieces lane + 32 i of the two records
+                    if (32 * i + 32 <= CHUNKS) {
+                        if (got & 1u) copy_async_16(dst + 512 * i, p0 + 512 * i);
+                    } else if (32 * i >= CHUNKS) {
+                        if ((got & 2u) && (32 * i + 32 <= 2 * CHUNKS || lane < 2 * CHUNKS - 32 * i)) copy_async_16(dst + 512 * i, p1 + 512 * i);
+                    } else {
+                        if (got & (lane < CHUNKS - 32 * i ? 1u : 2u)) copy_async_16(dst + 512 * i, (lane < CHUNKS - 32 * i ? p0 : p1) + 512 * i);
+                    }
                 }
             }
             copy_async_commit();
+            in_slot = in_slot + 1 == STAGES ? 0 : in_slot + 1;
         };
 #pragma unroll
         for (int k = 0; k < STAGES - 1; ++k) issue(k);
 
-        for (int k = 0; k < steps; ++k) {
+
+        // ---- Q^T fragments: column g of each eight, elements [t4 * D / 4, + D / 4), as FP16 scaled by a power of two
+        uint32_t qf[NQ][KS][2];
+        float mul[NQ][2], slack[NQ][2];                                    // score -> exponent of two, columns 2 t4, 2 t4 + 1
+        int pos[NQ][2];                                                    // last position they attend to (-1: none)
+        const float S_k = __ldg(a.s_k + h);
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            const int col = col0 + nq * 8 + g;
+            const bool real = col < cols;
+            const int i = real ? (int)divu32((uint32_t)col, p.dv_group) : 0;
+            const int hq = real ? h * a.group + (col - i * a.group) : 0;
+            const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(rq.first + i) * a.q_token + (int64_t)hq * a.q_head + t4 * (D / 4));
+            uint32_t w[D / 8], m2 = 0;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (real) v = __ldg(src + k);
+                w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+            }
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) m2 = absmax_bf16x2_int(m2, w[k]);
+            uint32_t amax = fold_halves(m2);
+            if (amax >= 0x7F80u) {                                         // infinities and NaN go through as they are
+                amax = 0;
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) {
+                    const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+                    amax = max(amax, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+                }
+            }
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            // x * 2^(142 - e) with e the biased exponent of the largest element (27 at least: the factor stays finite)
+            const int e = max((int)(amax >> 7), 27);
+            const float c = a.scale * 1.4426950408889634f * S_k * __uint_as_float((uint32_t)(e - 15) << 23);
+            // a negative factor goes into Q: scores are then compared before they are multiplied
+            const float up = copysignf(__uint_as_float((uint32_t)(127 + 142 - e) << 23), c);
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) qf[nq][k >> 1][k & 1] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                mul[nq][j] = __shfl_sync(0xFFFFFFFFu, fabsf(c), 4 * (2 * t4 + j));
+                slack[nq][j] = fminf(ATT_SLACK / mul[nq][j], 1e30f);
+                const int cj = col0 + nq * 8 + 2 * t4 + j;
+                pos[nq][j] = cj < cols ? base_pos + (int)divu32((uint32_t)cj, p.dv_group) : -1;
+            }
+        }
+        // positions that every column of the tile attends to
+        const int last_col = min(cols, col0 + 8 * NQ) - 1;
+        const int all_hi = base_pos + (int)divu32((uint32_t)col0, p.dv_group) + 1;
+        const int all_lo = a.window > 0 ? max(0, base_pos + (int)divu32((uint32_t)last_col, p.dv_group) + 1 - a.window) : 0;
+
+        float o[NQ][MT][4] = {};
+        float m[NQ][2], l[NQ][2];
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                m[nq][j] = -INFINITY;
+                l[nq][j] = 0.0f;
+            }
+
+        int slot = 0, tok0 = (rq.tile0 + first_tile + warp) * ATT_TILE;
+        const uint8_t* const at_k = ring + kv_token_of_row(g) * (D / 2) + t4 * (D / 8);
+        const uint8_t* const at_ks = ring + kv_k_scales(D) + kv_token_of_row(g) * (D / 16) + t4 * (D / 64);
+        const uint8_t* const at_v = ring + kv_v_codes(D) + g * (D / 16);
+        const uint8_t* const at_vs = ring + kv_v_scales(D) + (D == 64 ? g >> 1 : (D == 128 ? g : 2 * g)) * 16 + 2 * t4;
+        const int v_row[2] = {kv_token_of_row(2 * t4) * (D / 2), kv_token_of_row(2 * t4 + 1) * (D / 2)};
+        for (int k = 0; k < steps; ++k, tok0 += ATT_WARPS * ATT_TILE) {
             copy_async_wait<STAGES - 2>();
             __syncwarp();
             issue(k + STAGES - 1);
-            const uint8_t* st = ring + (k % STAGES) * STAGE_BYTES;
-            const uint32_t have = (there >> (2 * (k % STAGES))) & 3u;
-            const int64_t tok0 = (int64_t)(rq.tile0 + first_tile + warp + ATT_WARPS * k) * ATT_TILE;
-            const bool full = have == 3u && tok0 + ATT_TILE <= all_hi && tok0 >= all_lo;
+            const int st = slot * STAGE_BYTES;
+            const uint32_t have = (there >> (2 * slot)) & 3u;
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            const bool full = have == 3u && tok0 <= all_hi - ATT_TILE && tok0 >= all_lo;
 
             // scores
             float s[2][NQ][4] = {};
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
-                const uint8_t* rec = st + gr * REC;
-                uint32_t kw[2][KW], ksc[2];
+                uint32_t kw[2][KW], ksc[2][(D + 127) / 128];                  // scales in pairs of blocks
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int tok = kv_token_of_row(g) + 8 * x;
-                    load_words<KW>(rec + tok * (D / 2) + t4 * (D / 8), kw[x]);
-                    const uint8_t* sc = rec + kv_k_scales(D) + tok * (D / 16) + t4 * (D / 64);
-                    if constexpr (D == 64) ksc[x] = *sc;
-                    else if constexpr (D == 128) ksc[x] = *reinterpret_cast<const uint16_t*>(sc);
-                    else ksc[x] = *reinterpret_cast<const uint32_t*>(sc);
+                    load_words<KW>(at_k + st + gr * REC + x * (8 * D / 2), kw[x]);
+                    const uint8_t* sc = at_ks + st + gr * REC + x * (8 * D / 16);
+                    if constexpr (D == 64) ksc[x][0] = e4m3x2_to_f16x2(*sc);
+                    else if constexpr (D == 128) ksc[x][0] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sc));
+                    else {
+                        const uint32_t four = *reinterpret_cast<const uint32_t*>(sc);
+                        ksc[x][0] = e4m3x2_to_f16x2(four);
+                        ksc[x][(D + 127) / 128 - 1] = e4m3x2_to_f16x2(four >> 16);
+                    }
                 }
 #pragma unroll
                 for (int w = 0; w < KW; ++w) {
@@ -323,9 +354,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         e2m1x8_to_f16(kw[x][w], f[x]);
-                        const uint32_t sc = e4m3x2_to_f16x2(__byte_perm(ksc[x], 0u, 0x1111u * (w >> 1)));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) f[x][i] = mul_f16x2(f[x][i], sc);
+                        for (int i = 0; i < 4; ++i)
+                            f[x][i] = ((w >> 1) & 1) ? mul_f16x2_hi(f[x][i], ksc[x][w >> 2]) : mul_f16x2_lo(f[x][i], ksc[x][w >> 2]);
                     }
 #pragma unroll
                     for (int nq = 0; nq < NQ; ++nq) {
@@ -347,16 +378,14 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float v = s[gr][nq][2 * x + j] * mul[nq][j];
                             if (!full) {
-                                const int64_t tok = tok0 + gr * 16 + 8 * x + kv_token_of_row(g);
-                                const bool in = ((have >> gr) & 1u) && tok <= pos[nq][j] && (a.window == 0 || tok > (int64_t)pos[nq][j] - a.window);
-                                v = in ? v : -INFINITY;
+                                const int tok = tok0 + gr * 16 + 8 * x + kv_token_of_row(g);
+                                const bool in = ((have >> gr) & 1u) && tok <= pos[nq][j] && (a.window == 0 || tok > pos[nq][j] - a.window);
+                                s[gr][nq][2 * x + j] = in ? s[gr][nq][2 * x + j] : -INFINITY;
                             }
-                            s[gr][nq][2 * x + j] = v;
-                            top[nq][j] = fmaxf(top[nq][j], v);
+                            top[nq][j] = fmaxf(top[nq][j], s[gr][nq][2 * x + j]);
                         }
-                raise |= top[nq][0] > m[nq][0] + ATT_SLACK || top[nq][1] > m[nq][1] + ATT_SLACK;
+                raise |= top[nq][0] > m[nq][0] + slack[nq][0] || top[nq][1] > m[nq][1] + slack[nq][1];
             }
             if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
@@ -368,7 +397,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-                        f[j] = v == -INFINITY ? 1.0f : ex2(m[nq][j] - v);
+                        f[j] = m[nq][j] == -INFINITY ? 0.0f : ex2((m[nq][j] - v) * mul[nq][j]);
                         m[nq][j] = v;
                         l[nq][j] *= f[j];
                     }
@@ -381,12 +410,17 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             uint32_t pf[2][NQ][2];                                         // P as B fragments
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
-                const float m0 = m[nq][0] == -INFINITY ? 0.0f : m[nq][0], m1 = m[nq][1] == -INFINITY ? 0.0f : m[nq][1];
+                // 2^(mul s - mul m); a column with nothing so far has only -inf, to which 0 is added
+                const float m0 = m[nq][0] == -INFINITY ? 0.0f : -m[nq][0] * mul[nq][0], m1 = m[nq][1] == -INFINITY ? 0.0f : -m[nq][1] * mul[nq][1];
 #pragma unroll
                 for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float p0 = ex2(s[gr][nq][2 * x] - m0), p1 = ex2(s[gr][nq][2 * x + 1] - m1);
+                        float p0 = ex2(__fmaf_rn(s[gr][nq][2 * x], mul[nq][0], m0)), p1 = ex2(__fmaf_rn(s[gr][nq][2 * x + 1], mul[nq][1], m1));
+                        if (!full) {                                       // masked, also where the factor is zero
+                            if (s[gr][nq][2 * x] == -INFINITY) p0 = 0.0f;
+                            if (s[gr][nq][2 * x + 1] == -INFINITY) p1 = 0.0f;
+                        }
                         l[nq][0] += p0;
                         l[nq][1] += p1;
                         pf[gr][nq][x] = transpose_8x8(pack_f16x2(p0, p1));
@@ -396,19 +430,17 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             // output: dimensions [g * D / 8, + D / 8) of each pair of tokens; byte i of the interleaved words is a dimension
 #pragma unroll
             for (int gr = 0; gr < 2; ++gr) {
-                const uint8_t* rec = st + gr * REC;
                 uint32_t vw[2][2][VW], vsc[2][(D + 127) / 128];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
-                        load_words<VW>(rec + kv_v_codes(D) + (8 * x + kv_token_of_row(2 * t4 + y)) * (D / 2) + g * (D / 16), vw[x][y]);
+                        load_words<VW>(at_v + v_row[y] + st + gr * REC + x * (8 * D / 2), vw[x][y]);
 #pragma unroll
                     for (int b = 0; b < (D + 127) / 128; ++b) {
-                        const int blk = D == 64 ? g >> 1 : (D == 128 ? g : 2 * g + b);
-                        uint32_t sc = *reinterpret_cast<const uint16_t*>(rec + kv_v_scales(D) + blk * 16 + 8 * x + 2 * t4);
+                        uint32_t sc = *reinterpret_cast<const uint16_t*>(at_vs + st + gr * REC + 16 * b + 8 * x);
                         if (!full) {                                       // bytes beyond the context may be anything
-                            const int64_t tok = tok0 + gr * 16 + 8 * x;
+                            const int tok = tok0 + gr * 16 + 8 * x;
                             const bool hv = (have >> gr) & 1u;
                             if (!hv || tok + kv_token_of_row(2 * t4) >= rq.len) sc &= 0xFF00u;
                             if (!hv || tok + kv_token_of_row(2 * t4 + 1) >= rq.len) sc &= 0x00FFu;
@@ -444,6 +476,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+                if (m[nq][j] != -INFINITY) m[nq][j] *= mul[nq][j];           // from here on an exponent of two
                 float v = l[nq][j];
                 v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
                 v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
@@ -503,12 +536,12 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         }
         if (first_tile == 0 && tid == 0 && (p.by_item || !whole)) {
             Piece pc{(int)blockIdx.x, 0, rq.first, h, col0, cols};
-            if (!whole) pc.count = (int)((at + rq.tiles - 1) / share) - (int)blockIdx.x + 1;
+            if (!whole) pc.count = (int)((item_at + per_item - 1) / share) - (int)blockIdx.x + 1;
             p.pieces[p.by_item ? item0 + item : (int)blockIdx.x] = pc;
         }
         __syncthreads();                                                   // buffer free for the next item's ring
-        at += n_tiles;
-        off += n_tiles;
+        at += run;
+        off += run;
     }
 }
 

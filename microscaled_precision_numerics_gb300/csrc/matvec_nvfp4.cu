@@ -16,7 +16,7 @@
 // GEMM scale layout holds for a row of the first band are the four bands' scales of the same four columns, so no
 // scale sector is fetched for a quarter of its bytes.  In a step of 128 values a thread reads 16 bytes of codes from
 // each of its four rows (a quad: 64 contiguous bytes) and one 16-byte piece of scales, through a cp.async
-// ring of its warp's: what keeps HBM busy is bytes in flight, and the ring holds 110 to 147 KB an SM without registers.  It
+// ring of its warp's: what keeps HBM busy is bytes in flight, and the ring holds 74 to 110 KB an SM without registers.  It
 // runs on across the rows that a CTA takes in turn, while x stays where it is.
 // A CTA has 16 warps, WK of them along K for each group of 32 rows: 1 where there are rows enough for every warp of the
 // GPU, which then never wait for each other, up to all 16 where there are few.  Partial sums meet in shared memory,
@@ -35,7 +35,7 @@ constexpr int MV_SLOT = 4 * 512 + 256;                // a warp's step in the ri
 constexpr int MV_MAX_SPLIT = 8;                       // CTAs of a cluster
 constexpr int MV_SMEM = 225 * 1024;                   // dynamic shared memory of a CTA, which has its SM to itself
 constexpr int MV_WARPS = 16;
-__host__ __device__ constexpr int mv_stages(int NQ) { return NQ == 1 ? 4 : 3; }
+__host__ __device__ constexpr int mv_stages(int NQ) { return NQ == 1 ? 3 : 2; }
 __host__ __device__ constexpr int mv_ring(int NQ) { return MV_WARPS * mv_stages(NQ) * MV_SLOT; }
 // Bytes of a staged token: a stretch of `steps` steps, and 64 so that odd and even tokens lie on both bank halves.
 __host__ __device__ constexpr int mv_row_bytes(int steps) { return steps * MV_STEP * 2 + 64; }
@@ -325,10 +325,10 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
 }
 
 // The split of the work: warps along K and CTAs of a cluster along K, for one CTA an SM, such that the busiest warp has
-// the least to do, in steps.  Counted besides the steps: half a step for a meeting of a CTA's warps, two for one of a
+// the least to do, in steps.  Counted besides the steps: one for a meeting of a CTA's warps, two for one of a
 // cluster, the staging of x by its size.  clusters[c] is how many clusters of c CTAs the device runs at once (the SMs
 // of a cluster share a GPC, so it is below SMs / c).
-constexpr double MV_STAGING = 0.008, MV_MEET = 0.5, MV_MEET_CLUSTER = 2.0;
+constexpr double MV_STAGING = 0.008, MV_MEET = 1.0, MV_MEET_CLUSTER = 2.0;
 MvPlan mv_plan(int NQ, const MatvecArgs& a, const int (&clusters)[MV_MAX_SPLIT + 1], int& ctas_k) {
     const int steps = (int)((a.K + MV_STEP - 1) / MV_STEP), warps = MV_WARPS;
     const int64_t groups = (a.N + 127) / 128 * 4;
