@@ -31,11 +31,11 @@ namespace {
 constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_TILE = 32;                 // tokens of a warp's step: two records
-constexpr int ATT_ITEM_COST = 8;             // what an item costs besides its tiles, in tiles
-constexpr int ATT_MIN_SHARE = 12;            // smallest share of a CTA: an item's fixed cost and one step a warp
+constexpr int ATT_ITEM_COST = 12;             // what an item costs besides its tiles, in tiles
+constexpr int ATT_MIN_SHARE = 8;             // smallest share of a CTA: two steps a warp
 constexpr float ATT_SLACK = 8.0f;            // the running maximum may lag by 2^8 (P stays below 2^8 in FP16)
 
-__host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 6 : (D == 128 ? 3 : 2); }
+__host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 4 : 2; }
 // Resident CTAs per SM: by registers (O holds D / 4 * NQ of them) and by shared memory.
 __host__ __device__ constexpr int att_ctas(int D, int NQ) { return D == 256 ? (NQ == 1 ? 3 : 2) : (NQ == 1 ? 4 : (NQ == 2 ? 3 : 2)); }
 __host__ __device__ constexpr int att_ring_bytes(int D) { return ATT_WARPS * att_stages(D) * 2 * kv_record_bytes(D); }
@@ -236,14 +236,17 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                 there = (there & ~(3u << (2 * in_slot))) | (got << (2 * in_slot));
                 const uint32_t dst = ring_u32 + in_slot * STAGE_BYTES + 16 * lane;
                 const uint8_t *p0 = a.cache + a0 + 16 * lane, *p1 = a.cache + a1 + 16 * (lane - CHUNKS);
+                // 16-byte pieces lane + 32 i of the two records
+                if (got == 3u) {
 #pragma unroll
-                for (int i = 0; i < (2 * CHUNKS + 31) / 32; ++i) {                // 16-byte pieces lane + 32 i of the two records
-                    if (32 * i + 32 <= CHUNKS) {
-                        if (got & 1u) copy_async_16(dst + 512 * i, p0 + 512 * i);
-                    } else if (32 * i >= CHUNKS) {
-                        if ((got & 2u) && (32 * i + 32 <= 2 * CHUNKS || lane < 2 * CHUNKS - 32 * i)) copy_async_16(dst + 512 * i, p1 + 512 * i);
-                    } else {
-                        if (got & (lane < CHUNKS - 32 * i ? 1u : 2u)) copy_async_16(dst + 512 * i, (lane < CHUNKS - 32 * i ? p0 : p1) + 512 * i);
+                    for (int i = 0; i < (2 * CHUNKS + 31) / 32; ++i) {
+                        const uint8_t* from = 32 * i + 32 <= CHUNKS ? p0 : (32 * i >= CHUNKS || lane >= CHUNKS - 32 * i ? p1 : p0);
+                        if (32 * i + 32 <= 2 * CHUNKS || lane < 2 * CHUNKS - 32 * i) copy_async_16(dst + 512 * i, from + 512 * i);
+                    }
+                } else if (got != 0u) {
+                    for (int i = 0; 32 * i + lane < 2 * CHUNKS; ++i) {
+                        const bool second = 32 * i + lane >= CHUNKS;
+                        if (got & (second ? 2u : 1u)) copy_async_16(dst + 512 * i, (second ? p1 : p0) + 512 * i);
                     }
                 }
             }
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             for (int k = 0; k < D / 8; ++k) qf[nq][k >> 1][k & 1] = pack_f16x2(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                mul[nq][j] = __shfl_sync(0xFFFFFFFFu, fabsf(c), 4 * (2 * t4 + j));
+                mul[nq][j] = __shfl_sync(0xFFFFFFFFu, c == 0.0f ? FLT_MIN : fabsf(c), 4 * (2 * t4 + j));      // not 0: 0 * -inf
                 slack[nq][j] = fminf(ATT_SLACK / mul[nq][j], 1e30f);
                 const int cj = col0 + nq * 8 + 2 * t4 + j;
                 pos[nq][j] = cj < cols ? base_pos + (int)divu32((uint32_t)cj, p.dv_group) : -1;
@@ -366,7 +369,24 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                 }
             }
 
-            // softmax: fragment row g of half x of record gr is token gr * 16 + 8 x + token_of_row(g)
+            // fragment row g of half x of record gr is token gr * 16 + 8 x + token_of_row(g)
+            if (!full) {
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int tok = tok0 + gr * 16 + 8 * x + kv_token_of_row(g);
+                        const bool there_is = (have >> gr) & 1u;
+#pragma unroll
+                        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const bool in = there_is && tok <= pos[nq][j] && (a.window == 0 || tok > pos[nq][j] - a.window);
+                                if (!in) s[gr][nq][2 * x + j] = -INFINITY;
+                            }
+                    }
+            }
+            // softmax
             float top[NQ][2];
             bool raise = false;
 #pragma unroll
@@ -378,11 +398,6 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                     for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            if (!full) {
-                                const int tok = tok0 + gr * 16 + 8 * x + kv_token_of_row(g);
-                                const bool in = ((have >> gr) & 1u) && tok <= pos[nq][j] && (a.window == 0 || tok > pos[nq][j] - a.window);
-                                s[gr][nq][2 * x + j] = in ? s[gr][nq][2 * x + j] : -INFINITY;
-                            }
                             top[nq][j] = fmaxf(top[nq][j], s[gr][nq][2 * x + j]);
                         }
                 raise |= top[nq][0] > m[nq][0] + slack[nq][0] || top[nq][1] > m[nq][1] + slack[nq][1];
@@ -416,11 +431,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                 for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        float p0 = ex2(__fmaf_rn(s[gr][nq][2 * x], mul[nq][0], m0)), p1 = ex2(__fmaf_rn(s[gr][nq][2 * x + 1], mul[nq][1], m1));
-                        if (!full) {                                       // masked, also where the factor is zero
-                            if (s[gr][nq][2 * x] == -INFINITY) p0 = 0.0f;
-                            if (s[gr][nq][2 * x + 1] == -INFINITY) p1 = 0.0f;
-                        }
+                        const float p0 = ex2(__fmaf_rn(s[gr][nq][2 * x], mul[nq][0], m0)), p1 = ex2(__fmaf_rn(s[gr][nq][2 * x + 1], mul[nq][1], m1));
                         l[nq][0] += p0;
                         l[nq][1] += p1;
                         pf[gr][nq][x] = transpose_8x8(pack_f16x2(p0, p1));
@@ -437,17 +448,24 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                     for (int y = 0; y < 2; ++y)
                         load_words<VW>(at_v + v_row[y] + st + gr * REC + x * (8 * D / 2), vw[x][y]);
 #pragma unroll
-                    for (int b = 0; b < (D + 127) / 128; ++b) {
-                        uint32_t sc = *reinterpret_cast<const uint16_t*>(at_vs + st + gr * REC + 16 * b + 8 * x);
-                        if (!full) {                                       // bytes beyond the context may be anything
-                            const int tok = tok0 + gr * 16 + 8 * x;
-                            const bool hv = (have >> gr) & 1u;
-                            if (!hv || tok + kv_token_of_row(2 * t4) >= rq.len) sc &= 0xFF00u;
-                            if (!hv || tok + kv_token_of_row(2 * t4 + 1) >= rq.len) sc &= 0x00FFu;
-                        }
-                        vsc[x][b] = e4m3x2_to_f16x2(sc);
+                    for (int b = 0; b < (D + 127) / 128; ++b)
+                        vsc[x][b] = *reinterpret_cast<const uint16_t*>(at_vs + st + gr * REC + 16 * b + 8 * x);
+                }
+                if (!full) {                                               // bytes beyond the context may be anything
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int tok = tok0 + gr * 16 + 8 * x;
+                        const bool hv = (have >> gr) & 1u;
+                        const uint32_t keep = (hv && tok + kv_token_of_row(2 * t4) < rq.len ? 0x00FFu : 0u) |
+                                              (hv && tok + kv_token_of_row(2 * t4 + 1) < rq.len ? 0xFF00u : 0u);
+#pragma unroll
+                        for (int b = 0; b < (D + 127) / 128; ++b) vsc[x][b] &= keep;
                     }
                 }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int b = 0; b < (D + 127) / 128; ++b) vsc[x][b] = e4m3x2_to_f16x2(vsc[x][b]);
 #pragma unroll
                 for (int w = 0; w < VW; ++w) {
                     uint32_t f[2][2][4];                                   // [half][even / odd dimension][byte]
@@ -545,78 +563,86 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
     }
 }
 
-// Join of the pieces of an item, in the order of the CTAs.  A CTA takes the columns y, y + gridDim.y, ... of piece x.
-// With one column a CTA (few items, many pieces) its warps share the pieces; else each warp takes columns.
-template <int D>
-__global__ void __launch_bounds__(256) kv_attention_join_kernel(const __grid_constant__ AttParams p, int columns) {
-    constexpr int V = D / 32;
+// Join of the pieces of an item, in the order of the CTAs: a warp takes a column, or with SHARED (few items, many pieces) all
+// warps of a CTA share a column's pieces.  A lane holds D / 32 neighbouring dimensions.
+constexpr int JOIN_THREADS = 256;
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(JOIN_THREADS) kv_attention_join_kernel(const __grid_constant__ AttParams p, int columns) {
+    constexpr int V = D / 32, WARPS = JOIN_THREADS / 32, UB = 8;             // UB pieces in flight
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Piece pc = p.pieces[blockIdx.x];
     if (pc.count <= 0) return;
     const KvAttentionArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool one = gridDim.y == (unsigned)columns;
-    __shared__ float s_o[8][D], s_ml[8][2];
-    for (int c = one ? (int)blockIdx.y : warp; c < columns; c += one ? columns : 8) {
-        const int col = pc.col0 + c;
-        if (col >= pc.cols) break;
-        float M = -INFINITY, L = 0.0f, o[V] = {};
-        const int w0 = one ? warp : 0, dw = one ? 8 : 1;
-        for (int k0 = w0; k0 < pc.count; k0 += 4 * dw) {
-            float x[4][V], ml[4][2];
+    const int c = SHARED ? (int)blockIdx.y : (int)blockIdx.y * WARPS + warp, col = pc.col0 + c;
+    if (col >= pc.cols) return;
+    float M = -INFINITY, L = 0.0f, o[V] = {};
+    constexpr int step = SHARED ? WARPS : 1;
+    for (int k0 = SHARED ? warp : 0; k0 < pc.count; k0 += UB * step) {
+        float x[UB][V], ml[UB][2];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int k = k0 + u * dw;
-                ml[u][0] = -INFINITY;
-                ml[u][1] = 0.0f;
+        for (int u = 0; u < UB; ++u) {
+            const int k = k0 + u * step;
+            const int64_t at = ((int64_t)(pc.first_cta + k) * 2 + (k == 0 ? 1 : 0)) * columns + c;
+            const bool in = k < pc.count;
+            const float2 q = in ? *reinterpret_cast<const float2*>(p.part_ml + at * 2) : make_float2(-INFINITY, 0.0f);
+            ml[u][0] = q.x;
+            ml[u][1] = q.y;
+            const float* src = p.part_o + at * D + lane * V;
 #pragma unroll
-                for (int v = 0; v < V; ++v) x[u][v] = 0.0f;
-                if (k < pc.count) {
-                    const int64_t at = ((int64_t)(pc.first_cta + k) * 2 + (k == 0 ? 1 : 0)) * columns + c;
-                    ml[u][0] = p.part_ml[at * 2];
-                    ml[u][1] = p.part_ml[at * 2 + 1];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) x[u][v] = p.part_o[at * D + v * 32 + lane];
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float Mn = fmaxf(M, ml[u][0]);
-                const float f0 = M == -INFINITY ? 0.0f : ex2(M - Mn), f1 = ml[u][0] == -INFINITY ? 0.0f : ex2(ml[u][0] - Mn);
-                L = __fmaf_rn(L, f0, ml[u][1] * f1);
-#pragma unroll
-                for (int v = 0; v < V; ++v) o[v] = __fmaf_rn(o[v], f0, x[u][v] * f1);
-                M = Mn;
+            for (int v = 0; v < V; v += 2) {
+                const float2 f = in ? *reinterpret_cast<const float2*>(src + v) : make_float2(0.0f, 0.0f);
+                x[u][v] = f.x;
+                x[u][v + 1] = f.y;
             }
         }
-        if (one) {
+        float Mn = M;
 #pragma unroll
-            for (int v = 0; v < V; ++v) s_o[warp][v * 32 + lane] = o[v];
-            if (lane == 0) {
-                s_ml[warp][0] = M;
-                s_ml[warp][1] = L;
-            }
-            __syncthreads();
-            if (warp != 0) return;
-            M = -INFINITY;
-            for (int w = 0; w < 8; ++w) M = fmaxf(M, s_ml[w][0]);
-            L = 0.0f;
+        for (int u = 0; u < UB; ++u) Mn = fmaxf(Mn, ml[u][0]);
+        const float f0 = M == -INFINITY ? 0.0f : ex2(M - Mn);
+        L *= f0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = 0.0f;
-            for (int w = 0; w < 8; ++w) {
-                const float f = s_ml[w][0] == -INFINITY ? 0.0f : ex2(s_ml[w][0] - M);
-                L = __fmaf_rn(s_ml[w][1], f, L);
+        for (int v = 0; v < V; ++v) o[v] *= f0;
 #pragma unroll
-                for (int v = 0; v < V; ++v) o[v] = __fmaf_rn(s_o[w][v * 32 + lane], f, o[v]);
-            }
+        for (int u = 0; u < UB; ++u) {
+            const float f = ml[u][0] == -INFINITY ? 0.0f : ex2(ml[u][0] - Mn);
+            L = __fmaf_rn(ml[u][1], f, L);
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = __fmaf_rn(x[u][v], f, o[v]);
         }
-        const int i = (int)divu32((uint32_t)col, p.dv_group), hq = pc.kv_head * a.group + (col - i * a.group);
-        const int64_t t = pc.token0 + i;
-        const float f = L == 0.0f ? 0.0f : __ldg(a.s_v + pc.kv_head) / L;
-#pragma unroll
-        for (int v = 0; v < V; ++v) a.out[t * a.o_token + (int64_t)hq * a.o_head + v * 32 + lane] = (uint16_t)pack_bf16x2(o[v] * f, 0.0f);
-        if (a.lse && lane == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
+        M = Mn;
     }
+    if constexpr (SHARED) {
+        __shared__ float s_o[WARPS][D], s_ml[WARPS][2];
+#pragma unroll
+        for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = o[v];
+        if (lane == 0) {
+            s_ml[warp][0] = M;
+            s_ml[warp][1] = L;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+        M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_ml[w][0]);
+        L = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const float f = s_ml[w][0] == -INFINITY ? 0.0f : ex2(s_ml[w][0] - M);
+            L = __fmaf_rn(s_ml[w][1], f, L);
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = __fmaf_rn(s_o[w][lane * V + v], f, o[v]);
+        }
+    }
+    const int i = (int)divu32((uint32_t)col, p.dv_group), hq = pc.kv_head * a.group + (col - i * a.group);
+    const int64_t t = pc.token0 + i;
+    const float f = L == 0.0f ? 0.0f : __ldg(a.s_v + pc.kv_head) / L;
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.out + t * a.o_token + (int64_t)hq * a.o_head + lane * V);
+#pragma unroll
+    for (int v = 0; v < V; v += 2) out[v >> 1] = pack_bf16x2(o[v] * f, o[v + 1] * f);
+    if (a.lse && lane == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
 }
 
 constexpr int att_max_columns(int D) { return D == 256 ? 16 : 32; }
@@ -643,15 +669,17 @@ cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // the join starts while the last CTAs finish and waits for them on the device
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)p.n_pieces, p.by_item && items * 8 <= ctas ? 8 * NQ : 1);
-    cfg.blockDim = dim3(256);
+    const bool shared = items * 8 <= ctas;
+    cfg.gridDim = dim3((unsigned)p.n_pieces, shared ? 8 * NQ : 8 * NQ * 32 / JOIN_THREADS);
+    cfg.blockDim = dim3(JOIN_THREADS);
     cfg.stream = stream;
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D>, p, 8 * NQ);
+    return shared ? cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, true>, p, 8 * NQ)
+                  : cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, false>, p, 8 * NQ);
 }
 
 template <int D>
