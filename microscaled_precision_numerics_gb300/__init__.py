@@ -523,49 +523,68 @@ MX_KV_MAX_REQUESTS = 4096
 MX_MATVEC_MAX_TOKENS = 64
 
 
-def _ptrs(*tensors):
-    """The device pointers of the tensors (None stays None), all on the current device: _p() for the calls of a
-    generation step, which are many and short."""
-    if not tensors[0].is_cuda:
-        _p(tensors[0])                                  # raises
-    cur = torch.cuda.current_device()
-    return [None if t is None else t.data_ptr() if t.get_device() == cur else _p(t) for t in tensors]
+# The calls of a generation step are many and short, and reading a tensor's attributes is what their checks cost:
+# each tensor is looked at once, for all checks and for its pointer.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _typed(fn: str, name: str, t, dtype, n: int):
-    """Raise unless t is a contiguous tensor of this type with at least n elements."""
+def _device_of(t) -> int:
+    """The current device, on which all tensors of the call must be; -1 for a tensor that is not on a CUDA device, which
+    _stream_on refuses once the other arguments are found in order."""
+    return _current_device() if t.is_cuda else -1
+
+
+def _stream_on(cur: int, stream):
+    if cur < 0:
+        raise ValueError("mxnum operates on CUDA tensors only (no CPU path)")
+    return _stream(stream) if stream is not None or _raw_stream is None else _raw_stream(cur)
+
+
+def _refuse(fn: str, name: str, t, dtype, n: int):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{fn}: {name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
-    if t.numel() < n or not t.is_contiguous():
-        _need(fn, name, t, n * t.element_size())
+    _need(fn, name, t, n * t.element_size())
+    _p(t)
 
 
-def _block_table(fn: str, t, requests: int):
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] < requests or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{fn}: block_table must be int32 [requests, pages] with unit column stride")
-    return t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _array(fn: str, name: str, t, dtype, n: int, cur: int) -> int:
+    """The pointer of a contiguous array of at least n elements of this type on device cur."""
+    if t.dtype is not dtype or t.numel() < n or t.get_device() != cur or not t.is_contiguous():
+        _refuse(fn, name, t, dtype, n)
+    return t.data_ptr()
 
 
-def _kv_cache(fn: str, cache, s_k, s_v):
-    """(pages, page size, kv heads, head dimension) of a cache [pages, kv heads, page_size / 16, 18 * head_dim]."""
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or cache.shape[3] % 18 or not cache.is_contiguous():
+def _block_table(fn: str, t, requests: int, cur: int):
+    """(pointer, width, row stride) of a block table int32 [requests, pages]."""
+    if t.dtype is not torch.int32 or t.dim() != 2:
+        raise ValueError(f"{fn}: block_table must be int32 [requests, pages]")
+    (rows, width), (row, col) = t.shape, t.stride()
+    if rows < requests or (width > 1 and col != 1):
+        raise ValueError(f"{fn}: block_table must be int32 [{requests}, pages] with unit column stride, got {tuple(t.shape)}")
+    return t.data_ptr() if t.get_device() == cur else _p(t), width, row if rows > 1 else width
+
+
+def _kv_cache(fn: str, cache, cur: int):
+    """(pointer, pages, page size, kv heads, head dimension) of a cache [pages, kv heads, page_size / 16, 18 * head_dim]."""
+    if cache.dtype is not torch.uint8 or cache.dim() != 4 or not cache.is_contiguous() or cache.shape[3] % 18:
         raise ValueError(f"{fn}: cache must be a contiguous uint8 [pages, kv_heads, page_size / 16, 18 * head_dim]")
     pages, heads, groups, record = cache.shape
-    _typed(fn, "s_k", s_k, torch.float32, heads)
-    _typed(fn, "s_v", s_v, torch.float32, heads)
-    return pages, 16 * groups, heads, record // 18
+    return cache.data_ptr() if cache.get_device() == cur else _p(cache), pages, 16 * groups, heads, record // 18
 
 
-def _heads_bf16(fn: str, name: str, t, heads, dim: int, tokens=None):
-    """A BF16 [tokens, heads, dim] view with unit element stride; its token and head strides."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads) or (
-            tokens is not None and t.shape[0] != tokens) or t.stride(2) != 1:
+def _heads_bf16(fn: str, name: str, t, heads, dim: int, tokens, cur: int):
+    """(pointer, token stride, head stride, tokens, heads) of a BF16 [tokens, heads, dim] view with unit element stride."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != dim or stride[2] != 1 or (
+            heads is not None and shape[1] != heads) or (tokens is not None and shape[0] != tokens):
         raise ValueError(f"{fn}: {name} must be bfloat16 [{tokens if tokens is not None else 'tokens'}, "
                          f"{heads if heads is not None else 'heads'}, {dim}] with unit element stride, got "
-                         f"{t.dtype} {tuple(t.shape)}")
-    T, H = t.shape[0], t.shape[1]
-    head = t.stride(1) if H > 1 else dim
-    return (t.stride(0) if T > 1 else H * head), head
+                         f"{t.dtype} {tuple(shape)}")
+    T, H, _ = shape
+    head = stride[1] if H > 1 else dim
+    return t.data_ptr() if t.get_device() == cur else _p(t), stride[0] if T > 1 else H * head, head, T, H
 
 
 def kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
@@ -579,85 +598,82 @@ def kv_attention_workspace_bytes(head_dim: int) -> int:
 def mx_kv_slots(seq_lens, new_lens, page_size: int, block_table, free_pages, free_count, q_start, total_lens, slots,
                 positions, free_left, unplaced, stream=None):
     """Page and slot maps of a step (see include/mxnum_generate.h).  total_lens may be seq_lens, free_left may be free_count."""
-    fn, R, T = "mx_kv_slots", seq_lens.numel(), slots.numel()
-    width, row = _block_table(fn, block_table, R)
-    for name, t, n in (("seq_lens", seq_lens, R), ("new_lens", new_lens, R), ("free_pages", free_pages, 0),
-                       ("free_count", free_count, 1), ("q_start", q_start, R + 1), ("total_lens", total_lens, R),
-                       ("slots", slots, T), ("positions", positions, T), ("free_left", free_left, 1),
-                       ("unplaced", unplaced, 1)):
-        _typed(fn, name, t, torch.int32, n)
-    p = _ptrs(seq_lens, new_lens, block_table, free_pages, free_count, q_start, total_lens, slots, positions, free_left, unplaced)
-    _check(fn, lib().mx_kv_slots(p[0], p[1], R, page_size, p[2], width, row, p[3], free_pages.numel(), p[4], p[5], p[6],
-                                 p[7], p[8], T, p[9], p[10], _stream(stream)))
+    fn, i32, R, T, F = "mx_kv_slots", torch.int32, seq_lens.numel(), slots.numel(), free_pages.numel()
+    cur = _device_of(seq_lens)
+    table, width, row = _block_table(fn, block_table, R, cur)
+    _check(fn, lib().mx_kv_slots(
+        _array(fn, "seq_lens", seq_lens, i32, R, cur), _array(fn, "new_lens", new_lens, i32, R, cur), R, page_size, table,
+        width, row, _array(fn, "free_pages", free_pages, i32, F, cur), F, _array(fn, "free_count", free_count, i32, 1, cur),
+        _array(fn, "q_start", q_start, i32, R + 1, cur), _array(fn, "total_lens", total_lens, i32, R, cur),
+        _array(fn, "slots", slots, i32, T, cur), _array(fn, "positions", positions, i32, T, cur), T,
+        _array(fn, "free_left", free_left, i32, 1, cur), _array(fn, "unplaced", unplaced, i32, 1, cur),
+        _stream_on(cur, stream)))
 
 
 def mx_nvfp4_kv_append(k, v, slots, s_k, s_v, cache, stream=None):
     """Quantize keys and values [T, kv_heads, head_dim] (BF16, any token and head stride) into the cache at slots [T]."""
-    fn = "mx_nvfp4_kv_append"
-    pages, page, heads, dim = _kv_cache(fn, cache, s_k, s_v)
-    kt, kh = _heads_bf16(fn, "k", k, heads, dim)
-    T = k.shape[0]
-    vt, vh = _heads_bf16(fn, "v", v, heads, dim, T)
-    _typed(fn, "slots", slots, torch.int32, T)
-    p = _ptrs(k, v, slots, s_k, s_v, cache)
-    _check(fn, lib().mx_nvfp4_kv_append(p[0], kt, kh, p[1], vt, vh, p[2], T, p[3], p[4], p[5], pages, page, heads, dim,
-                                        _stream(stream)))
+    fn, cur = "mx_nvfp4_kv_append", _device_of(cache)
+    at, pages, page, heads, dim = _kv_cache(fn, cache, cur)
+    kp, kt, kh, T, _ = _heads_bf16(fn, "k", k, heads, dim, None, cur)
+    vp, vt, vh, _, _ = _heads_bf16(fn, "v", v, heads, dim, T, cur)
+    _check(fn, lib().mx_nvfp4_kv_append(
+        kp, kt, kh, vp, vt, vh, _array(fn, "slots", slots, torch.int32, T, cur), T,
+        _array(fn, "s_k", s_k, torch.float32, heads, cur), _array(fn, "s_v", s_v, torch.float32, heads, cur), at, pages,
+        page, heads, dim, _stream_on(cur, stream)))
 
 
 def mx_nvfp4_kv_gather(cache, slots, s_k, s_v, k, v, stream=None):
     """Read the cached tokens at slots [T] back into k, v [T, kv_heads, head_dim] (BF16, any token and head stride)."""
-    fn = "mx_nvfp4_kv_gather"
-    pages, page, heads, dim = _kv_cache(fn, cache, s_k, s_v)
-    kt, kh = _heads_bf16(fn, "k", k, heads, dim)
-    T = k.shape[0]
-    vt, vh = _heads_bf16(fn, "v", v, heads, dim, T)
-    _typed(fn, "slots", slots, torch.int32, T)
-    p = _ptrs(cache, slots, s_k, s_v, k, v)
-    _check(fn, lib().mx_nvfp4_kv_gather(p[0], pages, page, heads, dim, p[1], T, p[2], p[3], p[4], kt, kh, p[5], vt, vh,
-                                        _stream(stream)))
+    fn, cur = "mx_nvfp4_kv_gather", _device_of(cache)
+    at, pages, page, heads, dim = _kv_cache(fn, cache, cur)
+    kp, kt, kh, T, _ = _heads_bf16(fn, "k", k, heads, dim, None, cur)
+    vp, vt, vh, _, _ = _heads_bf16(fn, "v", v, heads, dim, T, cur)
+    _check(fn, lib().mx_nvfp4_kv_gather(
+        at, pages, page, heads, dim, _array(fn, "slots", slots, torch.int32, T, cur), T,
+        _array(fn, "s_k", s_k, torch.float32, heads, cur), _array(fn, "s_v", s_v, torch.float32, heads, cur), kp, kt, kh,
+        vp, vt, vh, _stream_on(cur, stream)))
 
 
 def mx_nvfp4_kv_attention(q, q_start, seq_lens, block_table, cache, s_k, s_v, scale: float, max_q: int, out, workspace,
                           lse=None, window: int = 0, stream=None):
     """Attention of a step's new tokens q [T, heads, head_dim] over the cache into out (and lse [T, heads], FP32)."""
-    fn = "mx_nvfp4_kv_attention"
-    pages, page, kv_heads, dim = _kv_cache(fn, cache, s_k, s_v)
-    qt, qh = _heads_bf16(fn, "q", q, None, dim)
-    T, heads = q.shape[0], q.shape[1]
-    ot, oh = _heads_bf16(fn, "out", out, heads, dim, T)
+    fn, cur = "mx_nvfp4_kv_attention", _device_of(cache)
+    at, pages, page, kv_heads, dim = _kv_cache(fn, cache, cur)
+    qp, qt, qh, T, heads = _heads_bf16(fn, "q", q, None, dim, None, cur)
+    op, ot, oh, _, _ = _heads_bf16(fn, "out", out, heads, dim, T, cur)
     R = seq_lens.numel()
-    width, row = _block_table(fn, block_table, R)
-    _typed(fn, "seq_lens", seq_lens, torch.int32, R)
-    _typed(fn, "q_start", q_start, torch.int32, R + 1)
-    if lse is not None:
-        _typed(fn, "lse", lse, torch.float32, T * heads)
-    if not workspace.is_contiguous():
-        raise ValueError(f"{fn}: workspace must be contiguous")
-    p = _ptrs(q, q_start, seq_lens, block_table, cache, s_k, s_v, out, lse, workspace)
-    _check(fn, lib().mx_nvfp4_kv_attention(p[0], qt, qh, T, heads, p[1], p[2], R, max_q, p[3], width, row, p[4], pages, page,
-                                           kv_heads, dim, p[5], p[6], scale, window, p[7], ot, oh, p[8], p[9],
-                                           workspace.numel() * workspace.element_size(), _stream(stream)))
+    table, width, row = _block_table(fn, block_table, R, cur)
+    ws = workspace.nbytes
+    if not workspace.is_contiguous() or workspace.get_device() != cur:
+        _need(fn, "workspace", workspace, 0)
+        _p(workspace)
+    _check(fn, lib().mx_nvfp4_kv_attention(
+        qp, qt, qh, T, heads, _array(fn, "q_start", q_start, torch.int32, R + 1, cur),
+        _array(fn, "seq_lens", seq_lens, torch.int32, R, cur), R, max_q, table, width, row, at, pages, page, kv_heads, dim,
+        _array(fn, "s_k", s_k, torch.float32, kv_heads, cur), _array(fn, "s_v", s_v, torch.float32, kv_heads, cur), scale,
+        window, op, ot, oh, None if lse is None else _array(fn, "lse", lse, torch.float32, T * heads, cur),
+        workspace.data_ptr(), ws, _stream_on(cur, stream)))
 
 
 def mx_nvfp4_matvec(x, q, s, s2, s2_scope: int, y, stream=None):
     """y = s2 * x @ W^T for x BF16 [M, K] (M <= MX_MATVEC_MAX_TOKENS, any row stride) and W given as NVFP4 codes q [N, K/2],
     GEMM-layout scales s and FP32 second-level scales s2; y BF16 or FP32 [M, N] (any row stride)."""
-    fn = "mx_nvfp4_matvec"
+    fn, u8 = "mx_nvfp4_matvec", torch.uint8
     x = _bf16_bits(x)
-    M, K = x.shape
-    if q.dim() != 2 or 2 * q.shape[1] != K:
-        raise ValueError(f"{fn}: q must be [N, {K // 2}], got {tuple(q.shape)}")
-    N = q.shape[0]
-    if y.dtype not in (torch.bfloat16, torch.float32):
+    cur = _device_of(x)
+    (M, K), qs, ys, y_step, fp32 = x.shape, q.shape, y.shape, y.stride(), y.dtype is torch.float32
+    if len(qs) != 2 or 2 * qs[1] != K:
+        raise ValueError(f"{fn}: q must be [N, {K // 2}], got {tuple(qs)}")
+    N = qs[0]
+    if not fp32 and y.dtype is not torch.bfloat16:
         raise TypeError(f"{fn}: y must be bfloat16 or float32")
-    if y.shape[0] != M or y.shape[1] != N or (N > 1 and y.stride(1) != 1):
+    if len(ys) != 2 or ys[0] != M or ys[1] != N or (N > 1 and y_step[1] != 1):
         raise ValueError(f"{fn}: y must be [{M}, {N}] with unit column stride")
-    _need(fn, "q", q, N * K // 2)
-    _need(fn, "s", s, (N + 127) // 128 * ((K // 16 + 3) // 4) * 512)
-    _typed(fn, "s2", s2, torch.float32, _alpha_count(s2_scope, N))
-    p = _ptrs(x, q, s, s2, y)
-    _check(fn, lib().mx_nvfp4_matvec(p[0], x.stride(0) if M > 1 else K, p[1], p[2], p[3], s2_scope, M, N, K, p[4],
-                                     y.stride(0) if M > 1 else N, int(y.dtype == torch.float32), _stream(stream)))
+    _check(fn, lib().mx_nvfp4_matvec(
+        x.data_ptr() if x.get_device() == cur else _p(x), x.stride(0) if M > 1 else K,
+        _array(fn, "q", q, u8, N * K // 2, cur), _array(fn, "s", s, u8, (N + 127) // 128 * ((K // 16 + 3) // 4) * 512, cur),
+        _array(fn, "s2", s2, torch.float32, _alpha_count(s2_scope, N), cur), s2_scope, M, N, K,
+        y.data_ptr() if y.get_device() == cur else _p(y), y_step[0] if M > 1 else N, fp32, _stream_on(cur, stream)))
 
 
 def mx_count_mismatch(x, y, count, stream=None):
