@@ -20,7 +20,7 @@ namespace {
 //
 // Two exclusive sums over the requests (tokens and pages) and then independent look-ups: a few kilobytes, bound by
 // latency.  Every CTA of the one cluster sums all requests for itself (R / 1024 steps a thread) rather
-// than wait for another launch; the outputs are shared out afterwards.
+// than wait for another launch; the outputs are shared out afterwards, each thread's look-ups side by side.
 // ------------------------------------------------------------------------------------------------
 constexpr int SLOT_THREADS = 1024;
 
@@ -29,6 +29,7 @@ struct SlotArgs {
     const int32_t* new_lens;
     int R;
     uint32_t page;
+    DivU32 dv_page;
     int32_t* table;
     int64_t width, stride;
     const int32_t* free_pages;
@@ -53,14 +54,18 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Largest i in [0, n) with v[i] <= x (v[0] = 0 <= x, v non-decreasing).
-__device__ __forceinline__ int last_not_above(const int* v, int n, int x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (v[mid] <= x) lo = mid; else hi = mid;
+// For U values x: the largest i in [0, n) with v[i] <= x (v[0] = 0, v non-decreasing), the searches side by side.
+template <int U>
+__device__ __forceinline__ void last_not_above(const int* v, int n, const int (&x)[U], int (&at)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) at[u] = 0;
+    for (int span = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; span > 0; span >>= 1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int next = at[u] + span;
+            if (next < n && v[next] <= x[u]) at[u] = next;
+        }
     }
-    return lo;
 }
 
 __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a) {
@@ -76,17 +81,18 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
     const uint32_t P = a.page;
     const int64_t n_free = max64(0, min64(__ldg(a.free_count), a.free_capacity));
 
-    auto lengths = [&](int r, int& seq, int& fresh, int& pages) {
-        seq = max(0, a.seq_lens[r]);
-        fresh = max(0, a.new_lens[r]);
-        const int64_t had = ((int64_t)seq + P - 1) / P, want = ((int64_t)seq + fresh + P - 1) / P;
-        pages = (int)max64(0, min64(want, a.width) - had);
+    auto meet = [&]() {                        // of the cluster, or of the one CTA
+        if (cluster_size() > 1) cluster_sync();
+        else __syncthreads();
     };
     int2 sum = make_int2(0, 0);
     for (int r = r0; r < min(a.R, r0 + per); ++r) {
-        int seq, fresh, pages;
-        lengths(r, seq, fresh, pages);
+        const int seq = max(0, a.seq_lens[r]), fresh = max(0, a.new_lens[r]);
+        const uint32_t had = divu32((uint32_t)seq + P - 1, a.dv_page), want = divu32((uint32_t)seq + (uint32_t)fresh + P - 1, a.dv_page);
+        const int pages = (int)max64(0, min64(want, a.width) - had);
         s_seq[r] = seq;
+        s_start[r] = fresh;                    // for the moment
+        s_pages[r] = pages;
         sum.x += fresh;
         sum.y += pages;
     }
@@ -101,14 +107,13 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
     }
     if (lane == 31) s_warp[wid] = incl;
     __syncthreads();
-    int2 run = make_int2(incl.x - sum.x, incl.y - sum.y);
-    for (int w = 0; w < wid; ++w) {
-        run.x += s_warp[w].x;
-        run.y += s_warp[w].y;
-    }
+    // the warps' sums before this one's
+    int2 before = lane < wid ? s_warp[lane] : make_int2(0, 0);
+    before.x = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)before.x);
+    before.y = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)before.y);
+    int2 run = make_int2(before.x + incl.x - sum.x, before.y + incl.y - sum.y);
     for (int r = r0; r < min(a.R, r0 + per); ++r) {
-        int seq, fresh, pages;
-        lengths(r, seq, fresh, pages);
+        const int fresh = s_start[r], pages = s_pages[r];
         s_start[r] = run.x;
         s_pages[r] = run.y;
         run.x += fresh;
@@ -120,8 +125,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
     }
     // every read of seq_lens and free_count is done before any CTA writes total_lens or free_left, which
     // may be the same arrays
-    __syncthreads();
-    cluster_sync();
+    meet();
 
     const int nthr = SLOT_THREADS * (int)cluster_size(), me = (int)cluster_rank() * SLOT_THREADS + tid;
     const int tokens = s_start[a.R], fresh_pages = s_pages[a.R];
@@ -129,33 +133,48 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
         a.q_start[r] = s_start[r];
         if (r < a.R) a.total_lens[r] = s_seq[r] + (s_start[r + 1] - s_start[r]);
     }
+    auto had_of = [&](int r) { return divu32((uint32_t)s_seq[r] + P - 1, a.dv_page); };
     for (int k = me; k < fresh_pages; k += nthr) {
-        const int r = last_not_above(s_pages, a.R, k);
-        const int64_t col = ((int64_t)s_seq[r] + P - 1) / P + (k - s_pages[r]);
-        if (col < a.width) a.table[r * a.stride + col] = k < n_free ? __ldg(a.free_pages + (n_free - 1 - k)) : -1;
+        const int x[1] = {k};
+        int r[1];
+        last_not_above(s_pages, a.R, x, r);
+        const int64_t col = (int64_t)had_of(r[0]) + (k - s_pages[r[0]]);
+        if (col < a.width) a.table[r[0] * a.stride + col] = k < n_free ? __ldg(a.free_pages + (n_free - 1 - k)) : -1;
     }
     int placed = 0;
-    for (int64_t t = me; t < a.max_tokens; t += nthr) {
-        int slot = -1, pos = -1;
-        if (t < tokens) {
-            const int r = last_not_above(s_start, a.R, (int)t);
-            pos = s_seq[r] + ((int)t - s_start[r]);
-            const int64_t col = (uint32_t)pos / P, had = ((int64_t)s_seq[r] + P - 1) / P;
-            int page = -1;
-            if (pos >= 0 && col < a.width) {
-                if (col < had) {
-                    page = a.table[r * a.stride + col];               // an older page: not written by this call
-                } else {
-                    const int64_t k = s_pages[r] + (col - had);
-                    if (k < n_free) page = __ldg(a.free_pages + (n_free - 1 - k));
+    constexpr int U = 4;                       // tokens of a thread looked up side by side
+    for (int64_t t0 = me; t0 < a.max_tokens; t0 += (int64_t)U * nthr) {
+        int x[U], r[U], pos[U], page[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = (int)min64(t0 + (int64_t)u * nthr, INT32_MAX);
+        if (x[0] < tokens) last_not_above(s_start, a.R, x, r);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            pos[u] = page[u] = -1;
+            if (x[u] < tokens) {
+                pos[u] = s_seq[r[u]] + (x[u] - s_start[r[u]]);
+                const uint32_t col = divu32((uint32_t)pos[u], a.dv_page), had = had_of(r[u]);
+                if (pos[u] >= 0 && col < a.width) {
+                    if (col < had) {
+                        page[u] = a.table[r[u] * a.stride + col];       // an older page: not written by this call
+                    } else {
+                        const int64_t k = s_pages[r[u]] + (int64_t)(col - had);
+                        if (k < n_free) page[u] = __ldg(a.free_pages + (n_free - 1 - k));
+                    }
                 }
             }
-            const int64_t s = (int64_t)page * P + (uint32_t)pos % P;
-            if (page >= 0 && s <= INT32_MAX) slot = (int)s;
-            placed += slot >= 0;
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t0 + (int64_t)u * nthr;
+            if (t >= a.max_tokens) break;
+            const uint32_t off = (uint32_t)pos[u] - divu32((uint32_t)pos[u], a.dv_page) * P;
+            const int64_t s = (int64_t)page[u] * P + off;
+            const int slot = page[u] >= 0 && s <= INT32_MAX ? (int)s : -1;
+            placed += slot >= 0;
+            a.slots[t] = slot;
+            a.positions[t] = pos[u];
+        }
     }
     placed = __reduce_add_sync(0xFFFFFFFFu, placed);
     if (lane == 0) s_placed[wid] = placed;
@@ -164,7 +183,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
         placed = __reduce_add_sync(0xFFFFFFFFu, s_placed[lane]);
         if (lane == 0) s_total_placed = placed;
     }
-    cluster_sync();                                                     // every CTA's count is in its shared memory
+    meet();                                                             // every CTA's count is in its shared memory
     if (me == 0) {
         int all = 0;
         const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&s_total_placed);
@@ -178,12 +197,15 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
         *a.unplaced = tokens - all;
         *a.free_left = (int)max64(0, n_free - fresh_pages);
     }
-    cluster_sync();                                                     // nobody leaves while CTA 0 reads its count
+    meet();                                                             // nobody leaves while CTA 0 reads its count
 }
 
 // ------------------------------------------------------------------------------------------------
 // Write and read of cached tokens: one thread per 16-element block, as the quantizers and dequantizers of
 // the framework, with the same arithmetic and S per head.  Both are bound by memory (2.5625 bytes a value).
+// A warp holds the D / 16 blocks of neighbouring tokens of one head, so that the single bytes of the V scales, whose
+// neighbours in memory are other tokens' of the same block, leave it merged by sectors (4 tokens a sector for D = 128
+// instead of one).  Grid: tokens, heads, K or V; no index is divided.
 // ------------------------------------------------------------------------------------------------
 
 // The record of (slot, head), or null when the slot is outside the cache.
@@ -196,16 +218,16 @@ __device__ __forceinline__ T* record_of(T* cache, int64_t slot, int h, const KvS
     return cache + rec * kv_record_bytes(c.dim);
 }
 
+template <int D>
 __global__ void __launch_bounds__(256)
 kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_token, int64_t k_head,
                  int64_t v_token, int64_t v_head, const int32_t* __restrict__ slots, int64_t T,
                  const float* __restrict__ s_k, const float* __restrict__ s_v, uint8_t* __restrict__ cache, KvShape c) {
-    const bool is_v = blockIdx.y != 0;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int nb = c.dim / 16, per = nb * c.heads;
-    const int64_t t = i / per;
+    const bool is_v = blockIdx.z != 0;
+    constexpr int nb = D / 16;
+    const int64_t t = (int64_t)blockIdx.x * (256 / nb) + threadIdx.x / nb;
+    const int h = blockIdx.y, b = threadIdx.x % nb;
     if (t >= T) return;
-    const int e = (int)(i - t * per), h = e / nb, b = e - h * nb;
     int token;
     uint8_t* rec = record_of(cache, __ldg(slots + t), h, c, token);
     if (!rec) return;
@@ -236,28 +258,28 @@ kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
         out.x &= 0x88888888u;
         out.y &= 0x88888888u;
     }
-    *reinterpret_cast<uint2*>(rec + (is_v ? kv_v_codes(c.dim) : 0) + token * (c.dim / 2) + b * 8) = out;
-    if (is_v) rec[kv_v_scales(c.dim) + b * 16 + kv_token_of_row(token)] = (uint8_t)bs;
-    else rec[kv_k_scales(c.dim) + token * nb + b] = (uint8_t)bs;
+    *reinterpret_cast<uint2*>(rec + (is_v ? kv_v_codes(D) : 0) + token * (D / 2) + b * 8) = out;
+    if (is_v) rec[kv_v_scales(D) + b * 16 + kv_token_of_row(token)] = (uint8_t)bs;
+    else rec[kv_k_scales(D) + token * nb + b] = (uint8_t)bs;
 }
 
+template <int D>
 __global__ void __launch_bounds__(256)
 kv_gather_kernel(const uint8_t* __restrict__ cache, const int32_t* __restrict__ slots, int64_t T,
                  const float* __restrict__ s_k, const float* __restrict__ s_v, uint16_t* __restrict__ k,
                  uint16_t* __restrict__ v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, KvShape c) {
-    const bool is_v = blockIdx.y != 0;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int nb = c.dim / 16, per = nb * c.heads;
-    const int64_t t = i / per;
+    const bool is_v = blockIdx.z != 0;
+    constexpr int nb = D / 16;
+    const int64_t t = (int64_t)blockIdx.x * (256 / nb) + threadIdx.x / nb;
+    const int h = blockIdx.y, b = threadIdx.x % nb;
     if (t >= T) return;
-    const int e = (int)(i - t * per), h = e / nb, b = e - h * nb;
     uint32_t out[8] = {};
     int token;
     const uint8_t* rec = record_of(cache, __ldg(slots + t), h, c, token);
     if (rec) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(rec + (is_v ? kv_v_codes(c.dim) : 0) + token * (c.dim / 2) + b * 8));
-        const uint32_t bs = __ldg(is_v ? rec + kv_v_scales(c.dim) + b * 16 + kv_token_of_row(token)
-                                       : rec + kv_k_scales(c.dim) + token * nb + b);
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(rec + (is_v ? kv_v_codes(D) : 0) + token * (D / 2) + b * 8));
+        const uint32_t bs = __ldg(is_v ? rec + kv_v_scales(D) + b * 16 + kv_token_of_row(token)
+                                       : rec + kv_k_scales(D) + token * nb + b);
         const float S = __ldg((is_v ? s_v : s_k) + h), f = e4m3_to_f32(bs);
         const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
@@ -288,10 +310,10 @@ cudaError_t launch_kv_slots(const int32_t* seq_lens, const int32_t* new_lens, in
                                     (3 * (int)KV_MAX_REQUESTS + 2) * (int)sizeof(int));
     });
     if (e != cudaSuccess) return e;
-    const SlotArgs a{seq_lens, new_lens, (int)R, (uint32_t)page, table, width, stride, free_pages, free_capacity,
+    const SlotArgs a{seq_lens, new_lens, (int)R, (uint32_t)page, make_divu32((uint64_t)page), table, width, stride, free_pages, free_capacity,
                      free_count, q_start, total_lens, slots, positions, max_tokens, free_left, unplaced};
     cudaLaunchConfig_t cfg{};
-    const unsigned ctas = max_tokens > 2 * SLOT_THREADS ? 8 : 1;
+    const unsigned ctas = max_tokens > 4 * SLOT_THREADS ? 8 : 1;          // one CTA as long as it looks up once
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(SLOT_THREADS);
     cfg.dynamicSmemBytes = (size_t)(3 * R + 2) * sizeof(int);
@@ -307,18 +329,22 @@ cudaError_t launch_kv_slots(const int32_t* seq_lens, const int32_t* new_lens, in
 cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token,
                              int64_t v_head, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
                              uint8_t* cache, const KvShape& c, cudaStream_t stream) {
-    const int64_t blocks = (T * c.heads * (c.dim / 16) + 255) / 256;
-    kv_append_kernel<<<dim3((unsigned)blocks, 2), 256, 0, stream>>>(k, v, k_token, k_head, v_token, v_head, slots, T,
-                                                                    s_k, s_v, cache, c);
+    const dim3 grid((unsigned)((T + 256 / (c.dim / 16) - 1) / (256 / (c.dim / 16))), (unsigned)c.heads, 2);
+    auto run = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(k, v, k_token, k_head, v_token, v_head, slots, T, s_k, s_v, cache, c); };
+    if (c.dim == 64) run(kv_append_kernel<64>);
+    else if (c.dim == 128) run(kv_append_kernel<128>);
+    else run(kv_append_kernel<256>);
     return cudaGetLastError();
 }
 
 cudaError_t launch_kv_gather(const uint8_t* cache, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
                              uint16_t* k, uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
                              const KvShape& c, cudaStream_t stream) {
-    const int64_t blocks = (T * c.heads * (c.dim / 16) + 255) / 256;
-    kv_gather_kernel<<<dim3((unsigned)blocks, 2), 256, 0, stream>>>(cache, slots, T, s_k, s_v, k, v, k_token, k_head,
-                                                                    v_token, v_head, c);
+    const dim3 grid((unsigned)((T + 256 / (c.dim / 16) - 1) / (256 / (c.dim / 16))), (unsigned)c.heads, 2);
+    auto run = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(cache, slots, T, s_k, s_v, k, v, k_token, k_head, v_token, v_head, c); };
+    if (c.dim == 64) run(kv_gather_kernel<64>);
+    else if (c.dim == 128) run(kv_gather_kernel<128>);
+    else run(kv_gather_kernel<256>);
     return cudaGetLastError();
 }
 
