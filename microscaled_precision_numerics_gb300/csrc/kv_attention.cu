@@ -451,15 +451,46 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                     for (int b = 0; b < (D + 127) / 128; ++b)
                         vsc[x][b] = *reinterpret_cast<const uint16_t*>(at_vs + st + gr * REC + 16 * b + 8 * x);
                 }
-                if (!full) {                                               // bytes beyond the context may be anything
+                if (!full) {
+                    uint32_t nan[2][(D + 127) / 128], any = 0;             // 0x7F in the byte of a scale that is NaN
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int tok = tok0 + gr * 16 + 8 * x;
                         const bool hv = (have >> gr) & 1u;
+                        // bytes beyond the context may be anything
                         const uint32_t keep = (hv && tok + kv_token_of_row(2 * t4) < rq.len ? 0x00FFu : 0u) |
                                               (hv && tok + kv_token_of_row(2 * t4 + 1) < rq.len ? 0xFF00u : 0u);
 #pragma unroll
-                        for (int b = 0; b < (D + 127) / 128; ++b) vsc[x][b] &= keep;
+                        for (int b = 0; b < (D + 127) / 128; ++b) {
+                            vsc[x][b] &= keep;
+                            nan[x][b] = ((vsc[x][b] & 0x007Fu) == 0x007Fu ? 0x00FFu : 0u) | ((vsc[x][b] & 0x7F00u) == 0x7F00u ? 0xFF00u : 0u);
+                            vsc[x][b] &= ~nan[x][b];
+                            any |= nan[x][b];
+                        }
+                    }
+                    // A NaN would reach the columns that mask its token, as 0 * NaN.  It goes instead, block by block, to the
+                    // columns whose probability for the token is not zero.
+                    if (__any_sync(0xFFFFFFFFu, any != 0)) {
+#pragma unroll 1
+                        for (int q = 0; q < 8; ++q)
+#pragma unroll
+                            for (int nq = 0; nq < NQ; ++nq) {
+                                const uint32_t p0 = __shfl_sync(0xFFFFFFFFu, pf[gr][nq][0], 4 * q + t4), p1 = __shfl_sync(0xFFFFFFFFu, pf[gr][nq][1], 4 * q + t4);
+                                const uint32_t on0 = ((p0 & 0x7FFFu) ? 0x00FFu : 0u) | ((p0 & 0x7FFF0000u) ? 0xFF00u : 0u);
+                                const uint32_t on1 = ((p1 & 0x7FFFu) ? 0x00FFu : 0u) | ((p1 & 0x7FFF0000u) ? 0xFF00u : 0u);
+#pragma unroll
+                                for (int b = 0; b < (D + 127) / 128; ++b) {
+                                    uint32_t hit = (nan[0][b] & on0) | (nan[1][b] & on1);
+                                    hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 1);
+                                    hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 2);
+                                    const float add = hit && (q >> 1) == t4 ? __int_as_float(0x7FC00000) : 0.0f;
+#pragma unroll
+                                    for (int w = 2 * b; w < VW && w < 2 * b + 2; ++w)
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e)
+                                            if ((e & 1) == (q & 1)) o[nq][4 * w + (e >> 2)][e & 3] += add;
+                                }
+                            }
                     }
                 }
 #pragma unroll

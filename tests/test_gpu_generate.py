@@ -375,6 +375,33 @@ def test_attention_nan_key_spreads_inside_its_head_only(mx):
     assert out[0, 2:].isnan().all() and torch.equal(out[0, :2], good[0, :2]) and torch.equal(out[1], good[1])
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_nan_value_reaches_only_rows_that_attend_to_it(mx, D):
+    """A NaN block scale of V at a position that some rows of a run of new tokens mask (a later token, or one before the
+    window): those rows are as without it, the others have NaN in that block of 16 dimensions and nowhere else."""
+    kv, group, n, L = 2, 3, 6, 75
+    q, q_start, lens, table, cache, s_k, s_v = attention_case(11, [L], [n], kv * group, kv, D, 16)
+    window = 20
+    base, _ = check_attention(mx, q, q_start, lens, table, cache, s_k, s_v, 0.1, 16, window)
+    blk = D // 16 - 1
+    for tok in (L - 3, L - n - window + 3):                             # masked by the first rows; by the last rows
+        hurt = cache.clone()
+        i = tok % 16
+        hurt[int(table[0, tok // 16]), 1, 0, 17 * D + blk * 16 + ref.v_scale_position(i)] = 0xFF
+        out = torch.zeros_like(base)
+        ws = torch.empty(mx.kv_attention_workspace_bytes(D), dtype=torch.uint8, device=DEV)
+        mx.mx_nvfp4_kv_attention(q, i32(q_start), i32(lens), i32(table), hurt, f32(s_k), f32(s_v), 0.1, n, out, ws, window=window)
+        done(mx)
+        for t in range(n):
+            pos = L - n + t
+            sees = pos - window < tok <= pos
+            assert torch.equal(out[t, :group], base[t, :group])
+            assert out[t, group:, blk * 16:].isnan().all() == sees and out[t, group:, blk * 16:].isnan().any() == sees
+            assert torch.equal(out[t, group:, :blk * 16], base[t, group:, :blk * 16])
+            if not sees:
+                assert torch.equal(out[t], base[t])
+
+
 def test_attention_strided_stream_graph_and_repeatable(mx):
     """q and out as views of larger tensors, on a side stream, captured in a graph and replayed: the same bits."""
     q, q_start, lens, table, cache, s_k, s_v = attention_case(10, [900, 35, 410], [1, 2, 1], 8, 2, 128, 16)
