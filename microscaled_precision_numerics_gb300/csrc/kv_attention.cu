@@ -37,7 +37,7 @@ constexpr float ATT_SLACK = 8.0f;            // the running maximum may lag by 2
 
 __host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 4 : 2; }
 // Resident CTAs per SM: by registers (O holds D / 4 * NQ of them) and by shared memory.
-__host__ __device__ constexpr int att_ctas(int D, int NQ) { return D == 256 ? (NQ == 1 ? 3 : 2) : (NQ == 1 ? 4 : (NQ == 2 ? 3 : 2)); }
+__host__ __device__ constexpr int att_ctas(int D, int NQ) { return D == 64 && NQ == 1 ? 4 : (D == 256 && NQ == 2 ? 2 : 3); }
 __host__ __device__ constexpr int att_ring_bytes(int D) { return ATT_WARPS * att_stages(D) * 2 * kv_record_bytes(D); }
 constexpr int ATT_MAX_CTAS_PER_SM = 4;
 
@@ -676,8 +676,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) kv_attention_join_kernel(const _
     if (a.lse && lane == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
 }
 
-constexpr int att_max_columns(int D) { return D == 256 ? 16 : 32; }
-
 template <int D, int NQ>
 cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
     static PerDevice pd;
@@ -716,17 +714,16 @@ cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
 template <int D>
 cudaError_t launch_d(AttParams& p, int num_sms, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.a.max_q * p.a.group;
-    if (rows <= 8) return launch_nq<D, 1>(p, num_sms, stream);
-    if (D != 64 || rows <= 16) return launch_nq<D, 2>(p, num_sms, stream);
-    if constexpr (D == 64) return launch_nq<D, 4>(p, num_sms, stream);
-    return cudaErrorInvalidValue;
+    // Two column fragments for more than eight query rows of a kv head; wider items of 32 (drafts, D = 64: 26.8 us instead of
+    // 20.3) keep too few warps on an SM, and their registers spill for larger D.
+    return rows <= 8 ? launch_nq<D, 1>(p, num_sms, stream) : launch_nq<D, 2>(p, num_sms, stream);
 }
 
 }  // namespace
 
 size_t kv_attention_workspace_bytes(int64_t D) {
-    const int64_t ctas = (int64_t)device_sm_count() * ATT_MAX_CTAS_PER_SM;
-    return (size_t)(ctas * ((int64_t)sizeof(Piece) + 2 * att_max_columns((int)D) * (D + 2) * 4));
+    const int columns = 8 * (att_ctas((int)D, 1) > 2 * att_ctas((int)D, 2) ? att_ctas((int)D, 1) : 2 * att_ctas((int)D, 2));   // of an SM's CTAs
+    return (size_t)((int64_t)device_sm_count() * (ATT_MAX_CTAS_PER_SM * (int64_t)sizeof(Piece) + 2 * columns * (D + 2) * 4));
 }
 
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, int num_sms, cudaStream_t stream) {
