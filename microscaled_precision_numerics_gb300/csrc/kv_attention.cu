@@ -23,6 +23,7 @@
 #include "mx_internal.h"
 #include "mx_kv.cuh"
 #include "mx_fragment.cuh"
+#include "mx_chain.cuh"
 
 namespace mxk {
 
@@ -94,11 +95,11 @@ struct Request {
 template <int NQ>
 __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r) {
     Request q;
-    q.first = __ldg(a.q_start + r);
+    q.first = load_global(a.q_start + r);
     // (offsets outside [0, T] are invalid input; the clamps keep every access inside q and out all the same)
-    q.count = q.first < 0 ? 0 : (int)min64(min64(__ldg(a.q_start + r + 1), a.T) - q.first, a.max_q);
+    q.count = q.first < 0 ? 0 : (int)min64(min64(load_global(a.q_start + r + 1), a.T) - q.first, a.max_q);
     q.count = max(0, q.count);
-    q.len = max(0, __ldg(a.seq_lens + r));
+    q.len = max(0, load_global(a.seq_lens + r));
     const int64_t lo = a.window > 0 ? max64(0, (int64_t)q.len - q.count + 1 - a.window) : 0;
     q.tile0 = (int)(lo / ATT_TILE);
     q.tiles = max(1, (int)(((uint32_t)q.len + ATT_TILE - 1) / ATT_TILE) - q.tile0);
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
 
     // ---- the CTA's share: equal runs over (request, kv head, column tile, fixed cost and context tiles)
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    chain_begin();
     const int per = (a.R + ATT_THREADS - 1) / ATT_THREADS, r0 = tid * per;
     int64_t mine = 0;
     int my_items = 0;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             if (grp * KV_GROUP >= rq.len) return -1;
             const uint32_t col = divu32((uint32_t)grp, p.dv_page_groups);
             if (col >= a.width) return -1;
-            const int page = __ldg(a.table + r * a.stride + col);
+            const int page = load_global(a.table + r * a.stride + col);
             if (page < 0 || page >= a.pages) return -1;
             return (((int64_t)page * a.kv_heads + h) * p.page_groups + ((uint32_t)grp - col * (uint32_t)p.page_groups)) * REC;
         };
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         uint32_t qf[NQ][KS][2];
         float mul[NQ][2], slack[NQ][2];                                    // score -> exponent of two, columns 2 t4, 2 t4 + 1
         int pos[NQ][2];                                                    // last position they attend to (-1: none)
-        const float S_k = __ldg(a.s_k + h);
+        const float S_k = load_global(a.s_k + h);
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
             const int col = col0 + nq * 8 + g;
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (real) v = __ldg(src + k);
+                if (real) v = load_global(src + k);
                 w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
             }
 #pragma unroll
@@ -541,7 +542,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         float* buf = reinterpret_cast<float*>(smem);                       // [warp][8][D + 4]
         constexpr int LD = D + 4;
         static_assert(ATT_WARPS * 8 * LD * 4 <= att_ring_bytes(D), "the join fits in the ring");
-        const float S_v = __ldg(a.s_v + h);
+        const float S_v = load_global(a.s_v + h);
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
             __syncthreads();                                               // ring (or buffer) no longer read; s_m, s_l written
@@ -600,7 +601,7 @@ constexpr int JOIN_THREADS = 256;
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(JOIN_THREADS) kv_attention_join_kernel(const __grid_constant__ AttParams p, int columns) {
     constexpr int V = D / 32, WARPS = JOIN_THREADS / 32, UB = 8;             // UB pieces in flight
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chain_begin();
     const Piece pc = p.pieces[blockIdx.x];
     if (pc.count <= 0) return;
     const KvAttentionArgs& a = p.a;
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) kv_attention_join_kernel(const _
     }
     const int i = (int)divu32((uint32_t)col, p.dv_group), hq = pc.kv_head * a.group + (col - i * a.group);
     const int64_t t = pc.token0 + i;
-    const float f = L == 0.0f ? 0.0f : __ldg(a.s_v + pc.kv_head) / L;
+    const float f = L == 0.0f ? 0.0f : load_global(a.s_v + pc.kv_head) / L;
     uint32_t* out = reinterpret_cast<uint32_t*>(a.out + t * a.o_token + (int64_t)hq * a.o_head + lane * V);
 #pragma unroll
     for (int v = 0; v < V; v += 2) out[v >> 1] = pack_bf16x2(o[v] * f, o[v + 1] * f);
@@ -693,22 +694,12 @@ cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
     p.pieces = reinterpret_cast<Piece*>(ws);
     p.part_ml = reinterpret_cast<float*>(ws + (int64_t)num_sms * ATT_MAX_CTAS_PER_SM * sizeof(Piece));
     p.part_o = p.part_ml + (int64_t)ctas * 2 * (8 * NQ) * 2;
-    kv_attention_kernel<D, NQ><<<ctas, ATT_THREADS, att_ring_bytes(D), stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_chained(kv_attention_kernel<D, NQ>, dim3((unsigned)ctas), ATT_THREADS, att_ring_bytes(D), 0, stream, p);
     if (e != cudaSuccess) return e;
-    // the join starts while the last CTAs finish and waits for them on the device
-    cudaLaunchConfig_t cfg{};
     const bool shared = items * 8 <= ctas;
-    cfg.gridDim = dim3((unsigned)p.n_pieces, shared ? 8 * NQ : 8 * NQ * 32 / JOIN_THREADS);
-    cfg.blockDim = dim3(JOIN_THREADS);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return shared ? cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, true>, p, 8 * NQ)
-                  : cudaLaunchKernelEx(&cfg, kv_attention_join_kernel<D, false>, p, 8 * NQ);
+    const dim3 grid((unsigned)p.n_pieces, shared ? 8 * NQ : 8 * NQ * 32 / JOIN_THREADS);
+    return shared ? launch_chained(kv_attention_join_kernel<D, true>, grid, JOIN_THREADS, 0, 0, stream, p, 8 * NQ)
+                  : launch_chained(kv_attention_join_kernel<D, false>, grid, JOIN_THREADS, 0, 0, stream, p, 8 * NQ);
 }
 
 template <int D>

@@ -5,6 +5,7 @@
 // calibrated ahead (NeMo RL FP8 page, "FP8 KV cache"); here the second-level scale S is one FP32 per kv head.
 #include "mx_internal.h"
 #include "mx_kv.cuh"
+#include "mx_chain.cuh"
 
 namespace mxk {
 
@@ -79,7 +80,8 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int per = (a.R + SLOT_THREADS - 1) / SLOT_THREADS, r0 = tid * per;
     const uint32_t P = a.page;
-    const int64_t n_free = max64(0, min64(__ldg(a.free_count), a.free_capacity));
+    chain_begin();
+    const int64_t n_free = max64(0, min64(load_global(a.free_count), a.free_capacity));
 
     auto meet = [&]() {                        // of the cluster, or of the one CTA
         if (cluster_size() > 1) cluster_sync();
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
         int r[1];
         last_not_above(s_pages, a.R, x, r);
         const int64_t col = (int64_t)had_of(r[0]) + (k - s_pages[r[0]]);
-        if (col < a.width) a.table[r[0] * a.stride + col] = k < n_free ? __ldg(a.free_pages + (n_free - 1 - k)) : -1;
+        if (col < a.width) a.table[r[0] * a.stride + col] = k < n_free ? load_global(a.free_pages + (n_free - 1 - k)) : -1;
     }
     int placed = 0;
     constexpr int U = 4;                       // tokens of a thread looked up side by side
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
                         page[u] = a.table[r[u] * a.stride + col];       // an older page: not written by this call
                     } else {
                         const int64_t k = s_pages[r[u]] + (int64_t)(col - had);
-                        if (k < n_free) page[u] = __ldg(a.free_pages + (n_free - 1 - k));
+                        if (k < n_free) page[u] = load_global(a.free_pages + (n_free - 1 - k));
                     }
                 }
             }
@@ -220,24 +222,25 @@ __device__ __forceinline__ T* record_of(T* cache, int64_t slot, int h, const KvS
 
 template <int D>
 __global__ void __launch_bounds__(256)
-kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v, int64_t k_token, int64_t k_head,
-                 int64_t v_token, int64_t v_head, const int32_t* __restrict__ slots, int64_t T,
-                 const float* __restrict__ s_k, const float* __restrict__ s_v, uint8_t* __restrict__ cache, KvShape c) {
+kv_append_kernel(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t k_head,
+                 int64_t v_token, int64_t v_head, const int32_t* slots, int64_t T,
+                 const float* s_k, const float* s_v, uint8_t* cache, KvShape c) {
+    chain_begin();
     const bool is_v = blockIdx.z != 0;
     constexpr int nb = D / 16;
     const int64_t t = (int64_t)blockIdx.x * (256 / nb) + threadIdx.x / nb;
     const int h = blockIdx.y, b = threadIdx.x % nb;
     if (t >= T) return;
     int token;
-    uint8_t* rec = record_of(cache, __ldg(slots + t), h, c, token);
+    uint8_t* rec = record_of(cache, load_global(slots + t), h, c, token);
     if (!rec) return;
     const uint4* src = reinterpret_cast<const uint4*>((is_v ? v + t * v_token + h * v_head : k + t * k_token + h * k_head) + b * 16);
-    const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+    const uint4 x0 = load_global(src), x1 = load_global(src + 1);
     const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
     uint32_t m2 = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m2 = absmax_bf16x2_int(m2, w[j]);     // integer maximum: a NaN is the largest
-    const float S = __ldg((is_v ? s_v : s_k) + h);
+    const float S = load_global((is_v ? s_v : s_k) + h);
     const uint32_t bs = nvfp4_block_scale_fast(__uint_as_float(fold_halves(m2) << 16), S, nvfp4_fast_rs(S));
     const float r = nvfp4_block_recip(bs, S);
     uint2 out;
@@ -265,9 +268,10 @@ kv_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
 
 template <int D>
 __global__ void __launch_bounds__(256)
-kv_gather_kernel(const uint8_t* __restrict__ cache, const int32_t* __restrict__ slots, int64_t T,
-                 const float* __restrict__ s_k, const float* __restrict__ s_v, uint16_t* __restrict__ k,
-                 uint16_t* __restrict__ v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, KvShape c) {
+kv_gather_kernel(const uint8_t* cache, const int32_t* slots, int64_t T,
+                 const float* s_k, const float* s_v, uint16_t* k,
+                 uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, KvShape c) {
+    chain_begin();
     const bool is_v = blockIdx.z != 0;
     constexpr int nb = D / 16;
     const int64_t t = (int64_t)blockIdx.x * (256 / nb) + threadIdx.x / nb;
@@ -275,12 +279,12 @@ kv_gather_kernel(const uint8_t* __restrict__ cache, const int32_t* __restrict__ 
     if (t >= T) return;
     uint32_t out[8] = {};
     int token;
-    const uint8_t* rec = record_of(cache, __ldg(slots + t), h, c, token);
+    const uint8_t* rec = record_of(cache, load_global(slots + t), h, c, token);
     if (rec) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(rec + (is_v ? kv_v_codes(D) : 0) + token * (D / 2) + b * 8));
-        const uint32_t bs = __ldg(is_v ? rec + kv_v_scales(D) + b * 16 + kv_token_of_row(token)
+        const uint2 q = load_global(reinterpret_cast<const uint2*>(rec + (is_v ? kv_v_codes(D) : 0) + token * (D / 2) + b * 8));
+        const uint32_t bs = load_global(is_v ? rec + kv_v_scales(D) + b * 16 + kv_token_of_row(token)
                                        : rec + kv_k_scales(D) + token * nb + b);
-        const float S = __ldg((is_v ? s_v : s_k) + h), f = e4m3_to_f32(bs);
+        const float S = load_global((is_v ? s_v : s_k) + h), f = e4m3_to_f32(bs);
         const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -312,40 +316,24 @@ cudaError_t launch_kv_slots(const int32_t* seq_lens, const int32_t* new_lens, in
     if (e != cudaSuccess) return e;
     const SlotArgs a{seq_lens, new_lens, (int)R, (uint32_t)page, make_divu32((uint64_t)page), table, width, stride, free_pages, free_capacity,
                      free_count, q_start, total_lens, slots, positions, max_tokens, free_left, unplaced};
-    cudaLaunchConfig_t cfg{};
     const unsigned ctas = max_tokens > 4 * SLOT_THREADS ? 8 : 1;          // one CTA as long as it looks up once
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(SLOT_THREADS);
-    cfg.dynamicSmemBytes = (size_t)(3 * R + 2) * sizeof(int);
-    cfg.stream = stream;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim = {ctas, 1, 1};
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_slots_kernel, a);
+    return launch_chained(kv_slots_kernel, dim3(ctas), SLOT_THREADS, (size_t)(3 * R + 2) * sizeof(int), ctas, stream, a);
 }
 
 cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token,
                              int64_t v_head, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
                              uint8_t* cache, const KvShape& c, cudaStream_t stream) {
     const dim3 grid((unsigned)((T + 256 / (c.dim / 16) - 1) / (256 / (c.dim / 16))), (unsigned)c.heads, 2);
-    auto run = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(k, v, k_token, k_head, v_token, v_head, slots, T, s_k, s_v, cache, c); };
-    if (c.dim == 64) run(kv_append_kernel<64>);
-    else if (c.dim == 128) run(kv_append_kernel<128>);
-    else run(kv_append_kernel<256>);
-    return cudaGetLastError();
+    return launch_chained(c.dim == 64 ? kv_append_kernel<64> : (c.dim == 128 ? kv_append_kernel<128> : kv_append_kernel<256>), grid, 256, 0, 0,
+                          stream, k, v, k_token, k_head, v_token, v_head, slots, T, s_k, s_v, cache, c);
 }
 
 cudaError_t launch_kv_gather(const uint8_t* cache, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
                              uint16_t* k, uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
                              const KvShape& c, cudaStream_t stream) {
     const dim3 grid((unsigned)((T + 256 / (c.dim / 16) - 1) / (256 / (c.dim / 16))), (unsigned)c.heads, 2);
-    auto run = [&](auto kernel) { kernel<<<grid, 256, 0, stream>>>(cache, slots, T, s_k, s_v, k, v, k_token, k_head, v_token, v_head, c); };
-    if (c.dim == 64) run(kv_gather_kernel<64>);
-    else if (c.dim == 128) run(kv_gather_kernel<128>);
-    else run(kv_gather_kernel<256>);
-    return cudaGetLastError();
+    return launch_chained(c.dim == 64 ? kv_gather_kernel<64> : (c.dim == 128 ? kv_gather_kernel<128> : kv_gather_kernel<256>), grid, 256, 0, 0,
+                          stream, cache, slots, T, s_k, s_v, k, v, k_token, k_head, v_token, v_head, c);
 }
 
 }  // namespace mxk

@@ -24,6 +24,7 @@
 // so a result does not depend on timing.
 #include "mx_internal.h"
 #include "mx_fragment.cuh"
+#include "mx_chain.cuh"
 
 namespace mxk {
 
@@ -88,7 +89,7 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             x[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (m < a.M && (!TAIL || k + u * 8 < a.K)) x[u] = __ldg(reinterpret_cast<const uint4*>(a.x + m * a.ldx + k) + u);
+            if (m < a.M && (!TAIL || k + u * 8 < a.K)) x[u] = load_global(reinterpret_cast<const uint4*>(a.x + m * a.ldx + k) + u);
         }
     };
     auto stage_x = [&](int c0, int n_steps, bool loaded) {
@@ -130,6 +131,7 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
         }
         __syncthreads();
     };
+    chain_begin();
     load_x(cta0, min(plan.stretch, cta1 - cta0), tid);
 
     // ---- the warp's steps, cta0 + wk, + WK, ... of one row group after the other, enter the ring STAGES - 1 ahead
@@ -263,7 +265,7 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
         auto store = [&](int group, int b, int r, int m, float v) {
             const int64_t n = (int64_t)(group >> 2) * 128 + 8 * (group & 3) + 32 * b + r;
             if (group >= groups || n >= a.N || m >= a.M) return;
-            v *= __ldg(a.s2 + (a.s2_per_row ? n : 0));
+            v *= load_global(a.s2 + (a.s2_per_row ? n : 0));
             if (a.y_fp32) static_cast<float*>(a.y)[m * a.ldy + n] = v;
             else static_cast<uint16_t*>(a.y)[m * a.ldy + n] = (uint16_t)pack_bf16x2(v, 0.0f);
         };
@@ -384,10 +386,8 @@ cudaError_t launch_nq(const MatvecArgs& a, cudaStream_t stream) {
     const MvPlan plan = mv_plan(NQ, a, clusters[dev], c);
     const int per_turn = MV_WARPS / plan.wk;
     const int64_t turns = ((a.N + 127) / 128 * 4 + per_turn - 1) / per_turn;
-    at.val.clusterDim = {(unsigned)c, 1, 1};
-    cfg.gridDim = dim3((unsigned)(min64(turns, max(1, clusters[dev][c])) * c));
-    cfg.stream = stream;
-    return cudaLaunchKernelEx(&cfg, matvec_kernel<NQ, TAIL, A16>, a, plan);
+    return launch_chained(matvec_kernel<NQ, TAIL, A16>, dim3((unsigned)(min64(turns, max(1, clusters[dev][c])) * c)), 32 * MV_WARPS, MV_SMEM,
+                          (unsigned)c, stream, a, plan);
 }
 
 template <int NQ>
