@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
 // the framework, with the same arithmetic and S per head.  Both are bound by memory (2.5625 bytes a value).
 // A warp holds the D / 16 blocks of neighbouring tokens of one head, so that the single bytes of the V scales, whose
 // neighbours in memory are other tokens' of the same block, leave it merged by sectors (4 tokens a sector for D = 128
-// instead of one).  Grid: tokens, heads, K or V; no index is divided.
+// instead of one).  Grid: tokens, heads; no index is divided, and K and V of a block share a thread's indexes.
 // ------------------------------------------------------------------------------------------------
 
 // The record of (slot, head), or null when the slot is outside the cache.
@@ -220,28 +220,13 @@ __device__ __forceinline__ T* record_of(T* cache, int64_t slot, int h, const KvS
     return cache + rec * kv_record_bytes(c.dim);
 }
 
-template <int D>
-__global__ void __launch_bounds__(256)
-kv_append_kernel(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t k_head,
-                 int64_t v_token, int64_t v_head, const int32_t* slots, int64_t T,
-                 const float* s_k, const float* s_v, uint8_t* cache, KvShape c) {
-    chain_begin();
-    const bool is_v = blockIdx.z != 0;
-    constexpr int nb = D / 16;
-    const int64_t t = (int64_t)blockIdx.x * (256 / nb) + threadIdx.x / nb;
-    const int h = blockIdx.y, b = threadIdx.x % nb;
-    if (t >= T) return;
-    int token;
-    uint8_t* rec = record_of(cache, load_global(slots + t), h, c, token);
-    if (!rec) return;
-    const uint4* src = reinterpret_cast<const uint4*>((is_v ? v + t * v_token + h * v_head : k + t * k_token + h * k_head) + b * 16);
-    const uint4 x0 = load_global(src), x1 = load_global(src + 1);
+// A 16-block of BF16 as codes and block scale byte under S.
+__device__ __forceinline__ uint2 quantize_block(const uint4& x0, const uint4& x1, float S, uint32_t& bs) {
     const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
     uint32_t m2 = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m2 = absmax_bf16x2_int(m2, w[j]);     // integer maximum: a NaN is the largest
-    const float S = load_global((is_v ? s_v : s_k) + h);
-    const uint32_t bs = nvfp4_block_scale_fast(__uint_as_float(fold_halves(m2) << 16), S, nvfp4_fast_rs(S));
+    bs = nvfp4_block_scale_fast(__uint_as_float(fold_halves(m2) << 16), S, nvfp4_fast_rs(S));
     const float r = nvfp4_block_recip(bs, S);
     uint2 out;
     float f[8];
@@ -261,43 +246,72 @@ kv_append_kernel(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t 
         out.x &= 0x88888888u;
         out.y &= 0x88888888u;
     }
-    *reinterpret_cast<uint2*>(rec + (is_v ? kv_v_codes(D) : 0) + token * (D / 2) + b * 8) = out;
-    if (is_v) rec[kv_v_scales(D) + b * 16 + kv_token_of_row(token)] = (uint8_t)bs;
-    else rec[kv_k_scales(D) + token * nb + b] = (uint8_t)bs;
+    return out;
+}
+
+// The BF16 values of a 16-block.
+__device__ __forceinline__ void dequantize_block(uint2 q, uint32_t bs, float S, uint4& y0, uint4& y1) {
+    const float f = e4m3_to_f32(bs);
+    const uint32_t w[2] = {q.x, q.y};
+    uint32_t out[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t p = e2m1x2_to_f16x2((w[j >> 2] >> (8 * (j & 3))) & 0xFFu);
+        // the product with the block scale is exact, so the value is rounded by S and once to BF16
+        const float v0 = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(p & 0xFFFFu))), f);
+        const float v1 = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(p >> 16))), f);
+        out[j] = pack_bf16x2(__fmul_rn(v0, S), __fmul_rn(v1, S));
+    }
+    y0 = make_uint4(out[0], out[1], out[2], out[3]);
+    y1 = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 template <int D>
 __global__ void __launch_bounds__(256)
-kv_gather_kernel(const uint8_t* cache, const int32_t* slots, int64_t T,
-                 const float* s_k, const float* s_v, uint16_t* k,
-                 uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, KvShape c) {
+kv_append_kernel(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
+                 const int32_t* slots, int64_t T, const float* s_k, const float* s_v, uint8_t* cache, KvShape c) {
     chain_begin();
-    const bool is_v = blockIdx.z != 0;
     constexpr int nb = D / 16;
     const int64_t t = (int64_t)blockIdx.x * (256 / nb) + threadIdx.x / nb;
     const int h = blockIdx.y, b = threadIdx.x % nb;
     if (t >= T) return;
-    uint32_t out[8] = {};
+    const uint4* from_k = reinterpret_cast<const uint4*>(k + t * k_token + h * k_head + b * 16);
+    const uint4* from_v = reinterpret_cast<const uint4*>(v + t * v_token + h * v_head + b * 16);
+    const uint4 k0 = load_global(from_k), k1 = load_global(from_k + 1), v0 = load_global(from_v), v1 = load_global(from_v + 1);
+    int token;
+    uint8_t* rec = record_of(cache, load_global(slots + t), h, c, token);
+    if (!rec) return;
+    uint32_t bs;
+    *reinterpret_cast<uint2*>(rec + token * (D / 2) + b * 8) = quantize_block(k0, k1, load_global(s_k + h), bs);
+    rec[kv_k_scales(D) + token * nb + b] = (uint8_t)bs;
+    *reinterpret_cast<uint2*>(rec + kv_v_codes(D) + token * (D / 2) + b * 8) = quantize_block(v0, v1, load_global(s_v + h), bs);
+    rec[kv_v_scales(D) + b * 16 + kv_token_of_row(token)] = (uint8_t)bs;
+}
+
+template <int D>
+__global__ void __launch_bounds__(256)
+kv_gather_kernel(const uint8_t* cache, const int32_t* slots, int64_t T, const float* s_k, const float* s_v, uint16_t* k,
+                 uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, KvShape c) {
+    chain_begin();
+    constexpr int nb = D / 16;
+    const int64_t t = (int64_t)blockIdx.x * (256 / nb) + threadIdx.x / nb;
+    const int h = blockIdx.y, b = threadIdx.x % nb;
+    if (t >= T) return;
+    uint4 k0 = make_uint4(0u, 0u, 0u, 0u), k1 = k0, v0 = k0, v1 = k0;
     int token;
     const uint8_t* rec = record_of(cache, load_global(slots + t), h, c, token);
     if (rec) {
-        const uint2 q = load_global(reinterpret_cast<const uint2*>(rec + (is_v ? kv_v_codes(D) : 0) + token * (D / 2) + b * 8));
-        const uint32_t bs = load_global(is_v ? rec + kv_v_scales(D) + b * 16 + kv_token_of_row(token)
-                                       : rec + kv_k_scales(D) + token * nb + b);
-        const float S = load_global((is_v ? s_v : s_k) + h), f = e4m3_to_f32(bs);
-        const uint32_t w[2] = {q.x, q.y};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t p = e2m1x2_to_f16x2((w[j >> 2] >> (8 * (j & 3))) & 0xFFu);
-            // the product with the block scale is exact, so the value is rounded by S and once to BF16
-            const float v0 = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(p & 0xFFFFu))), f);
-            const float v1 = __fmul_rn(__half2float(__ushort_as_half((unsigned short)(p >> 16))), f);
-            out[j] = pack_bf16x2(__fmul_rn(v0, S), __fmul_rn(v1, S));
-        }
+        const uint2 kq = load_global(reinterpret_cast<const uint2*>(rec + token * (D / 2) + b * 8));
+        const uint2 vq = load_global(reinterpret_cast<const uint2*>(rec + kv_v_codes(D) + token * (D / 2) + b * 8));
+        const uint32_t ks = load_global(rec + kv_k_scales(D) + token * nb + b);
+        const uint32_t vs = load_global(rec + kv_v_scales(D) + b * 16 + kv_token_of_row(token));
+        dequantize_block(kq, ks, load_global(s_k + h), k0, k1);
+        dequantize_block(vq, vs, load_global(s_v + h), v0, v1);
     }
-    uint4* dst = reinterpret_cast<uint4*>((is_v ? v + t * v_token + h * v_head : k + t * k_token + h * k_head) + b * 16);
-    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    uint4* to_k = reinterpret_cast<uint4*>(k + t * k_token + h * k_head + b * 16);
+    uint4* to_v = reinterpret_cast<uint4*>(v + t * v_token + h * v_head + b * 16);
+    stcs_32b(to_k, k0, k1);
+    stcs_32b(to_v, v0, v1);
 }
 
 }  // namespace
@@ -323,7 +337,7 @@ cudaError_t launch_kv_slots(const int32_t* seq_lens, const int32_t* new_lens, in
 cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token,
                              int64_t v_head, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
                              uint8_t* cache, const KvShape& c, cudaStream_t stream) {
-    const dim3 grid((unsigned)((T + 256 / (c.dim / 16) - 1) / (256 / (c.dim / 16))), (unsigned)c.heads, 2);
+    const dim3 grid((unsigned)((T + 256 / (c.dim / 16) - 1) / (256 / (c.dim / 16))), (unsigned)c.heads);
     return launch_chained(c.dim == 64 ? kv_append_kernel<64> : (c.dim == 128 ? kv_append_kernel<128> : kv_append_kernel<256>), grid, 256, 0, 0,
                           stream, k, v, k_token, k_head, v_token, v_head, slots, T, s_k, s_v, cache, c);
 }
@@ -331,7 +345,7 @@ cudaError_t launch_kv_append(const uint16_t* k, const uint16_t* v, int64_t k_tok
 cudaError_t launch_kv_gather(const uint8_t* cache, const int32_t* slots, int64_t T, const float* s_k, const float* s_v,
                              uint16_t* k, uint16_t* v, int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
                              const KvShape& c, cudaStream_t stream) {
-    const dim3 grid((unsigned)((T + 256 / (c.dim / 16) - 1) / (256 / (c.dim / 16))), (unsigned)c.heads, 2);
+    const dim3 grid((unsigned)((T + 256 / (c.dim / 16) - 1) / (256 / (c.dim / 16))), (unsigned)c.heads);
     return launch_chained(c.dim == 64 ? kv_gather_kernel<64> : (c.dim == 128 ? kv_gather_kernel<128> : kv_gather_kernel<256>), grid, 256, 0, 0,
                           stream, cache, slots, T, s_k, s_v, k, v, k_token, k_head, v_token, v_head, c);
 }

@@ -327,10 +327,10 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
 }
 
 // The split of the work: warps along K and CTAs of a cluster along K, for one CTA an SM, such that the busiest warp has
-// the least to do, in steps.  Counted besides the steps: one for a meeting of a CTA's warps, two for one of a
+// the least to do, in steps.  Counted besides the steps: one for a meeting of a CTA's warps, three for one of a
 // cluster, the staging of x by its size.  clusters[c] is how many clusters of c CTAs the device runs at once (the SMs
 // of a cluster share a GPC, so it is below SMs / c).
-constexpr double MV_STAGING = 0.008, MV_MEET = 1.0, MV_MEET_CLUSTER = 2.0;
+constexpr double MV_STAGING = 0.008, MV_MEET = 1.0, MV_MEET_CLUSTER = 3.0;
 MvPlan mv_plan(int NQ, const MatvecArgs& a, const int (&clusters)[MV_MAX_SPLIT + 1], int& ctas_k) {
     const int steps = (int)((a.K + MV_STEP - 1) / MV_STEP), warps = MV_WARPS;
     const int64_t groups = (a.N + 127) / 128 * 4;
