@@ -291,7 +291,7 @@ def attention_case(seed, lens, new, heads, kv, D, page, junk=255, scale_v=1.0):
     return q, q_start, lens, table, torch.from_numpy(cache).to(DEV), s_k, s_v
 
 
-@pytest.mark.parametrize("lens,new,heads,kv,D,page,window", [
+ATTENTION_CASES = [
     ([1], [1], 4, 4, 64, 16, 0),                                   # one token of context
     ([15, 16, 17, 31, 32, 33], [1] * 6, 8, 2, 128, 16, 0),         # around the record and tile lengths
     ([63, 64, 65, 127, 129], [1] * 5, 8, 1, 128, 64, 0),
@@ -308,10 +308,41 @@ def attention_case(seed, lens, new, heads, kv, D, page, junk=255, scale_v=1.0):
     ([500], [40], 4, 2, 128, 32, 64),                              # shorter than the run of new tokens,
     ([300, 50], [1, 1], 4, 2, 128, 16, 100000),                    # longer than the context
     ([260, 260, 260], [1, 1, 1], 40, 1, 128, 16, 0),               # group of forty: several row tiles
-])
+]
+
+
+@pytest.mark.parametrize("lens,new,heads,kv,D,page,window", ATTENTION_CASES)
 def test_attention(mx, lens, new, heads, kv, D, page, window):
     q, q_start, lens, table, cache, s_k, s_v = attention_case(1, lens, new, heads, kv, D, page)
     check_attention(mx, q, q_start, lens, table, cache, s_k, s_v, D ** -0.5, page, window)
+
+
+def wide(table, columns):
+    """The table with columns of -1 behind: contexts of wide tables are split among CTAs, those of narrow ones are not."""
+    return np.pad(table, ((0, 0), (0, columns)), constant_values=-1)
+
+
+@pytest.mark.parametrize("lens,new,heads,kv,D,page,window", ATTENTION_CASES)
+def test_attention_wide_table(mx, lens, new, heads, kv, D, page, window):
+    q, q_start, lens, table, cache, s_k, s_v = attention_case(1, lens, new, heads, kv, D, page)
+    check_attention(mx, q, q_start, lens, wide(table, 5000 // page), cache, s_k, s_v, D ** -0.5, page, window)
+
+
+@pytest.mark.parametrize("group,drafts", [(2, 1), (6, 3)])
+def test_attention_more_items_than_ctas(mx, group, drafts):
+    """Hundreds of short contexts and a few long ones, split and not."""
+    rng = np.random.default_rng(12)
+    lens = rng.integers(0, 24, 260)
+    lens[[3, 77, 200]] = 1300, 641, 33
+    new = np.minimum(lens, rng.integers(1, drafts + 1, 260))
+    q, q_start, lens, table, cache, s_k, s_v = attention_case(13, lens, new, 4 * group, 4, 64, 16)
+    check_attention(mx, q, q_start, lens, table, cache, s_k, s_v, 0.125, 16)
+    short = lens < 700
+    keep = np.flatnonzero(short)
+    rows = np.concatenate([np.arange(q_start[r], q_start[r + 1]) for r in keep]).astype(int)
+    starts = np.concatenate([[0], np.cumsum(np.diff(q_start)[keep])])
+    check_attention(mx, q[torch.from_numpy(rows).to(DEV)].contiguous(), starts, lens[keep], np.ascontiguousarray(table[keep][:, :50]), cache,
+                    s_k, s_v, 0.125, 16)
 
 
 def test_attention_many_ragged_requests(mx):
