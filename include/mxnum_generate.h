@@ -77,7 +77,8 @@ mx_status mx_nvfp4_kv_gather(const uint8_t* cache, int64_t pages, int64_t page_s
  * with nothing to attend to gives zeros and lse = -inf.  Positions whose page number lies outside the cache are
  * skipped.
  *   q [T, heads, head_dim] BF16 and out alike, with token and head strides in elements (multiples of 8)
- *   q_start [requests + 1]  first token of each request (nondecreasing, q_start[0] = 0, q_start[requests] = T)
+ *   q_start [requests + 1]  first token of each request (nondecreasing, at most T; rows of out and lse that belong to
+ *            no request are not written)
  *   seq_lens [requests]  cached tokens, the new ones included;  max_q: at least the largest n
  *   block_table [requests, table_width] as written by mx_kv_slots;  s_k, s_v [kv_heads]
  *   lse [T, heads] FP32 or NULL

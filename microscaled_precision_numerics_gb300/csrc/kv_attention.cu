@@ -117,7 +117,8 @@ __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r) {
     q.len = max(0, load_global(a.seq_lens + r));
     const int64_t lo = a.window > 0 ? max64(0, (int64_t)q.len - q.count + 1 - a.window) : 0;
     q.tile0 = (int)(lo / ATT_TILE);
-    q.tiles = max(1, (int)(((uint32_t)q.len + ATT_TILE - 1) / ATT_TILE) - q.tile0);
+    const uint32_t held = (uint32_t)min64(q.len, a.width * a.page);       // positions that the table has pages for
+    q.tiles = max(1, (int)((held + ATT_TILE - 1) / ATT_TILE) - q.tile0);
     q.col_tiles = (q.count * a.group + 8 * NQ - 1) / (8 * NQ);
     return q;
 }

@@ -360,6 +360,21 @@ def test_attention_rows_with_nothing_to_attend(mx):
     check_attention(mx, q, np.array([0, 5, 7, 8]), lens, table, cache, s_k, s_v, 0.125, 16)
 
 
+def test_attention_leaves_padding_rows_alone(mx):
+    """More rows than the requests have tokens (a buffer of fixed length): the rest keeps what it holds."""
+    q, q_start, lens, table, cache, s_k, s_v = attention_case(14, [50, 1000], [2, 1], 4, 2, 64, 16)
+    for tab in (table, wide(table, 10)):
+        q6 = torch.cat([q, q])[:6]
+        out = torch.full((6, 4, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((6, 4), 9.0, dtype=torch.float32, device=DEV)
+        ws = torch.empty(mx.kv_attention_workspace_bytes(64), dtype=torch.uint8, device=DEV)
+        mx.mx_nvfp4_kv_attention(q6, i32(q_start), i32(lens), i32(tab), cache, f32(s_k), f32(s_v), 0.125, 2, out, ws, lse=lse)
+        done(mx)
+        want, want_lse = check_attention(mx, q, q_start, lens, tab, cache, s_k, s_v, 0.125, 16)
+        assert torch.equal(out[:3], want) and torch.equal(lse[:3], want_lse)
+        assert (out[3:] == 9).all() and (lse[3:] == 9).all()
+
+
 def test_attention_skips_missing_pages(mx):
     q, q_start, lens, table, cache, s_k, s_v = attention_case(5, [200, 64, 40], [2, 1, 1], 4, 2, 128, 16)
     table[0, 3], table[0, 12], table[1, :4], table[2, 1] = -1, 10 ** 6, -1, -7
