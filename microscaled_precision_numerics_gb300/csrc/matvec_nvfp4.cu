@@ -40,12 +40,13 @@ namespace {
 
 constexpr int MV_ROWS = 32;                           // of a warp
 constexpr int MV_STEP = 128;                          // values of K a step
-constexpr int MV_SLOT = 4 * 512 + 256;                // a warp's step in the ring: codes of four rows a lane, scales
+// A warp's step in the ring: codes of four rows a lane, scales; where rows start on 8 bytes only, 8 bytes more of a row.
+__host__ __device__ constexpr int mv_slot(bool A16) { return 4 * 512 + 256 + (A16 ? 0 : 256); }
 constexpr int MV_MAX_SPLIT = 8;                       // CTAs of a cluster
 constexpr int MV_SMEM = 225 * 1024;                   // dynamic shared memory of a CTA, which has its SM to itself
 constexpr int MV_WARPS = 16;
 __host__ __device__ constexpr int mv_stages(int NQ) { return NQ == 1 ? 3 : 2; }
-__host__ __device__ constexpr int mv_ring(int NQ) { return MV_WARPS * mv_stages(NQ) * MV_SLOT; }
+__host__ __device__ constexpr int mv_ring(int NQ, bool A16) { return MV_WARPS * mv_stages(NQ) * mv_slot(A16); }
 // Bytes of a staged token: a stretch of `steps` steps, and 64 so that odd and even tokens lie on both bank halves.
 __host__ __device__ constexpr int mv_row_bytes(int steps) { return steps * MV_STEP * 2 + 64; }
 // Partial sums, FP32 [warp][token][row]; staged x; its scales, FP32 [token][step].
@@ -67,15 +68,18 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// TAIL: K is not a multiple of the step.  A16: rows start on 16 bytes (K % 32 == 0).
+// TAIL: K is not a multiple of the step.  A16: rows start on 16 bytes (K % 32 == 0).  Where they do not, odd rows lie 8
+// bytes into a 16-byte piece: a quad brings the pieces that cover them, its last lane the 8 bytes of the fifth, and a
+// lane reads its 16 bytes from two neighbours.  All rows of a lane are odd or all even, as its g is.  4 x 57611 x 3152 takes
+// 32 us so, and 43 with two copies of 8 bytes a lane (3200, a multiple of the step: 23).
 template <int NQ, bool TAIL, bool A16>
 __global__ void __launch_bounds__(32 * MV_WARPS, 1)
 matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
-    constexpr int WARPS = MV_WARPS, THREADS = 32 * WARPS, STAGES = mv_stages(NQ);
+    constexpr int WARPS = MV_WARPS, THREADS = 32 * WARPS, STAGES = mv_stages(NQ), SLOT = mv_slot(A16);
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int WK = plan.wk, wk = warp & (WK - 1), groups_cta = WARPS / WK, row_bytes = mv_row_bytes(plan.stretch);
-    float* sums = reinterpret_cast<float*>(smem + mv_ring(NQ));                 // [warp][M][MV_ROWS]
+    float* sums = reinterpret_cast<float*>(smem + mv_ring(NQ, A16));                 // [warp][M][MV_ROWS]
     float* xscale = sums + WARPS * a.M * MV_ROWS;                               // [M][stretch]
     uint8_t* xs = smem + (MV_SMEM - a.M * row_bytes) / 16 * 16;
     uint32_t rank, ranks;
@@ -143,37 +147,40 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
     load_x(cta0, min(plan.stretch, cta1 - cta0), tid);
 
     // ---- the warp's steps, cta0 + wk, + WK, ... of one row group after the other, enter the ring STAGES - 1 ahead
-    uint8_t* ring = smem + warp * (STAGES * MV_SLOT);
+    uint8_t* ring = smem + warp * (STAGES * SLOT);
     const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
     int in_group = cta0 + wk < cta1 ? turn0 * groups_cta + warp / WK : groups;
     int in_step = cta0 + wk, in_slot = 0;
     const uint8_t *in_q[4], *in_s;                    // the thread's next bytes
-    auto left_of = [&](int step) { return (int)min64(32, a.K - (int64_t)step * MV_STEP - t4 * 32); };   // valid values of the thread's 32
+    const int odd = A16 ? 0 : 8 * (g & 1);            // bytes that the thread's rows lie beyond a 16-byte boundary
+    const bool beyond = odd && t4 == 3;               // the upper half of the thread's 16 bytes is of the fifth piece
+    // rows beyond the last repeat it, or the one before it that starts as they do (-1: there is none, and nothing is read)
+    const int64_t last_row = A16 ? a.N - 1 : a.N - 1 - ((a.N - 1 - g) & 1);
+    const int inputs = (int)a.K;                      // 2^24 at most
+    auto left_of = [&](int step) { return min(32, inputs - step * MV_STEP - t4 * 32); };     // valid values of the thread's 32
     auto aim = [&]() {                                // at the first step of in_group
         const int64_t band = in_group >> 2, r0 = band * 128 + 8 * (in_group & 3) + g;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) in_q[b] = a.q + min64(a.N - 1, r0 + 32 * b) * (a.K / 2) + (int64_t)in_step * (MV_STEP / 2) + t4 * 16;
+        for (int b = 0; b < 4; ++b) in_q[b] = a.q + min64(last_row, r0 + 32 * b) * (a.K / 2) + (int64_t)in_step * (MV_STEP / 2) + t4 * 16 - odd;
         in_s = a.s + ((band * nct + 2 * (int64_t)in_step + (t4 >> 1)) << 9) + ((8 * (in_group & 3) + g) << 4);
     };
     if (in_group < groups) aim();
     auto issue = [&]() {
         if (in_group < groups) {
-            const uint32_t slot_at = ring_u32 + in_slot * MV_SLOT, dst = slot_at + lane * 16, dst_s = slot_at + 4 * 512 + (g * 2 + (t4 >> 1)) * 16;
+            const uint32_t slot_at = ring_u32 + in_slot * SLOT, dst = slot_at + lane * 16, dst_s = slot_at + 4 * 512 + (g * 2 + (t4 >> 1)) * 16;
             if (!TAIL) {
 #pragma unroll
                 for (int b = 0; b < 4; ++b) copy_async_16(dst + b * 512, in_q[b]);
                 if ((t4 & 1) == 0) copy_async_16(dst_s, in_s);
             } else {                                  // beyond K zeros, from an address that is valid all the same
                 const int left = max(0, left_of(in_step));
+                // of an even row, or of one on 16 bytes, the piece may hold 16 values of the row; of an odd one 32, or none
+                const int bytes = !A16 && last_row < 0 ? 0 : (left > 0 && odd ? 16 : left / 2);
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    const uint8_t* src = left > 0 ? in_q[b] : a.q;
-                    if (A16) {
-                        copy_async_16z(dst + b * 512, src, left > 0 ? 16 : 0);
-                    } else {                          // K % 32 == 16: rows start on 8 bytes only
-                        copy_async_8z(dst + b * 512, src, left > 0 ? 8 : 0);
-                        copy_async_8z(dst + b * 512 + 8, left > 16 ? src + 8 : src, left > 16 ? 8 : 0);
-                    }
+                    copy_async_16z(dst + b * 512, bytes > 0 ? in_q[b] : a.q, bytes);
+                    if (beyond)
+                        copy_async_8z(slot_at + 4 * 512 + 256 + b * 64 + g * 8, bytes > 0 && left > 16 ? in_q[b] + 16 : a.q, bytes > 0 && left > 16 ? 8 : 0);
                 }
                 if ((t4 & 1) == 0) copy_async_16z(dst_s, left > 0 ? in_s : a.s, left > 0 ? 16 : 0);
             }
@@ -196,6 +203,7 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
 
     int slot = 0;
     const int sc_shift = 16 * (t4 & 1);
+    const int hi_at = beyond ? 4 * 512 + 256 + g * 8 : lane * 16 + odd + 8, hi_step = beyond ? 64 : 512;
     const bool once = cta1 - cta0 <= plan.stretch;    // x is staged once for all rows
     for (int turn = turn0; turn < turns; turn += turn_step) {
         const int group = turn * groups_cta + warp / WK;
@@ -217,10 +225,18 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
                 for (int step = c0 + wk; step < c1; step += WK) {
                     copy_async_wait<STAGES - 2>();
                     __syncwarp();                     // the scales come by other lanes; and the slot of the last step is free
-                    const uint8_t* st = ring + slot * MV_SLOT;
+                    const uint8_t* st = ring + slot * SLOT;
                     uint4 q[4], s;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) q[b] = *reinterpret_cast<const uint4*>(st + b * 512 + lane * 16);
+                    for (int b = 0; b < 4; ++b) {
+                        if (A16) {
+                            q[b] = *reinterpret_cast<const uint4*>(st + b * 512 + lane * 16);
+                        } else {
+                            const uint2 lo = *reinterpret_cast<const uint2*>(st + b * 512 + lane * 16 + odd);
+                            const uint2 hi = *reinterpret_cast<const uint2*>(st + hi_at + b * hi_step);
+                            q[b] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                        }
+                    }
                     s = *reinterpret_cast<const uint4*>(st + 4 * 512 + (g * 2 + (t4 >> 1)) * 16);
                     if (TAIL && left_of(step) < 32) {  // scales beyond K are padding
                         const uint32_t keep = left_of(step) < 16 ? 0u : ((t4 & 1) ? 0x00FF0000u : 0x000000FFu);
@@ -339,11 +355,11 @@ matvec_kernel(const __grid_constant__ MatvecArgs a, const MvPlan plan) {
 // cluster, the staging of x by its size.  clusters[c] is how many clusters of c CTAs the device runs at once (the SMs
 // of a cluster share a GPC, so it is below SMs / c).
 constexpr double MV_STAGING = 0.008, MV_MEET = 1.0, MV_MEET_CLUSTER = 3.0;
-MvPlan mv_plan(int NQ, const MatvecArgs& a, const int (&clusters)[MV_MAX_SPLIT + 1], int& ctas_k) {
+MvPlan mv_plan(int ring, const MatvecArgs& a, const int (&clusters)[MV_MAX_SPLIT + 1], int& ctas_k) {
     const int steps = (int)((a.K + MV_STEP - 1) / MV_STEP), warps = MV_WARPS;
     const int64_t groups = (a.N + 127) / 128 * 4;
     int fits = 0;                                     // steps of x that have room
-    while (fits < steps && mv_ring(NQ) + mv_sums(a.M) + mv_x(a.M, fits + 1) + 16 <= MV_SMEM) ++fits;
+    while (fits < steps && ring + mv_sums(a.M) + mv_x(a.M, fits + 1) + 16 <= MV_SMEM) ++fits;
     MvPlan best{1, 1};
     double least = 1e30;
     ctas_k = 1;
@@ -391,7 +407,7 @@ cudaError_t launch_nq(const MatvecArgs& a, cudaStream_t stream) {
     });
     if (e != cudaSuccess) return e;
     int c = 1;
-    const MvPlan plan = mv_plan(NQ, a, clusters[dev], c);
+    const MvPlan plan = mv_plan(mv_ring(NQ, A16), a, clusters[dev], c);
     const int per_turn = MV_WARPS / plan.wk;
     const int64_t turns = ((a.N + 127) / 128 * 4 + per_turn - 1) / per_turn;
     return launch_chained(matvec_kernel<NQ, TAIL, A16>, dim3((unsigned)(min64(turns, max(1, clusters[dev][c])) * c)), 32 * MV_WARPS, MV_SMEM,
