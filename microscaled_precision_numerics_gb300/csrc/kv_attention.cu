@@ -26,13 +26,15 @@
 // ATT_ITEM_COST tiles (look-ups, queries, the join of the warps; without it eight requests with one very short among them
 // took 32 us instead of 14), and every CTA takes an equal run of that line.  A run's first and last item may be shared
 // with neighbours; those leave (maximum, sum, output) pieces in the workspace and a second kernel joins them in CTA order.
+// Short contexts are not split so: a CTA takes an item, or a cluster of up to 8 CTAs divides it and joins its parts through
+// distributed shared memory, in one launch and without the workspace.
 // The four warps of a CTA take every fourth tile of 32 positions with statistics of their own, through two stages of
 // cp.async each (three stages, or eight warps a CTA, were slower: 75.1 and 84.3 against 73.7 us).
 //
 // Measured on a GB300 (device us, share of the measured copy rate): 64 requests to 8192 tokens, 32 q heads over 8 kv heads, D =
 // 128: 73.0 (75 %; of the scheduler slots 57 % issue, the ALU is busy 49 %, the pipe that HMUL2 and HMMA share 51 %: bound
 // by latency with the 12 warps an SM that the registers leave); one request of 131071 tokens: 34.5 (64 %; about 8 us
-// of it are fixed: launch, look-ups, joins).
+// of it are fixed: launch, look-ups, joins); one of 777: 6.8 (latency; 10.0 without clusters).
 #include "mx_internal.h"
 #include "mx_kv.cuh"
 #include "mx_fragment.cuh"
@@ -47,7 +49,9 @@ constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_TILE = 32;                 // tokens of a warp's step: two records
 constexpr int ATT_ITEM_COST = 12;             // what an item costs besides its tiles, in tiles
 constexpr int ATT_MIN_SHARE = 8;             // smallest share of a CTA: two steps a warp
-constexpr int64_t ATT_WHOLE_TOKENS = 896;    // longest table whose items are not split
+// Longest tables whose items are not split over the GPU: one CTA an item; a cluster, for each of its CTAs.  From
+// ATT_CLUSTER_TOKENS on an item has a cluster where the GPU has room.
+constexpr int64_t ATT_WHOLE_TOKENS = 896, ATT_WHOLE_CLUSTER_TOKENS = 640, ATT_CLUSTER_TOKENS = 384;
 constexpr float ATT_SLACK = 8.0f;            // the running maximum may lag by 2^8 (P stays below 2^8 in FP16)
 
 __host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 4 : 2; }
@@ -55,6 +59,7 @@ __host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 4 : 2; }
 __host__ __device__ constexpr int att_ctas(int D, int NQ) { return D == 64 && NQ == 1 ? 4 : (D == 256 && NQ == 2 ? 2 : 3); }
 __host__ __device__ constexpr int att_ring_bytes(int D) { return ATT_WARPS * att_stages(D) * 2 * kv_record_bytes(D); }
 constexpr int ATT_MAX_CTAS_PER_SM = 4;
+constexpr int ATT_MAX_CLUSTER = 8;
 
 // Workspace: partial results of the work items that several CTAs share.  Each CTA has two places: 0 for an item
 // that began in an earlier CTA, 1 for one that goes on in the next.
@@ -72,9 +77,29 @@ struct AttParams {
     Piece* pieces;
     int n_pieces;                            // entries of pieces
     bool by_item;                            // they are numbered by item (else by CTA)
-    bool whole_items;                        // no item is shared: a CTA takes those that begin in its share
+    bool whole_items;                        // an item is not shared: a CTA or cluster takes those that begin in its share, or one each
+    int cluster;                             // CTAs that divide the context of such an item (1: no cluster)
 };
 
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// The same place in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t there_u32(const void* p, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 load_there4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 load_there2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -104,11 +129,11 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 
 // What request r asks for: tiles of its context, items (kv head x column tile) and the first tile's position.
 struct Request {
-    int first, count, len, tile0, tiles, col_tiles;
-    __device__ int64_t cost(int kv_heads) const { return (int64_t)(tiles + ATT_ITEM_COST) * col_tiles * kv_heads; }
+    int first, count, len, tile0, tiles, col_tiles, per_item;             // per_item: cost of an item
+    __device__ int64_t cost(int kv_heads) const { return (int64_t)per_item * col_tiles * kv_heads; }
 };
 template <int NQ>
-__device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r) {
+__device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r, bool one_each) {
     Request q;
     q.first = load_global(a.q_start + r);
     // (offsets outside [0, T] are invalid input; the clamps keep every access inside q and out all the same)
@@ -120,10 +145,12 @@ __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r) {
     const uint32_t held = (uint32_t)min64(q.len, a.width * a.page);       // positions that the table has pages for
     q.tiles = max(1, (int)((held + ATT_TILE - 1) / ATT_TILE) - q.tile0);
     q.col_tiles = (q.count * a.group + 8 * NQ - 1) / (8 * NQ);
+    q.per_item = one_each ? 1 : q.tiles + ATT_ITEM_COST;
     return q;
 }
 
-template <int D, int NQ>
+// CLUSTER: every item belongs to a cluster, which divides its context and joins it in shared memory.
+template <int D, int NQ, bool CLUSTER>
 __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_kernel(const __grid_constant__ AttParams p) {
     constexpr int STAGES = att_stages(D), REC = kv_record_bytes(D), STAGE_BYTES = 2 * REC;
     constexpr int KS = D / 16;               // k-steps of the scores
@@ -136,17 +163,19 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
     __shared__ int64_t s_off;
     __shared__ int s_r, s_item;
     __shared__ float s_m[ATT_WARPS][8 * NQ], s_l[ATT_WARPS][8 * NQ];
+    __shared__ float2 s_ml[8 * NQ];          // of the CTA, for its cluster
 
     const KvAttentionArgs& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
 
     // ---- the CTA's share: equal runs over (request, kv head, column tile, fixed cost and context tiles)
     chain_begin();
+    const bool whole_items = CLUSTER || p.whole_items, one_each = CLUSTER || (p.whole_items && p.by_item);
     const int per = (a.R + ATT_THREADS - 1) / ATT_THREADS, r0 = tid * per;
     int64_t mine = 0;
     int my_items = 0;
     for (int r = r0; r < min(a.R, r0 + per); ++r) {
-        const Request q = request_of<NQ>(a, r);
+        const Request q = request_of<NQ>(a, r, one_each);
         mine += q.cost(a.kv_heads);
         my_items += q.col_tiles * a.kv_heads;
     }
@@ -176,13 +205,15 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         }
         total += s_warp_sum[w];
     }
-    const int64_t share = max64(p.whole_items ? 1 : ATT_MIN_SHARE, (total + gridDim.x - 1) / gridDim.x);
-    const int64_t begin = min64(total, blockIdx.x * share), end = min64(total, begin + share);
+    const uint32_t rank = CLUSTER ? blockIdx.x % p.cluster : 0u, taker = CLUSTER ? blockIdx.x / p.cluster : blockIdx.x;
+    const uint32_t takers = CLUSTER ? gridDim.x / p.cluster : gridDim.x;
+    const int64_t share = max64(whole_items ? 1 : ATT_MIN_SHARE, (total + takers - 1) / takers);
+    const int64_t begin = min64(total, taker * share), end = min64(total, begin + share);
     if (mine > 0 && begin >= excl && begin < excl + mine && begin < end) {
         int64_t at = excl;
         int r = r0, it = excl_items;
         for (;; ++r) {
-            const Request q = request_of<NQ>(a, r);
+            const Request q = request_of<NQ>(a, r, one_each);
             const int64_t w = q.cost(a.kv_heads);
             if (begin < at + w) break;
             at += w;
@@ -193,7 +224,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         s_item = it;
     }
     // every entry is written in every call: by the item's first CTA, or here
-    if (p.whole_items) {
+    if (whole_items) {
     } else if (!p.by_item) {
         if (tid == 0) p.pieces[blockIdx.x].count = 0;
     } else {
@@ -204,7 +235,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
 
     int r = s_r, item0 = s_item;             // request; number of its first item
     int64_t off = s_off;                     // place inside the request
-    Request rq = request_of<NQ>(a, r);
+    Request rq = request_of<NQ>(a, r, one_each);
     uint8_t* ring = smem + warp * (STAGES * STAGE_BYTES);
     const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
 
@@ -212,20 +243,24 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         while (off >= rq.cost(a.kv_heads)) {                               // next request with work
             off -= rq.cost(a.kv_heads);
             item0 += rq.col_tiles * a.kv_heads;
-            rq = request_of<NQ>(a, ++r);
+            rq = request_of<NQ>(a, ++r, one_each);
         }
-        const int per_item = rq.tiles + ATT_ITEM_COST, item = (int)(off / per_item), in_item = (int)(off - (int64_t)item * per_item);
-        if (p.whole_items && in_item > 0) {                                // the CTA before has it
+        const int per_item = rq.per_item, item = (int)(off / per_item), in_item = (int)(off - (int64_t)item * per_item);
+        if (whole_items && in_item > 0) {                                // the CTA before has it
             at += per_item - in_item;
             off += per_item - in_item;
             continue;
         }
-        const int run = p.whole_items ? per_item : (int)min64(per_item - in_item, end - at);      // of the share inside this item
-        const int first_tile = max(0, in_item - ATT_ITEM_COST), n_tiles = in_item + run - ATT_ITEM_COST - first_tile;
+        const int run = whole_items ? per_item : (int)min64(per_item - in_item, end - at);      // of the share inside this item
+        int first_tile = whole_items ? 0 : max(0, in_item - ATT_ITEM_COST), n_tiles = whole_items ? rq.tiles : in_item + run - ATT_ITEM_COST - first_tile;
         if (n_tiles <= 0) {                                                // nothing but the fixed cost: the next CTA begins the item
             at += run;
             off += run;
             continue;
+        }
+        if (CLUSTER) {                                                     // the CTA's part of them, which may be none
+            first_tile = rq.tiles * (int)rank / p.cluster;
+            n_tiles = rq.tiles * (int)(rank + 1) / p.cluster - first_tile;
         }
         const int64_t item_at = at - in_item;                              // where the item begins
         const int h = item / rq.col_tiles, col0 = (item - h * rq.col_tiles) * 8 * NQ;
@@ -561,13 +596,22 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         const bool whole = first_tile == 0 && n_tiles == rq.tiles;
         const int place = first_tile > 0 ? 0 : 1;
         const int64_t part = ((int64_t)blockIdx.x * 2 + place) * (8 * NQ);
-        float* buf = reinterpret_cast<float*>(smem);                       // [warp][8][D + 4]
+        float* buf = reinterpret_cast<float*>(smem);                       // [warp][8 NQ][D + 4]
         constexpr int LD = D + 4;
-        static_assert(ATT_WARPS * 8 * LD * 4 <= att_ring_bytes(D), "the join fits in the ring");
+        static_assert(ATT_WARPS * 8 * NQ * LD * 4 <= att_ring_bytes(D), "the join fits in the ring");
         const float S_v = load_global(a.s_v + h);
+        auto store = [&](int col, int d, float4 x, float M, float L) {
+            if (col >= cols) return;
+            const int i = (int)divu32((uint32_t)col, p.dv_group), hq = h * a.group + (col - i * a.group);
+            const int64_t t = rq.first + i;
+            const float f = L == 0.0f ? 0.0f : S_v / L;
+            *reinterpret_cast<uint2*>(a.out + t * a.o_token + (int64_t)hq * a.o_head + d) =
+                make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+            if (a.lse && d == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
+        };
+        __syncthreads();                                                   // ring no longer read; s_m, s_l written
 #pragma unroll
-        for (int nq = 0; nq < NQ; ++nq) {
-            __syncthreads();                                               // ring (or buffer) no longer read; s_m, s_l written
+        for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int c = nq * 8 + 2 * t4 + j;
@@ -575,38 +619,64 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
 #pragma unroll
                 for (int w = 1; w < ATT_WARPS; ++w) M = fmaxf(M, s_m[w][c]);
                 const float f = m[nq][j] == -INFINITY ? 0.0f : ex2(m[nq][j] - M);
-                float* dst = buf + (warp * 8 + 2 * t4 + j) * LD + g * (D / 8);
+                float* dst = buf + (warp * 8 * NQ + c) * LD + g * (D / 8);
 #pragma unroll
                 for (int mt = 0; mt < MT; mt += 2)
                     *reinterpret_cast<float4*>(dst + 2 * mt) = make_float4(o[nq][mt][j] * f, o[nq][mt][2 + j] * f, o[nq][mt + 1][j] * f, o[nq][mt + 1][2 + j] * f);
             }
-            __syncthreads();
-            for (int e = tid; e < 8 * (D / 4); e += ATT_THREADS) {
-                const int c = e / (D / 4), d = (e - c * (D / 4)) * 4, cc = nq * 8 + c, col = col0 + cc;
-                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float M = -INFINITY, L = 0.0f;
+        __syncthreads();
+        for (int e = tid; e < 8 * NQ * (D / 4); e += ATT_THREADS) {
+            const int c = e / (D / 4), d = (e - c * (D / 4)) * 4;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float M = -INFINITY, L = 0.0f;
 #pragma unroll
-                for (int w = 0; w < ATT_WARPS; ++w) M = fmaxf(M, s_m[w][cc]);
+            for (int w = 0; w < ATT_WARPS; ++w) M = fmaxf(M, s_m[w][c]);
 #pragma unroll
-                for (int w = 0; w < ATT_WARPS; ++w) {
-                    const float4 v = *reinterpret_cast<const float4*>(buf + (w * 8 + c) * LD + d);
-                    x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
-                    L = __fmaf_rn(s_l[w][cc], s_m[w][cc] == -INFINITY ? 0.0f : ex2(s_m[w][cc] - M), L);
-                }
-                if (!whole) {
-                    *reinterpret_cast<float4*>(p.part_o + (part + cc) * D + d) = x;
-                    if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (part + cc) * 2) = make_float2(M, L);
-                } else if (col < cols) {
-                    const int i = (int)divu32((uint32_t)col, p.dv_group), hq = h * a.group + (col - i * a.group);
-                    const int64_t t = rq.first + i;
-                    const float f = L == 0.0f ? 0.0f : S_v / L;
-                    *reinterpret_cast<uint2*>(a.out + t * a.o_token + (int64_t)hq * a.o_head + d) =
-                        make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-                    if (a.lse && d == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
-                }
+            for (int w = 0; w < ATT_WARPS; ++w) {
+                const float4 v = *reinterpret_cast<const float4*>(buf + (w * 8 * NQ + c) * LD + d);
+                x.x += v.x; x.y += v.y; x.z += v.z; x.w += v.w;
+                L = __fmaf_rn(s_l[w][c], s_m[w][c] == -INFINITY ? 0.0f : ex2(s_m[w][c] - M), L);
+            }
+            if (CLUSTER) {                                                 // in the first warp's place, for the others
+                *reinterpret_cast<float4*>(buf + c * LD + d) = x;
+                if (d == 0) s_ml[c] = make_float2(M, L);
+            } else if (!whole) {
+                *reinterpret_cast<float4*>(p.part_o + (part + c) * D + d) = x;
+                if (d == 0) *reinterpret_cast<float2*>(p.part_ml + (part + c) * 2) = make_float2(M, L);
+            } else {
+                store(col0 + c, d, x, M, L);
             }
         }
-        if (first_tile == 0 && tid == 0 && !p.whole_items && (p.by_item || !whole)) {
+        if (CLUSTER) {                                                     // join of the cluster, in the order of its CTAs
+            cluster_barrier();
+            for (int e = (int)rank * ATT_THREADS + tid; e < 8 * NQ * (D / 4); e += ATT_THREADS * p.cluster) {
+                const int c = e / (D / 4), d = (e - c * (D / 4)) * 4;
+                float2 ml[ATT_MAX_CLUSTER];
+                float4 v[ATT_MAX_CLUSTER], x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float M = -INFINITY, L = 0.0f;
+#pragma unroll
+                for (int k = 0; k < ATT_MAX_CLUSTER; ++k) {                // beyond the last CTA its place again, with nothing in it
+                    ml[k] = load_there2(there_u32(s_ml + c, min(k, p.cluster - 1)));
+                    v[k] = load_there4(there_u32(buf + c * LD + d, min(k, p.cluster - 1)));
+                    if (k >= p.cluster) {
+                        ml[k] = make_float2(-INFINITY, 0.0f);
+                        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < ATT_MAX_CLUSTER; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+                for (int k = 0; k < ATT_MAX_CLUSTER; ++k) {
+                    const float f = ml[k].x == -INFINITY ? 0.0f : ex2(ml[k].x - M);
+                    L = __fmaf_rn(ml[k].y, f, L);
+                    x.x = __fmaf_rn(v[k].x, f, x.x); x.y = __fmaf_rn(v[k].y, f, x.y);
+                    x.z = __fmaf_rn(v[k].z, f, x.z); x.w = __fmaf_rn(v[k].w, f, x.w);
+                }
+                store(col0 + c, d, x, M, L);
+            }
+            cluster_barrier();                                             // before anybody writes its ring again, or leaves
+        }
+        if (first_tile == 0 && tid == 0 && !whole_items && (p.by_item || !whole)) {
             Piece pc{(int)blockIdx.x, 0, rq.first, h, col0, cols};
             if (!whole) pc.count = (int)((item_at + per_item - 1) / share) - (int)blockIdx.x + 1;
             p.pieces[p.by_item ? item0 + item : (int)blockIdx.x] = pc;
@@ -699,29 +769,40 @@ __global__ void __launch_bounds__(JOIN_THREADS) kv_attention_join_kernel(const _
     if (a.lse && lane == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
 }
 
-template <int D, int NQ>
-cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
+template <int D, int NQ, bool CLUSTER>
+cudaError_t launch_tiles(const AttParams& p, int64_t grid, cudaStream_t stream) {
     static PerDevice pd;
     int unused = 0;
-    cudaError_t e = per_device_once(pd, unused, [](int&) {
-        return cudaFuncSetAttribute(kv_attention_kernel<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, att_ring_bytes(D));
+    const cudaError_t e = per_device_once(pd, unused, [](int&) {
+        return cudaFuncSetAttribute(kv_attention_kernel<D, NQ, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, att_ring_bytes(D));
     });
     if (e != cudaSuccess) return e;
+    return launch_chained(kv_attention_kernel<D, NQ, CLUSTER>, dim3((unsigned)grid), ATT_THREADS, att_ring_bytes(D),
+                          CLUSTER ? (unsigned)p.cluster : 0u, stream, p);
+}
+
+template <int D, int NQ>
+cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
     const KvAttentionArgs& a = p.a;
     const int ctas = num_sms * att_ctas(D, NQ);
     const int64_t items = (int64_t)a.R * a.kv_heads * ((a.max_q * (int64_t)a.group + 8 * NQ - 1) / (8 * NQ));
     p.by_item = items <= ctas;
-    // Short contexts (by the table's width) are not split: one launch instead of two.  On the device that is quicker to
-    // about 600 positions (512: 7.6 instead of 8.4 us, 1000: 10.9 instead of 8.6); with the host's 11.0 instead of 12.8 us a
-    // call it is in a stream of calls to about 900.
-    p.whole_items = a.width * a.page <= ATT_WHOLE_TOKENS;
+    // Short contexts (by the table's width) are not split over the GPU: one launch instead of two.  Where the items leave room,
+    // each has a cluster of 2 to 8 CTAs, whose meeting takes 1.3 us: one request of 256 positions 6.9 us with one and 6.1
+    // without, 512 6.7 and 7.6, 2048 7.9 (split over the GPU 9.0), 4900 10.5 (10.2, and 2 us more of the host's time); 16
+    // requests to 860 positions 11.2 with clusters of 2, 13.5 without.  Without clusters, 64 requests to 512 positions take 15.4
+    // us and split 16.5, to 860 20.8 and 20.6.
+    p.cluster = 1;
+    while (a.width * a.page > ATT_CLUSTER_TOKENS && p.cluster < ATT_MAX_CLUSTER && items * p.cluster * 2 <= ctas) p.cluster *= 2;
+    p.whole_items = a.width * a.page <= (p.cluster == 1 ? ATT_WHOLE_TOKENS : ATT_WHOLE_CLUSTER_TOKENS * p.cluster);
+    if (!p.whole_items) p.cluster = 1;
     p.n_pieces = (int)(p.by_item ? items : ctas);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     p.pieces = reinterpret_cast<Piece*>(ws);
     p.part_ml = reinterpret_cast<float*>(ws + (int64_t)num_sms * ATT_MAX_CTAS_PER_SM * sizeof(Piece));
     p.part_o = p.part_ml + (int64_t)ctas * 2 * (8 * NQ) * 2;
-    const int64_t grid_x = p.whole_items ? min64(items, ctas) : ctas;
-    e = launch_chained(kv_attention_kernel<D, NQ>, dim3((unsigned)grid_x), ATT_THREADS, att_ring_bytes(D), 0, stream, p);
+    if (p.cluster > 1) return launch_tiles<D, NQ, true>(p, items * p.cluster, stream);
+    const cudaError_t e = launch_tiles<D, NQ, false>(p, p.whole_items ? min64(items, ctas) : ctas, stream);
     if (e != cudaSuccess || p.whole_items) return e;
     const bool shared = items * 8 <= ctas;
     const dim3 grid((unsigned)p.n_pieces, shared ? 8 * NQ : 8 * NQ * 32 / JOIN_THREADS);

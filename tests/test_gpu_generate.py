@@ -345,6 +345,48 @@ def test_attention_more_items_than_ctas(mx, group, drafts):
                     s_k, s_v, 0.125, 16)
 
 
+@pytest.mark.parametrize("positions", [500, 1200, 40000])
+@pytest.mark.parametrize("lens,new,heads,kv,D,page,window", ATTENTION_CASES)
+def test_attention_table_widths(mx, lens, new, heads, kv, D, page, window, positions):
+    """Contexts divided inside a cluster, where short ones leave some of its CTAs nothing, and split over the GPU."""
+    q, q_start, lens, table, cache, s_k, s_v = attention_case(1, lens, new, heads, kv, D, page)
+    check_attention(mx, q, q_start, lens, wide(table, positions // page), cache, s_k, s_v, D ** -0.5, page, window)
+
+
+@pytest.mark.parametrize("requests", [5, 9, 18, 27])
+def test_attention_clusters_of_every_size(mx, requests):
+    """Ragged batches of 8 kv heads, an idle request and a short one in each, with one and with several new tokens."""
+    rng = np.random.default_rng(requests)
+    lens = rng.integers(1, 420, requests)
+    lens[[1, 3, 4]] = 0, 415, 1
+    for most in (1, 3):
+        new = np.minimum(lens, rng.integers(1, most + 1, requests))
+        q, q_start, lens_, table, cache, s_k, s_v = attention_case(21, lens, new, 32, 8, 64, 16)
+        for window in (0, 40):
+            check_attention(mx, q, q_start, lens_, table, cache, s_k, s_v, 0.125, 16, window)
+
+
+def test_attention_cluster_nan_key_and_value(mx):
+    """One bad scale in one CTA's part of a context: a key's reaches all of its head, a value's its block of 16 only."""
+    L, D, kv, group = 900, 128, 2, 4
+    q, q_start, lens, table, cache, s_k, s_v = attention_case(22, [L], [1], kv * group, kv, D, 16)
+    good, _ = check_attention(mx, q, q_start, lens, table, cache, s_k, s_v, 0.09, 16)
+    ws = torch.empty(mx.kv_attention_workspace_bytes(D), dtype=torch.uint8, device=DEV)
+    for tok in (0, 450, L - 1):
+        rec = int(table[0, tok // 16])
+        for at, sees in ((8 * D + (tok % 16) * (D // 16), slice(None)), (17 * D + 3 * 16 + ref.v_scale_position(tok % 16), slice(48, 64))):
+            hurt = cache.clone()
+            hurt[rec, 1, 0, at] = 0x7F
+            out = torch.zeros_like(good)
+            mx.mx_nvfp4_kv_attention(q, i32(q_start), i32(lens), i32(table), hurt, f32(s_k), f32(s_v), 0.09, 1, out, ws)
+            done(mx)
+            want = torch.zeros(D, dtype=torch.bool, device=DEV)
+            want[sees] = True
+            assert torch.equal(out[0, :group], good[0, :group])
+            assert torch.equal(out[0, group:].isnan(), want.expand(group, D))
+            assert torch.equal(out[0, group:][:, ~want], good[0, group:][:, ~want])
+
+
 def test_attention_many_ragged_requests(mx):
     rng = np.random.default_rng(2)
     lens = rng.integers(0, 120, 150)
