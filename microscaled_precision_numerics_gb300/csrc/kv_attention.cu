@@ -49,9 +49,9 @@ constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_TILE = 32;                 // tokens of a warp's step: two records
 constexpr int ATT_ITEM_COST = 12;             // what an item costs besides its tiles, in tiles
 constexpr int ATT_MIN_SHARE = 8;             // smallest share of a CTA: two steps a warp
-// Longest tables whose items are not split over the GPU: one CTA an item; a cluster, for each of its CTAs.  From
-// ATT_CLUSTER_TOKENS on an item has a cluster where the GPU has room.
-constexpr int64_t ATT_WHOLE_TOKENS = 896, ATT_WHOLE_CLUSTER_TOKENS = 640, ATT_CLUSTER_TOKENS = 384;
+// Tables beyond which items have a cluster where the GPU has room, and longest tables whose items are not split over the GPU:
+// more items than CTAs, or clusters of 4 and 8 (for each CTA of the cluster), or else by the share of the GPU that the items fill.
+constexpr int64_t ATT_CLUSTER_TOKENS = 384, ATT_WHOLE_TOKENS = 896, ATT_WHOLE_CLUSTER_TOKENS = 512, ATT_WHOLE_FULL_TOKENS = 1920;
 constexpr float ATT_SLACK = 8.0f;            // the running maximum may lag by 2^8 (P stays below 2^8 in FP16)
 
 __host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 4 : 2; }
@@ -769,40 +769,55 @@ __global__ void __launch_bounds__(JOIN_THREADS) kv_attention_join_kernel(const _
     if (a.lse && lane == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
 }
 
-template <int D, int NQ, bool CLUSTER>
-cudaError_t launch_tiles(const AttParams& p, int64_t grid, cudaStream_t stream) {
-    static PerDevice pd;
-    int unused = 0;
-    const cudaError_t e = per_device_once(pd, unused, [](int&) {
-        return cudaFuncSetAttribute(kv_attention_kernel<D, NQ, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, att_ring_bytes(D));
-    });
-    if (e != cudaSuccess) return e;
-    return launch_chained(kv_attention_kernel<D, NQ, CLUSTER>, dim3((unsigned)grid), ATT_THREADS, att_ring_bytes(D),
-                          CLUSTER ? (unsigned)p.cluster : 0u, stream, p);
-}
-
 template <int D, int NQ>
 cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
+    static PerDevice pd;
+    static int clusters[MX_MAX_DEVICES][ATT_MAX_CLUSTER + 1];                 // that the device runs at once, by their CTAs
+    int dev = 0;
+    cudaError_t e = per_device_once(pd, dev, [](int& value) {
+        cudaError_t s = cudaGetDevice(&value);
+        if (s == cudaSuccess) s = cudaFuncSetAttribute(kv_attention_kernel<D, NQ, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, att_ring_bytes(D));
+        if (s == cudaSuccess) s = cudaFuncSetAttribute(kv_attention_kernel<D, NQ, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, att_ring_bytes(D));
+        for (int c = 2; c <= ATT_MAX_CLUSTER && s == cudaSuccess; c *= 2) {
+            cudaLaunchAttribute at{};
+            at.id = cudaLaunchAttributeClusterDimension;
+            at.val.clusterDim = {(unsigned)c, 1, 1};
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3((unsigned)c);
+            cfg.blockDim = dim3(ATT_THREADS);
+            cfg.dynamicSmemBytes = att_ring_bytes(D);
+            cfg.attrs = &at;
+            cfg.numAttrs = 1;
+            s = cudaOccupancyMaxActiveClusters(&clusters[value][c], kv_attention_kernel<D, NQ, true>, &cfg);
+        }
+        return s;
+    });
+    if (e != cudaSuccess) return e;
     const KvAttentionArgs& a = p.a;
     const int ctas = num_sms * att_ctas(D, NQ);
-    const int64_t items = (int64_t)a.R * a.kv_heads * ((a.max_q * (int64_t)a.group + 8 * NQ - 1) / (8 * NQ));
+    const int64_t items = (int64_t)a.R * a.kv_heads * ((a.max_q * (int64_t)a.group + 8 * NQ - 1) / (8 * NQ)), table = a.width * a.page;
     p.by_item = items <= ctas;
     // Short contexts (by the table's width) are not split over the GPU: one launch instead of two.  Where the items leave room,
     // each has a cluster of 2 to 8 CTAs, whose meeting takes 1.3 us: one request of 256 positions 6.9 us with one and 6.1
-    // without, 512 6.7 and 7.6, 2048 7.9 (split over the GPU 9.0), 4900 10.5 (10.2, and 2 us more of the host's time); 16
-    // requests to 860 positions 11.2 with clusters of 2, 13.5 without.  Without clusters, 64 requests to 512 positions take 15.4
-    // us and split 16.5, to 860 20.8 and 20.6.
+    // without, 512 6.7 and 7.6; 2048 7.9 and split over the GPU 9.0, 5000 10.6 and 10.4 (and 2 us more of the host's time).
+    // Clusters that wait for room cost more than the split: 56 of 8 CTAs 16.5 us instead of 12.3.  The fuller the GPU with
+    // unsplit items, the longer they may be: 320 items to 1000 positions 16.2 unsplit and 16.9 split, to 1700 23.5 and 20.7; 456
+    // items 17.0 and 20.3, 23.5 and 24.8.  512 items, more than CTAs, to 512 positions 15.4 and 16.5, to 1000 22.9 and 22.1.
     p.cluster = 1;
-    while (a.width * a.page > ATT_CLUSTER_TOKENS && p.cluster < ATT_MAX_CLUSTER && items * p.cluster * 2 <= ctas) p.cluster *= 2;
-    p.whole_items = a.width * a.page <= (p.cluster == 1 ? ATT_WHOLE_TOKENS : ATT_WHOLE_CLUSTER_TOKENS * p.cluster);
+    while (table > ATT_CLUSTER_TOKENS && p.cluster < ATT_MAX_CLUSTER && items <= clusters[dev][2 * p.cluster]) p.cluster *= 2;
+    const int64_t limit = !p.by_item ? ATT_WHOLE_TOKENS
+                        : p.cluster > 2 ? ATT_WHOLE_CLUSTER_TOKENS * p.cluster : max64(ATT_CLUSTER_TOKENS, ATT_WHOLE_FULL_TOKENS * items * p.cluster / ctas);
+    p.whole_items = table <= limit;
     if (!p.whole_items) p.cluster = 1;
     p.n_pieces = (int)(p.by_item ? items : ctas);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     p.pieces = reinterpret_cast<Piece*>(ws);
     p.part_ml = reinterpret_cast<float*>(ws + (int64_t)num_sms * ATT_MAX_CTAS_PER_SM * sizeof(Piece));
     p.part_o = p.part_ml + (int64_t)ctas * 2 * (8 * NQ) * 2;
-    if (p.cluster > 1) return launch_tiles<D, NQ, true>(p, items * p.cluster, stream);
-    const cudaError_t e = launch_tiles<D, NQ, false>(p, p.whole_items ? min64(items, ctas) : ctas, stream);
+    if (p.cluster > 1)
+        return launch_chained(kv_attention_kernel<D, NQ, true>, dim3((unsigned)(items * p.cluster)), ATT_THREADS, att_ring_bytes(D), (unsigned)p.cluster, stream, p);
+    const int64_t grid_x = p.whole_items ? min64(items, ctas) : ctas;
+    e = launch_chained(kv_attention_kernel<D, NQ, false>, dim3((unsigned)grid_x), ATT_THREADS, att_ring_bytes(D), 0, stream, p);
     if (e != cudaSuccess || p.whole_items) return e;
     const bool shared = items * 8 <= ctas;
     const dim3 grid((unsigned)p.n_pieces, shared ? 8 * NQ : 8 * NQ * 32 / JOIN_THREADS);
