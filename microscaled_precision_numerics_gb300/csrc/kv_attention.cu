@@ -23,7 +23,7 @@
 // down to 2^-29 of it stays exact.  P enters as FP16: 2^-12 relative rounding, against 2^-9 of the BF16 output.
 //
 // Split: all (request, kv head, column tile) items lie end to end, each as its tiles of 32 positions and a fixed cost of
-// ATT_ITEM_COST tiles (look-ups, queries, the join of the warps; without it eight requests with one very short among them
+// att_item_cost tiles (look-ups, queries, the join of the warps; without it eight requests with one very short among them
 // took 32 us instead of 14), and every CTA takes an equal run of that line.  A run's first and last item may be shared
 // with neighbours; those leave (maximum, sum, output) pieces in the workspace and a second kernel joins them in CTA order.
 // Short contexts are not split so: a CTA takes an item, or a cluster of up to 8 CTAs divides it and joins its parts through
@@ -47,7 +47,9 @@ namespace {
 constexpr int ATT_WARPS = 4;
 constexpr int ATT_THREADS = 32 * ATT_WARPS;
 constexpr int ATT_TILE = 32;                 // tokens of a warp's step: two records
-constexpr int ATT_ITEM_COST = 12;             // what an item costs besides its tiles, in tiles
+// What an item costs besides its tiles, in tiles: 3.5 us, in which a CTA does 12 tiles for D = 128 and more for 64 (24 requests with
+// drafts 18.9 us with 16 and 19.9 with 12; for 256 12 as well, 8 was 1 % slower).
+__host__ __device__ constexpr int att_item_cost(int D) { return D == 64 ? 16 : 12; }
 constexpr int ATT_MIN_SHARE = 8;             // smallest share of a CTA: two steps a warp
 // Tables beyond which items have a cluster where the GPU has room, and longest tables whose items are not split over the GPU:
 // more items than CTAs, or clusters of 4 and 8 (for each CTA of the cluster), or else by the share of the GPU that the items fill.
@@ -132,7 +134,7 @@ struct Request {
     int first, count, len, tile0, tiles, col_tiles, per_item;             // per_item: cost of an item
     __device__ int64_t cost(int kv_heads) const { return (int64_t)per_item * col_tiles * kv_heads; }
 };
-template <int NQ>
+template <int D, int NQ>
 __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r, bool one_each) {
     Request q;
     q.first = load_global(a.q_start + r);
@@ -145,7 +147,7 @@ __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r, b
     const uint32_t held = (uint32_t)min64(q.len, a.width * a.page);       // positions that the table has pages for
     q.tiles = max(1, (int)((held + ATT_TILE - 1) / ATT_TILE) - q.tile0);
     q.col_tiles = (q.count * a.group + 8 * NQ - 1) / (8 * NQ);
-    q.per_item = one_each ? 1 : q.tiles + ATT_ITEM_COST;
+    q.per_item = one_each ? 1 : q.tiles + att_item_cost(D);
     return q;
 }
 
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
     int64_t mine = 0;
     int my_items = 0;
     for (int r = r0; r < min(a.R, r0 + per); ++r) {
-        const Request q = request_of<NQ>(a, r, one_each);
+        const Request q = request_of<D, NQ>(a, r, one_each);
         mine += q.cost(a.kv_heads);
         my_items += q.col_tiles * a.kv_heads;
     }
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         int64_t at = excl;
         int r = r0, it = excl_items;
         for (;; ++r) {
-            const Request q = request_of<NQ>(a, r, one_each);
+            const Request q = request_of<D, NQ>(a, r, one_each);
             const int64_t w = q.cost(a.kv_heads);
             if (begin < at + w) break;
             at += w;
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
 
     int r = s_r, item0 = s_item;             // request; number of its first item
     int64_t off = s_off;                     // place inside the request
-    Request rq = request_of<NQ>(a, r, one_each);
+    Request rq = request_of<D, NQ>(a, r, one_each);
     uint8_t* ring = smem + warp * (STAGES * STAGE_BYTES);
     const uint32_t ring_u32 = (uint32_t)__cvta_generic_to_shared(ring);
 
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         while (off >= rq.cost(a.kv_heads)) {                               // next request with work
             off -= rq.cost(a.kv_heads);
             item0 += rq.col_tiles * a.kv_heads;
-            rq = request_of<NQ>(a, ++r, one_each);
+            rq = request_of<D, NQ>(a, ++r, one_each);
         }
         const int per_item = rq.per_item, item = (int)(off / per_item), in_item = (int)(off - (int64_t)item * per_item);
         if (whole_items && in_item > 0) {                                // the CTA before has it
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             continue;
         }
         const int run = whole_items ? per_item : (int)min64(per_item - in_item, end - at);      // of the share inside this item
-        int first_tile = whole_items ? 0 : max(0, in_item - ATT_ITEM_COST), n_tiles = whole_items ? rq.tiles : in_item + run - ATT_ITEM_COST - first_tile;
+        int first_tile = whole_items ? 0 : max(0, in_item - att_item_cost(D)), n_tiles = whole_items ? rq.tiles : in_item + run - att_item_cost(D) - first_tile;
         if (n_tiles <= 0) {                                                // nothing but the fixed cost: the next CTA begins the item
             at += run;
             off += run;
@@ -794,8 +796,13 @@ cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
     });
     if (e != cudaSuccess) return e;
     const KvAttentionArgs& a = p.a;
-    const int ctas = num_sms * att_ctas(D, NQ);
     const int64_t items = (int64_t)a.R * a.kv_heads * ((a.max_q * (int64_t)a.group + 8 * NQ - 1) / (8 * NQ)), table = a.width * a.page;
+    // Few items: all warps of a CTA join one column's pieces, and four places for CTAs stay empty.  Behind the kernel before, whose
+    // last CTAs still hold registers and shared memory, some SMs take one CTA less, and what waits for them begins when others
+    // end (one request of 130944 tokens, 72 tiles for each of 456 CTAs: 41.7 us, with 452 CTAs 34.7).
+    const int resident = num_sms * att_ctas(D, NQ);
+    const bool shared = items * 8 <= resident;
+    const int ctas = shared ? max(1, resident - 4) : resident;
     p.by_item = items <= ctas;
     // Short contexts (by the table's width) are not split over the GPU: one launch instead of two.  Where the items leave room,
     // each has a cluster of 2 to 8 CTAs, whose meeting takes 1.3 us: one request of 256 positions 6.9 us with one and 6.1
@@ -819,7 +826,6 @@ cudaError_t launch_nq(AttParams& p, int num_sms, cudaStream_t stream) {
     const int64_t grid_x = p.whole_items ? min64(items, ctas) : ctas;
     e = launch_chained(kv_attention_kernel<D, NQ, false>, dim3((unsigned)grid_x), ATT_THREADS, att_ring_bytes(D), 0, stream, p);
     if (e != cudaSuccess || p.whole_items) return e;
-    const bool shared = items * 8 <= ctas;
     const dim3 grid((unsigned)p.n_pieces, shared ? 8 * NQ : 8 * NQ * 32 / JOIN_THREADS);
     return shared ? launch_chained(kv_attention_join_kernel<D, true>, grid, JOIN_THREADS, 0, 0, stream, p, 8 * NQ)
                   : launch_chained(kv_attention_join_kernel<D, false>, grid, JOIN_THREADS, 0, 0, stream, p, 8 * NQ);
