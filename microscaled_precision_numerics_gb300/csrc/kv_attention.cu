@@ -32,8 +32,8 @@
 // cp.async each (three stages, or eight warps a CTA, were slower: 75.1 and 84.3 against 73.7 us).
 //
 // Measured on a GB300 (device us, share of the measured copy rate): 64 requests to 8192 tokens, 32 q heads over 8 kv heads, D =
-// 128: 73.0 (75 %; of the scheduler slots 57 % issue, the ALU is busy 49 %, the pipe that HMUL2 and HMMA share 51 %: bound
-// by latency with the 12 warps an SM that the registers leave); one request of 131071 tokens: 34.5 (64 %; about 8 us
+// 128: 72.9 (75 %; of the scheduler slots 57 % issue, the ALU is busy 49 %, the pipe that HMUL2 and HMMA share 51 %: bound
+// by latency with the 12 warps an SM that the registers leave); one request of 131071 tokens: 34.2 (65 %; about 8 us
 // of it are fixed: launch, look-ups, joins); one of 777: 6.8 (latency; 10.0 without clusters).
 #include "mx_internal.h"
 #include "mx_kv.cuh"
@@ -313,15 +313,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             copy_async_commit();
             in_slot = in_slot + 1 == STAGES ? 0 : in_slot + 1;
         };
-#pragma unroll
-        for (int k = 0; k < STAGES - 1; ++k) issue(k);
-
-
-        // ---- Q^T fragments: column g of each eight, elements [t4 * D / 4, + D / 4), as FP16 scaled by a power of two
-        uint32_t qf[NQ][KS][2];
-        float mul[NQ][2], slack[NQ][2];                                    // score -> exponent of two, columns 2 t4, 2 t4 + 1
-        int pos[NQ][2];                                                    // last position they attend to (-1: none)
-        const float S_k = load_global(a.s_k + h);
+        // the queries are fetched while the look-ups are on their way (behind the first copies: 47.4 -> 48.9 us, 64 requests, D = 64)
+        // and made into fragments behind the first copies
+        uint32_t qw[NQ][D / 8];
 #pragma unroll
         for (int nq = 0; nq < NQ; ++nq) {
             const int col = col0 + nq * 8 + g;
@@ -329,13 +323,24 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             const int i = real ? (int)divu32((uint32_t)col, p.dv_group) : 0;
             const int hq = real ? h * a.group + (col - i * a.group) : 0;
             const uint4* src = reinterpret_cast<const uint4*>(a.q + (int64_t)(rq.first + i) * a.q_token + (int64_t)hq * a.q_head + t4 * (D / 4));
-            uint32_t w[D / 8], m2 = 0;
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (real) v = load_global(src + k);
-                w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
+                qw[nq][4 * k] = v.x; qw[nq][4 * k + 1] = v.y; qw[nq][4 * k + 2] = v.z; qw[nq][4 * k + 3] = v.w;
             }
+        }
+        const float S_k = load_global(a.s_k + h);
+#pragma unroll
+        for (int k = 0; k < STAGES - 1; ++k) issue(k);
+
+        // ---- Q^T fragments: column g of each eight, elements [t4 * D / 4, + D / 4), as FP16 scaled by a power of two
+        uint32_t qf[NQ][KS][2];
+        float mul[NQ][2], slack[NQ][2];                                    // score -> exponent of two, columns 2 t4, 2 t4 + 1
+        int pos[NQ][2];                                                    // last position they attend to (-1: none)
+#pragma unroll
+        for (int nq = 0; nq < NQ; ++nq) {
+            uint32_t (&w)[D / 8] = qw[nq], m2 = 0;
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) m2 = absmax_bf16x2_int(m2, w[k]);
             uint32_t amax = fold_halves(m2);
