@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                         for (int j = 0; j < 2; ++j) {
                             top[nq][j] = fmaxf(top[nq][j], s[gr][nq][2 * x + j]);
                         }
-                raise |= top[nq][0] > m[nq][0] + slack[nq][0] || top[nq][1] > m[nq][1] + slack[nq][1];
+                raise |= top[nq][0] - m[nq][0] > slack[nq][0] || top[nq][1] - m[nq][1] > slack[nq][1];
             }
             if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
@@ -490,13 +490,14 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             uint32_t pf[2][NQ][2];                                         // P as B fragments
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
-                // 2^(mul s - mul m); a column with nothing so far has only -inf, to which 0 is added
-                const float m0 = m[nq][0] == -INFINITY ? 0.0f : -m[nq][0] * mul[nq][0], m1 = m[nq][1] == -INFINITY ? 0.0f : -m[nq][1] * mul[nq][1];
+                // 2^(mul (s - m)), the difference first: the products of large scores (2^31 and more) would be rounded by more than FP16
+                // has room for.  A column with nothing so far has only -inf, from which 0 is taken.
+                const float m0 = m[nq][0] == -INFINITY ? 0.0f : m[nq][0], m1 = m[nq][1] == -INFINITY ? 0.0f : m[nq][1];
 #pragma unroll
                 for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float p0 = ex2(__fmaf_rn(s[gr][nq][2 * x], mul[nq][0], m0)), p1 = ex2(__fmaf_rn(s[gr][nq][2 * x + 1], mul[nq][1], m1));
+                        const float p0 = ex2((s[gr][nq][2 * x] - m0) * mul[nq][0]), p1 = ex2((s[gr][nq][2 * x + 1] - m1) * mul[nq][1]);
                         l[nq][0] += p0;
                         l[nq][1] += p1;
                         pf[gr][nq][x] = transpose_8x8(pack_f16x2(p0, p1));

@@ -1,0 +1,58 @@
+"""GPU: attention over the NVFP4 cache at the edges of its arithmetic and arguments.  Against the 64-bit reference; bounds as in
+test_gpu_generate.py, with the term of small probabilities derived anew where it is used."""
+import numpy as np
+import pytest
+import torch
+
+import generate_ref as ref
+from gpu_util import DEV, bf16_dev, to_np_u16
+from test_gpu_generate import done, f32, i32, mx, wide    # noqa: F401  (mx is the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def sink_case(D, L, new, group, kv, page, nats, *sinks, zero=True):
+    """One request: keys are zero but for the positions `sinks`, which score `nats` (a little more from head to head); their values
+    are zero and all others are positive, so the output is made of small probabilities alone."""
+    rng = np.random.default_rng(L + D)
+    width = -(-L // page)
+    codes_v, one = rng.integers(1, 8, (width * page, kv, D)).astype(np.uint8), 0x38           # 0x38: E4M3 1.0
+    if zero:
+        codes_v[list(sinks)] = 0
+    codes_k = np.zeros_like(codes_v)
+    codes_k[list(sinks)] = 6                                                                  # 4.0
+    cache = np.zeros((width, kv, page // 16, 18 * D), np.uint8)
+    order = rng.permutation(width)
+    for j in range(width * page):
+        r, i = cache[order[j // page], :, j % page // 16], j % 16
+        r[:, i * (D // 2):(i + 1) * (D // 2)] = ref.pack(codes_k[j])
+        r[:, 8 * D + i * (D // 16):8 * D + (i + 1) * (D // 16)] = one
+        r[:, 9 * D + i * (D // 2):9 * D + (i + 1) * (D // 2)] = ref.pack(codes_v[j])
+        r[:, 17 * D + np.arange(D // 16) * 16 + ref.v_scale_position(i)] = one
+    scale = D ** -0.5
+    s_k, s_v = np.full(kv, nats / (scale * D * 4), np.float32), np.full(kv, 1 / 6, np.float32)
+    q = np.ones((new, kv * group, D)) * (1 + np.arange(kv * group) / 64)[None, :, None]
+    return bf16_dev(ref.bf16_bits(q)), [0, new], [L], order[None, :], torch.from_numpy(cache).to(DEV), s_k, s_v, scale
+
+
+SINKS = [(64, 384, 1, 4, 1, 16, 0), (64, 384, 5, 4, 1, 32, 0), (128, 383, 1, 8, 2, 16, 0), (128, 380, 3, 4, 2, 16, 0), (256, 384, 1, 2, 1, 16, 0),
+         (256, 384, 5, 2, 1, 16, 0),
+         (128, 1000, 1, 4, 1, 16, 0),                                       # divided inside a cluster
+         (64, 2000, 2, 4, 2, 16, 20000)]                                    # split over the GPU
+
+
+@pytest.mark.parametrize("nats", [3e4, 2e7, 1e10, 1e20])
+@pytest.mark.parametrize("D,L,new,group,kv,page,more", SINKS)
+def test_large_scores(mx, D, L, new, group, kv, page, more, nats):       # noqa: F811
+    """Two equal keys whose scores are so large that their products with scale and log2 e differ by rounding alone: each
+    has half of the weight all the same, so the output is the mean of two values, off by 2^-11 of it (P) and BF16's rounding."""
+    q, q_start, lens, table, cache, s_k, s_v, scale = sink_case(D, L, new, group, kv, page, nats, 5, L // 2, zero=False)
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], float("nan"), dtype=torch.float32, device=DEV)
+    ws = torch.empty(mx.kv_attention_workspace_bytes(D), dtype=torch.uint8, device=DEV)
+    mx.mx_nvfp4_kv_attention(q, i32(q_start), i32(lens), i32(wide(table, more // page)), cache, f32(s_k), f32(s_v), scale, new, out, ws, lse=lse)
+    done(mx)
+    o, l, _, _ = ref.attention(ref.bf16_value(to_np_u16(q)).astype(np.float64), q_start, lens, table, cache.cpu().numpy(), s_k, s_v, scale, page)
+    assert (np.abs(out.float().cpu().numpy() - o) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(o)).all()
+    # FP32: the sum of D products, three scalings, the product with ln 2
+    assert (np.abs(lse.cpu().numpy() - l) <= (D + 6) * 2.0 ** -24 * np.abs(l)).all()
