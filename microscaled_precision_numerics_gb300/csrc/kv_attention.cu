@@ -20,7 +20,10 @@
 //           are interleaved as packed codes (4 logic instructions for 32 codes), after which one conversion gives
 //           the pair (token, next token) of a dimension.  P^T comes out of S^T's accumulators by one 8x8 transpose.
 // Q enters as FP16, scaled by a power of two per row so that its largest element lies in [2^15, 2^16): every BF16 value
-// down to 2^-29 of it stays exact.  P enters as FP16: 2^-12 relative rounding, against 2^-9 of the BF16 output.
+// down to 2^-29 of it stays exact.  P enters as FP16, relative to the running maximum and times 2^7, which FP16 has room for with
+// a maximum that lags by 2^8: off by 2^-11 relatively at most, against 2^-8 of the BF16 output, and below 2^-21 by 2^-32
+// absolutely (without the 2^7 by 2^-25: the tail beside one strong position came out up to a third off).  The sum of P that
+// divides the output is FP32 and of P before this rounding.
 //
 // Split: all (request, kv head, column tile) items lie end to end, each as its tiles of 32 positions and a fixed cost of
 // att_item_cost tiles (look-ups, queries, the join of the warps; without it eight requests with one very short among them
@@ -54,7 +57,8 @@ constexpr int ATT_MIN_SHARE = 8;             // smallest share of a CTA: two ste
 // Tables beyond which items have a cluster where the GPU has room, and longest tables whose items are not split over the GPU:
 // more items than CTAs, or clusters of 4 and 8 (for each CTA of the cluster), or else by the share of the GPU that the items fill.
 constexpr int64_t ATT_CLUSTER_TOKENS = 384, ATT_WHOLE_TOKENS = 896, ATT_WHOLE_CLUSTER_TOKENS = 512, ATT_WHOLE_FULL_TOKENS = 1920;
-constexpr float ATT_SLACK = 8.0f;            // the running maximum may lag by 2^8 (P stays below 2^8 in FP16)
+constexpr float ATT_SLACK = 8.0f;            // the running maximum may lag by 2^8
+constexpr float ATT_P_SHIFT = 7.0f;          // P is held times 2^7: at most 2^15 in FP16
 
 __host__ __device__ constexpr int att_stages(int D) { return D == 64 ? 4 : 2; }
 // Resident CTAs per SM: by registers (O holds D / 4 * NQ of them) and by shared memory.
@@ -490,14 +494,14 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             uint32_t pf[2][NQ][2];                                         // P as B fragments
 #pragma unroll
             for (int nq = 0; nq < NQ; ++nq) {
-                // 2^(mul (s - m)), the difference first: the products of large scores (2^31 and more) would be rounded by more than FP16
+                // 2^(mul (s - m) + 7), the difference first: the products of large scores (2^31 and more) would be rounded by more than FP16
                 // has room for.  A column with nothing so far has only -inf, from which 0 is taken.
                 const float m0 = m[nq][0] == -INFINITY ? 0.0f : m[nq][0], m1 = m[nq][1] == -INFINITY ? 0.0f : m[nq][1];
 #pragma unroll
                 for (int gr = 0; gr < 2; ++gr)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float p0 = ex2((s[gr][nq][2 * x] - m0) * mul[nq][0]), p1 = ex2((s[gr][nq][2 * x + 1] - m1) * mul[nq][1]);
+                        const float p0 = ex2(__fmaf_rn(s[gr][nq][2 * x] - m0, mul[nq][0], ATT_P_SHIFT)), p1 = ex2(__fmaf_rn(s[gr][nq][2 * x + 1] - m1, mul[nq][1], ATT_P_SHIFT));
                         l[nq][0] += p0;
                         l[nq][1] += p1;
                         pf[gr][nq][x] = transpose_8x8(pack_f16x2(p0, p1));
@@ -591,7 +595,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                if (m[nq][j] != -INFINITY) m[nq][j] *= mul[nq][j];           // from here on an exponent of two
+                if (m[nq][j] != -INFINITY) m[nq][j] = __fmaf_rn(m[nq][j], mul[nq][j], -ATT_P_SHIFT);       // from here on the exponent of two of l and o
                 float v = l[nq][j];
                 v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
                 v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);

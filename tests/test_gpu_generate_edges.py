@@ -56,3 +56,28 @@ def test_large_scores(mx, D, L, new, group, kv, page, more, nats):       # noqa:
     assert (np.abs(out.float().cpu().numpy() - o) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(o)).all()
     # FP32: the sum of D products, three scalings, the product with ln 2
     assert (np.abs(lse.cpu().numpy() - l) <= (D + 6) * 2.0 ** -24 * np.abs(l)).all()
+
+
+@pytest.mark.parametrize("nats", [16.6, 17.0, 17.7, 18.5])
+@pytest.mark.parametrize("D,L,new,group,kv,page,more", SINKS)
+def test_small_probabilities_beside_a_large_one(mx, D, L, new, group, kv, page, more, nats):       # noqa: F811
+    """The probabilities of all but one position are 2^-24 to 2^-27 of the largest.  Each enters the second product as FP16
+    of 2^7 times itself relative to the running maximum: off by 2^-11 relatively or 2^-25 absolutely, which is 2^-32 of the
+    largest, so |error of o| <= (4 eps + 2^-10 + n 2^-24) mix + n 2^-32 max|v| + 2^-8 |o|."""
+    for sink in (0, L // 2):
+        q, q_start, lens, table, cache, s_k, s_v, scale = sink_case(D, L, new, group, kv, page, nats, sink)
+        out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+        lse = torch.full(q.shape[:2], float("nan"), dtype=torch.float32, device=DEV)
+        ws = torch.empty(mx.kv_attention_workspace_bytes(D), dtype=torch.uint8, device=DEV)
+        mx.mx_nvfp4_kv_attention(q, i32(q_start), i32(lens), i32(wide(table, more // page)), cache, f32(s_k), f32(s_v), scale, new, out, ws, lse=lse)
+        done(mx)
+        o, l, mix, reach = ref.attention(ref.bf16_value(to_np_u16(q)).astype(np.float64), q_start, lens, table, cache.cpu().numpy(), s_k, s_v,
+                                         scale, page)
+        eps = (D + 4) * 2.0 ** -24 * reach + 2.0 ** -23 * (np.abs(l) + np.log(L) + reach)
+        vmax = 6 * float(np.max(s_v))
+        bound = (4 * eps[..., None] + 2.0 ** -10 + L * 2.0 ** -24) * mix + L * 2.0 ** -32 * vmax + 2.0 ** -8 * 1.01 * np.abs(o)
+        got = out.float().cpu().numpy().astype(np.float64)
+        bad = ~(np.abs(got - o) <= bound)
+        assert not bad.any(), f"sink {sink}: {int(bad.sum())} of {bad.size} off, {got[bad][0]} want {o[bad][0]} within {bound[bad][0]}"
+        bad = ~(np.abs(lse.cpu().numpy() - l) <= eps + 2.0 ** -20 + L * 2.0 ** -24 + 2.0 ** -22 * np.abs(l))
+        assert not bad.any()
