@@ -79,7 +79,9 @@ mx_status mx_nvfp4_kv_gather(const uint8_t* cache, int64_t pages, int64_t page_s
  *   q [T, heads, head_dim] BF16 and out alike, with token and head strides in elements (multiples of 8)
  *   q_start [requests + 1]  first token of each request (nondecreasing, at most T; rows of out and lse that belong to
  *            no request are not written)
- *   seq_lens [requests]  cached tokens, the new ones included;  max_q: at least the largest n
+ *   seq_lens [requests]  cached tokens, the new ones included
+ *   max_q  rows of a request: at least the largest n (of a request with more the first max_q are written, the others left as
+ *            they are).  The work of all requests is laid out for it, so the largest n itself is fastest.
  *   block_table [requests, table_width] as written by mx_kv_slots;  s_k, s_v [kv_heads]
  *   lse [T, heads] FP32 or NULL
  *   workspace: mx_kv_attention_workspace_bytes(head_dim) bytes, 16-byte aligned, need not be cleared.

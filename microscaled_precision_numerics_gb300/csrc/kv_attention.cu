@@ -135,7 +135,7 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
 
 // What request r asks for: tiles of its context, items (kv head x column tile) and the first tile's position.
 struct Request {
-    int first, count, len, tile0, tiles, col_tiles, per_item;             // per_item: cost of an item
+    int first, count, base, len, tile0, tiles, col_tiles, per_item;       // count: rows (max_q at most); base: position of new token 0; per_item: cost of an item
     __device__ int64_t cost(int kv_heads) const { return (int64_t)per_item * col_tiles * kv_heads; }
 };
 template <int D, int NQ>
@@ -143,10 +143,11 @@ __device__ __forceinline__ Request request_of(const KvAttentionArgs& a, int r, b
     Request q;
     q.first = load_global(a.q_start + r);
     // (offsets outside [0, T] are invalid input; the clamps keep every access inside q and out all the same)
-    q.count = q.first < 0 ? 0 : (int)min64(min64(load_global(a.q_start + r + 1), a.T) - q.first, a.max_q);
-    q.count = max(0, q.count);
+    const int fresh = q.first < 0 ? 0 : (int)max64(0, min64(load_global(a.q_start + r + 1), a.T) - q.first);
+    q.count = min(fresh, a.max_q);
     q.len = max(0, load_global(a.seq_lens + r));
-    const int64_t lo = a.window > 0 ? max64(0, (int64_t)q.len - q.count + 1 - a.window) : 0;
+    q.base = q.len - fresh;                                                // whatever max_q leaves of the rows
+    const int64_t lo = a.window > 0 ? max64(0, (int64_t)q.base + 1 - a.window) : 0;
     q.tile0 = (int)(lo / ATT_TILE);
     const uint32_t held = (uint32_t)min64(q.len, a.width * a.page);       // positions that the table has pages for
     q.tiles = max(1, (int)((held + ATT_TILE - 1) / ATT_TILE) - q.tile0);
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
         const int64_t item_at = at - in_item;                              // where the item begins
         const int h = item / rq.col_tiles, col0 = (item - h * rq.col_tiles) * 8 * NQ;
         const int cols = rq.count * a.group;                               // query rows of this kv head
-        const int base_pos = rq.len - rq.count;                            // position of new token 0
+        const int base_pos = rq.base;
 
         // ---- the warp's tiles: first_tile + warp, + 4, ...; lane i looks up record i & 1 of step 16 b + i / 2
         const int steps = n_tiles > warp ? (n_tiles - warp + ATT_WARPS - 1) / ATT_WARPS : 0;

@@ -6,7 +6,7 @@ import torch
 
 import generate_ref as ref
 from gpu_util import DEV, bf16_dev, to_np_u16
-from test_gpu_generate import done, f32, i32, mx, wide    # noqa: F401  (mx is the fixture)
+from test_gpu_generate import attention_case, done, f32, i32, mx, wide    # noqa: F401  (mx is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,29 @@ def test_small_probabilities_beside_a_large_one(mx, D, L, new, group, kv, page, 
         assert not bad.any(), f"sink {sink}: {int(bad.sum())} of {bad.size} off, {got[bad][0]} want {o[bad][0]} within {bound[bad][0]}"
         bad = ~(np.abs(lse.cpu().numpy() - l) <= eps + 2.0 ** -20 + L * 2.0 ** -24 + 2.0 ** -22 * np.abs(l))
         assert not bad.any()
+
+
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("heads,kv,D", [(4, 4, 64), (8, 2, 128), (4, 1, 256)])
+def test_max_q_below_the_new_tokens(mx, heads, kv, D, window):       # noqa: F811
+    """A max_q below a request's new tokens: its first max_q rows are as with all of them, later ones are not written."""
+    page, new = 16, [5, 1, 7, 3]
+    q, q_start, lens, table, cache, s_k, s_v = attention_case(31, [90, 33, 40, 3], new, heads, kv, D, page)
+    o, l, mix, reach = ref.attention(ref.bf16_value(to_np_u16(q)).astype(np.float64), q_start, lens, table, cache.cpu().numpy(), s_k, s_v,
+                                     D ** -0.5, page, window)
+    ws = torch.empty(mx.kv_attention_workspace_bytes(D), dtype=torch.uint8, device=DEV)
+    for max_q in (1, 2, 4):
+        out = torch.full(q.shape, 9.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full(q.shape[:2], 9.0, dtype=torch.float32, device=DEV)
+        for tab in (table, wide(table, 200)):
+            mx.mx_nvfp4_kv_attention(q, i32(q_start), i32(lens), i32(tab), cache, f32(s_k), f32(s_v), D ** -0.5, max_q, out, ws, lse=lse,
+                                     window=window)
+            done(mx)
+            kept = np.concatenate([s + np.arange(min(n, max_q)) for s, n in zip(q_start, new)])
+            rest = np.setdiff1d(np.arange(len(o)), kept)
+            got, got_l = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+            assert (got[rest] == 9).all() and (got_l[rest] == 9).all()
+            eps = ((D + 4) * 2.0 ** -24 * reach + 2.0 ** -23 * (np.abs(l) + np.log(90) + reach))[kept]
+            bound = (4 * eps[..., None] + 2.0 ** -10 + 90 * 2.0 ** -24) * mix[kept] + 90 * 2.0 ** -32 * 6 * 448 * s_v.max() + 2.0 ** -8 * 1.01 * np.abs(o[kept])
+            assert (np.abs(got - o)[kept] <= bound + 1e-30).all()
+            assert (np.abs(got_l - l)[kept] <= eps + 2.0 ** -20 + 90 * 2.0 ** -24 + 2.0 ** -22 * np.abs(l[kept])).all()
