@@ -540,18 +540,24 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
                         }
                     }
                     // A NaN would reach the columns that mask its token, as 0 * NaN.  It goes instead, block by block, to the
-                    // columns whose probability for the token is not zero.
+                    // columns that attend to the token, however small their probability for it.
                     if (__any_sync(0xFFFFFFFFu, any != 0)) {
 #pragma unroll 1
                         for (int q = 0; q < 8; ++q)
 #pragma unroll
                             for (int nq = 0; nq < NQ; ++nq) {
-                                const uint32_t p0 = __shfl_sync(0xFFFFFFFFu, pf[gr][nq][0], 4 * q + t4), p1 = __shfl_sync(0xFFFFFFFFu, pf[gr][nq][1], 4 * q + t4);
-                                const uint32_t on0 = ((p0 & 0x7FFFu) ? 0x00FFu : 0u) | ((p0 & 0x7FFF0000u) ? 0xFF00u : 0u);
-                                const uint32_t on1 = ((p1 & 0x7FFFu) ? 0x00FFu : 0u) | ((p1 & 0x7FFF0000u) ? 0xFF00u : 0u);
+                                const int hi = __shfl_sync(0xFFFFFFFFu, (q & 1) ? pos[nq][1] : pos[nq][0], q >> 1);      // of column q
+                                uint32_t on[2] = {0u, 0u};
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                                    for (int y = 0; y < 2; ++y) {
+                                        const int tok = tok0 + gr * 16 + 8 * x + kv_token_of_row(2 * t4 + y);
+                                        if (tok <= hi && (a.window == 0 || tok > hi - a.window)) on[x] |= 0xFFu << (8 * y);
+                                    }
 #pragma unroll
                                 for (int b = 0; b < (D + 127) / 128; ++b) {
-                                    uint32_t hit = (nan[0][b] & on0) | (nan[1][b] & on1);
+                                    uint32_t hit = (nan[0][b] & on[0]) | (nan[1][b] & on[1]);
                                     hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 1);
                                     hit |= __shfl_xor_sync(0xFFFFFFFFu, hit, 2);
                                     const float add = hit && (q >> 1) == t4 ? __int_as_float(0x7FC00000) : 0.0f;

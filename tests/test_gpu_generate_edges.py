@@ -107,3 +107,33 @@ def test_max_q_below_the_new_tokens(mx, heads, kv, D, window):       # noqa: F81
             bound = (4 * eps[..., None] + 2.0 ** -10 + 90 * 2.0 ** -24) * mix[kept] + 90 * 2.0 ** -32 * 6 * 448 * s_v.max() + 2.0 ** -8 * 1.01 * np.abs(o[kept])
             assert (np.abs(got - o)[kept] <= bound + 1e-30).all()
             assert (np.abs(got_l - l)[kept] <= eps + 2.0 ** -20 + 90 * 2.0 ** -24 + 2.0 ** -22 * np.abs(l[kept])).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 3])
+def test_nan_value_of_small_probability(mx, D, new):       # noqa: F811
+    """A NaN among the values reaches every row that attends to its position, whatever its probability and wherever the position lies:
+    in the last tile, part of which is masked, as in one that is not."""
+    L, group, kv, page = 148, 4, 2, 16
+    q, q_start, lens, table, cache, s_k, s_v, scale = sink_case(D, L, new, group, kv, page, 40.0, 3)      # the rest at 2^-57
+    args = (i32(q_start), i32(lens), i32(table))
+    ws = torch.empty(mx.kv_attention_workspace_bytes(D), dtype=torch.uint8, device=DEV)
+
+    def attend(c, window):
+        out = torch.zeros_like(q)
+        mx.mx_nvfp4_kv_attention(q, *args, c, f32(s_k), f32(s_v), scale, new, out, ws, window=window)
+        done(mx)
+        return out
+
+    for window in (0, 146):                                                 # 146: the first tile is masked in part
+        base = attend(cache, window)
+        assert base.isfinite().all()
+        for tok in (2, 4, 20, 100, 127, 128, 140, L - 2, L - 1):
+            hurt = cache.clone()
+            hurt[int(table[0, tok // page]), 1, 0, 17 * D + ref.v_scale_position(tok % 16)] = 0x7F        # block 0 of kv head 1
+            out = attend(hurt, window)
+            for t in range(new):
+                pos = L - new + t
+                sees = tok <= pos and (window == 0 or tok > pos - window)
+                assert out[t, group:, :16].isnan().all() == sees and out[t, group:, :16].isnan().any() == sees, (tok, t)
+                assert torch.equal(out[t, group:, 16:], base[t, group:, 16:]) and torch.equal(out[t, :group], base[t, :group])
