@@ -76,8 +76,9 @@ class Decoder:
         self.unplaced = torch.zeros(1, **i32)
         self.workspace = torch.empty(mx.kv_attention_workspace_bytes(head_dim), dtype=torch.uint8, device=device)
 
-    def step(self, tokens, new_lens):
-        """Logits (FP32) of the new tokens: tokens [T] of all requests in order, new_lens [requests] how many each has."""
+    def step(self, tokens, new_lens, most_new=None):
+        """Logits (FP32) of the new tokens: tokens [T] of all requests in order, new_lens [requests] how many each has (on the
+        device), most_new the largest of them, which attention lays its work out for (T where it is not known)."""
         T, H, KV, D = tokens.numel(), self.heads, self.kv_heads, self.dim
         x = self.embedding[tokens]
         slots = torch.empty(T, dtype=torch.int32, device=x.device)
@@ -87,8 +88,8 @@ class Decoder:
         qkv = self.qkv(norm(x)).view(T, H + 2 * KV, D)
         mx.mx_nvfp4_kv_append(qkv[:, H:H + KV], qkv[:, H + KV:], slots, self.s_k, self.s_v, self.cache)
         attended = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
-        mx.mx_nvfp4_kv_attention(qkv[:, :H], self.q_start, self.lens, self.table, self.cache, self.s_k, self.s_v, D ** -0.5, T, attended,
-                                 self.workspace)
+        mx.mx_nvfp4_kv_attention(qkv[:, :H], self.q_start, self.lens, self.table, self.cache, self.s_k, self.s_v, D ** -0.5,
+                                 most_new or T, attended, self.workspace)
         x = x + self.o(attended.view(T, H * D))
         gate, up = self.gate_up(norm(x)).float().chunk(2, -1)
         x = x + self.down((torch.nn.functional.silu(gate) * up).to(torch.bfloat16))
@@ -100,12 +101,12 @@ def generate(decoder, prompts, steps):
     """Greedy tokens [requests, steps] after the prompts (lists of token numbers)."""
     dev = decoder.lens.device
     new = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device=dev)
-    logits = decoder.step(torch.tensor([t for p in prompts for t in p], device=dev), new)
+    logits = decoder.step(torch.tensor([t for p in prompts for t in p], device=dev), new, max(len(p) for p in prompts))
     last = logits[decoder.q_start[1:].long() - 1].argmax(-1)
     ones, out = torch.ones_like(new), []
     for _ in range(steps):
         out.append(last)
-        last = decoder.step(last, ones).argmax(-1)
+        last = decoder.step(last, ones, 1).argmax(-1)
     return torch.stack(out, 1)
 
 

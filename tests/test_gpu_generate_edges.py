@@ -7,6 +7,7 @@ import torch
 import generate_ref as ref
 from gpu_util import DEV, bf16_dev, to_np_u16
 from test_gpu_generate import attention_case, done, f32, i32, mx, wide    # noqa: F401  (mx is the fixture)
+from test_gpu_generate_example import load
 
 pytestmark = pytest.mark.gpu
 
@@ -137,3 +138,19 @@ def test_nan_value_of_small_probability(mx, D, new):       # noqa: F811
                 sees = tok <= pos and (window == 0 or tok > pos - window)
                 assert out[t, group:, :16].isnan().all() == sees and out[t, group:, :16].isnan().any() == sees, (tok, t)
                 assert torch.equal(out[t, group:, 16:], base[t, group:, 16:]) and torch.equal(out[t, :group], base[t, :group])
+
+
+def test_example_passes_the_largest_number_of_new_tokens(mx, monkeypatch):       # noqa: F811
+    """max_q of the example's attention calls: the longest prompt, then one token a request, not the whole batch's tokens."""
+    ex, seen = load(), []
+    real = ex.mx.mx_nvfp4_kv_attention
+    monkeypatch.setattr(ex.mx, "mx_nvfp4_kv_attention", lambda *a, **k: (seen.append(a[8]), real(*a, **k))[1])
+    prompts = [[5, 7, 11], [1], list(range(17))]
+    tokens = ex.generate(ex.Decoder(3, longest=32), prompts, 3)
+    done(mx)
+    assert seen == [17, 1, 1, 1]
+    # a step that is not told takes the batch's number of tokens, which is never too small, and gives the same tokens
+    d = ex.Decoder(3, longest=32)
+    new = torch.tensor([3, 1, 17], dtype=torch.int32, device=DEV)
+    logits = d.step(torch.tensor([t for p in prompts for t in p], device=DEV), new)
+    assert seen[-1] == 21 and torch.equal(logits[d.q_start[1:].long() - 1].argmax(-1), tokens[:, 0])
