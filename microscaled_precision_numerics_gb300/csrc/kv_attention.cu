@@ -623,9 +623,9 @@ __global__ void __launch_bounds__(ATT_THREADS, att_ctas(D, NQ)) kv_attention_ker
             if (col >= cols) return;
             const int i = (int)divu32((uint32_t)col, p.dv_group), hq = h * a.group + (col - i * a.group);
             const int64_t t = rq.first + i;
-            const float f = L == 0.0f ? 0.0f : S_v / L;
+            const float f = L == 0.0f ? 0.0f : 1.0f / L;                   // (S_v / L may be too small for FP32 where x * S_v / L is not)
             *reinterpret_cast<uint2*>(a.out + t * a.o_token + (int64_t)hq * a.o_head + d) =
-                make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+                make_uint2(pack_bf16x2(x.x * f * S_v, x.y * f * S_v), pack_bf16x2(x.z * f * S_v, x.w * f * S_v));
             if (a.lse && d == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
         };
         __syncthreads();                                                   // ring no longer read; s_m, s_l written
@@ -781,10 +781,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) kv_attention_join_kernel(const _
     }
     const int i = (int)divu32((uint32_t)col, p.dv_group), hq = pc.kv_head * a.group + (col - i * a.group);
     const int64_t t = pc.token0 + i;
-    const float f = L == 0.0f ? 0.0f : load_global(a.s_v + pc.kv_head) / L;
+    const float f = L == 0.0f ? 0.0f : 1.0f / L, S_v = load_global(a.s_v + pc.kv_head);
     uint32_t* out = reinterpret_cast<uint32_t*>(a.out + t * a.o_token + (int64_t)hq * a.o_head + lane * V);
 #pragma unroll
-    for (int v = 0; v < V; v += 2) out[v >> 1] = pack_bf16x2(o[v] * f, o[v + 1] * f);
+    for (int v = 0; v < V; v += 2) out[v >> 1] = pack_bf16x2(o[v] * f * S_v, o[v + 1] * f * S_v);
     if (a.lse && lane == 0) a.lse[t * ((int64_t)a.kv_heads * a.group) + hq] = L == 0.0f ? -INFINITY : __fmaf_rn(M, 0.6931471805599453f, logf(L));
 }
 

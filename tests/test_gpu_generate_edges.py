@@ -6,7 +6,7 @@ import torch
 
 import generate_ref as ref
 from gpu_util import DEV, bf16_dev, to_np_u16
-from test_gpu_generate import attention_case, done, f32, i32, mx, wide    # noqa: F401  (mx is the fixture)
+from test_gpu_generate import attention_case, check_attention, done, f32, i32, mx, wide    # noqa: F401  (mx is the fixture)
 from test_gpu_generate_example import load
 
 pytestmark = pytest.mark.gpu
@@ -138,6 +138,22 @@ def test_nan_value_of_small_probability(mx, D, new):       # noqa: F811
                 sees = tok <= pos and (window == 0 or tok > pos - window)
                 assert out[t, group:, :16].isnan().all() == sees and out[t, group:, :16].isnan().any() == sees, (tok, t)
                 assert torch.equal(out[t, group:, 16:], base[t, group:, 16:]) and torch.equal(out[t, :group], base[t, :group])
+
+
+@pytest.mark.parametrize("scale", [0.0, 0.1])
+@pytest.mark.parametrize("scale_v", [1e-34, 1e-36, 1e33])
+@pytest.mark.parametrize("lens,new,heads,kv,D,page,more", [([300, 40], [1, 1], 8, 2, 64, 16, 0), ([300, 40], [3, 2], 8, 2, 128, 16, 0),
+                                                           ([900], [1], 8, 2, 128, 16, 0), ([1500, 700], [2, 1], 8, 2, 256, 16, 20000)])
+def test_value_scales_near_the_ends_of_fp32(mx, lens, new, heads, kv, D, page, more, scale_v, scale):       # noqa: F811
+    """S_v so small that divided by the sum of the probabilities, most of all of equal ones, it would have few bits left or none."""
+    q, q_start, lens, table, cache, s_k, s_v = attention_case(41, lens, new, heads, kv, D, page, scale_v=scale_v)
+    out, _ = check_attention(mx, q, q_start, lens, wide(table, more // page), cache, s_k, s_v, scale, page, host_cache=cache.cpu().numpy())
+    want, l, mix, reach = ref.attention(ref.bf16_value(to_np_u16(q)).astype(np.float64), q_start, lens, table, cache.cpu().numpy(), s_k, s_v, scale, page)
+    # check_attention's bound has a floor of 1e-30 for zeros, which is above these outputs; BF16's smallest step here instead
+    n = int(max(lens))
+    eps = (D + 4) * 2.0 ** -24 * reach + 2.0 ** -23 * (np.abs(l) + np.log(n) + reach)
+    bound = (4 * eps[..., None] + 2.0 ** -10 + n * 2.0 ** -24) * mix + n * 2.0 ** -32 * 6 * 448 * s_v.max() + 2.0 ** -8 * 1.01 * np.abs(want) + 2.0 ** -133
+    assert (np.abs(out.float().cpu().numpy() - want) <= bound).all()
 
 
 def test_example_passes_the_largest_number_of_new_tokens(mx, monkeypatch):       # noqa: F811
