@@ -15,7 +15,7 @@
  *   V codes   16 rows of head_dim / 2 bytes
  *   V scales  [head_dim / 16][16] E4M3 bytes, token i of the record at position i ^ ((i >> 1) & 1)
  * with value = val(code) * val(block scale) * S, S one FP32 per kv head for K (s_k) and one for V (s_v), given by the
- * caller.  page_size is a multiple of 16 (at most 2^20), head_dim 64, 128 or 256, pages * page_size < 2^31.
+ * caller.  page_size is a multiple of 16 (at most 2^20), kv_heads at most 65535, head_dim 64, 128 or 256, pages * page_size < 2^31.
  * Slot number of a cached token: page * page_size + its offset inside the page.
  */
 #ifndef MXNUM_GENERATE_H

@@ -715,7 +715,7 @@ def alloc_nvfp4_rows(rows: int, k: int, device):
 def alloc_nvfp4_kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device):
     """An empty NVFP4 key/value cache [pages, kv_heads, page_size / 16, 18 * head_dim]."""
     if kv_page_bytes(page_size, kv_heads, head_dim) == 0:
-        raise ValueError("page_size must be a multiple of 16 and head_dim 64, 128 or 256")
+        raise ValueError("page_size must be a multiple of 16 up to 2^20, kv_heads 1 to 65535 and head_dim 64, 128 or 256")
     return torch.zeros((pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8, device=device)
 
 

@@ -447,9 +447,12 @@ mx_status mx_kv_slots(const int32_t* seq_lens, const int32_t* new_lens, int64_t 
                                           max_tokens, free_left, unplaced, stream));
 }
 
+static bool kv_sizes_taken(int64_t page_size, int64_t heads, int64_t dim) {
+    return (page_size % 16) == 0 && page_size <= (1 << 20) && heads <= 65535 && (dim == 64 || dim == 128 || dim == 256);
+}
+
 int64_t mx_kv_page_bytes(int64_t page_size, int64_t kv_heads, int64_t head_dim) {
-    if (page_size <= 0 || (page_size % 16) != 0 || kv_heads <= 0) return 0;
-    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return 0;
+    if (page_size <= 0 || kv_heads <= 0 || !kv_sizes_taken(page_size, kv_heads, head_dim)) return 0;
     return page_size / mxk::KV_GROUP * kv_heads * mxk::kv_record_bytes((int)head_dim);
 }
 
@@ -457,9 +460,7 @@ static mx_status check_kv_cache(const void* cache, int64_t pages, int64_t page_s
                                 const float* s_k, const float* s_v) {
     if (!cache || !s_k || !s_v || pages <= 0 || page_size <= 0 || heads <= 0 || dim <= 0) return MX_ERR_INVALID_ARG;
     if (!aligned16(cache) || !aligned4(s_k) || !aligned4(s_v)) return MX_ERR_ALIGNMENT;
-    if ((page_size % 16) != 0 || page_size > (1 << 20) || pages > INT32_MAX / page_size || heads > 65535 ||
-        (dim != 64 && dim != 128 && dim != 256))
-        return MX_ERR_UNSUPPORTED;
+    if (!kv_sizes_taken(page_size, heads, dim) || pages > INT32_MAX / page_size) return MX_ERR_UNSUPPORTED;
     return MX_OK;
 }
 

@@ -47,6 +47,21 @@ def test_sizes(lib):
     assert lib.mx_kv_attention_workspace_bytes(96) == 0
 
 
+@pytest.mark.parametrize("page_size,kv_heads,head_dim", [((1 << 20) + 16, 8, 128), (16, 65536, 128), (1 << 40, 1, 64), (16, 1 << 40, 64),
+                                                         (1 << 20, 65535, 256), (48, 65535, 64)])
+def test_page_bytes_are_of_sizes_that_the_cache_takes(lib, page_size, kv_heads, head_dim):
+    """0 exactly where an append to such a cache is refused for its sizes (checked before anything is launched: no slots)."""
+    import microscaled_precision_numerics_gb300 as mx
+    taken = page_size <= 1 << 20 and kv_heads <= 65535
+    assert lib.mx_kv_page_bytes(page_size, kv_heads, head_dim) == (page_size * kv_heads * 18 * head_dim // 16 if taken else 0)
+    bad = {**APPEND, "pages": 1, "page_size": page_size, "kv_heads": kv_heads, "head_dim": head_dim, "k_token": 1 << 20, "v_token": 1 << 20,
+           "k_head": 256, "v_head": 256, "T": 1, "slots": A if not taken else NUL}
+    assert lib.mx_nvfp4_kv_append(*bad.values()) == (INVALID if taken else UNSUPPORTED)
+    if not taken:
+        with pytest.raises(ValueError):
+            mx.alloc_nvfp4_kv_cache(0, page_size, kv_heads, head_dim, "cpu")
+
+
 SLOTS = dict(seq_lens=A, new_lens=A, requests=4, page_size=16, block_table=A, table_width=8, table_stride=8, free_pages=A,
              free_capacity=10, free_count=A, q_start=A, total_lens=A, slots=A, positions=A, max_tokens=5, free_left=A,
              unplaced=A, stream=NUL)
