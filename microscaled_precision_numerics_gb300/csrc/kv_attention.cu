@@ -32,12 +32,15 @@
 // Short contexts are not split so: a CTA takes an item, or a cluster of up to 8 CTAs divides it and joins its parts through
 // distributed shared memory, in one launch and without the workspace.
 // The four warps of a CTA take every fourth tile of 32 positions with statistics of their own, through two stages of
-// cp.async each (three stages, or eight warps a CTA, were slower: 75.1 and 84.3 against 73.7 us).
+// cp.async each, four for D = 64 (for D = 128 three stages, or eight warps a CTA, were slower: 75.1 and 84.3 against 73.7 us).
 //
 // Measured on a GB300 (device us, share of the measured copy rate): 64 requests to 8192 tokens, 32 q heads over 8 kv heads, D =
-// 128: 72.9 (75 %; of the scheduler slots 57 % issue, the ALU is busy 49 %, the pipe that HMUL2 and HMMA share 51 %: bound
-// by latency with the 12 warps an SM that the registers leave); one request of 131071 tokens: 34.2 (65 %; about 8 us
+// 128: 72.9 (75 %; of the scheduler slots 58 % issue, the ALU is busy 49 %, the pipe that HMUL2 and HMMA share 51 %: bound
+// by latency with the 12 warps an SM that the registers leave); one request of 131071 tokens: 34.1 (65 %; about 8 us
 // of it are fixed: launch, look-ups, joins); one of 777: 6.8 (latency; 10.0 without clusters).
+// The host knows the table's width and max_q, not the lengths, and lays the work out for those: under a table of 131072
+// positions the request of 777 takes 8.5 (the split and its second launch), 57 to 1000 tokens 19.9 instead of 16.6; with max_q = 64
+// for one new token each, 64 to 8192 take 104 instead of 73 (two column fragments, one of them empty and the other half empty).
 #include "mx_internal.h"
 #include "mx_kv.cuh"
 #include "mx_fragment.cuh"

@@ -20,8 +20,10 @@ namespace {
 // over all requests) sits at position L_r + t - start_r in page table[r][position / P].
 //
 // Two exclusive sums over the requests (tokens and pages) and then independent look-ups: a few kilobytes, bound by
-// latency (3.2 us for 64 requests of one token, 8.6 for 500 with 32 thousand tokens).  Every CTA of the one cluster sums all requests for itself (R / 1024 steps a thread) rather
-// than wait for another launch; the outputs are shared out afterwards, each thread's look-ups side by side.
+// latency (3.2 us for 64 requests of one token).  Every CTA of the one cluster sums all requests for itself (R / 1024 steps a
+// thread) rather than wait for another launch; the outputs are shared out afterwards, each thread's look-ups side by side.
+// One cluster of 8 CTAs, so that the tokens without a slot are counted in its shared memory, is also what a large step waits
+// for: 8.6 us for 500 requests with 32 thousand tokens, four thousand look-ups a CTA of nine dependent steps each.
 // ------------------------------------------------------------------------------------------------
 constexpr int SLOT_THREADS = 1024;
 

@@ -27,9 +27,11 @@
 // and across the CTAs of a cluster, which split K further, through distributed shared memory; always in the same order,
 // so a result does not depend on timing.
 //
-// Measured on a GB300 (device us, share of the measured copy rate): 1 x 151937 x 2048 33.1 (79 %: HBM, without loads 27.1),
-// 5 x 12288 x 4096 10.9 (39 %: about 4 us fixed, 96 of 152 SMs have rows), 16 x 4096 x 14336 16.8 (30 %: FP16 pipe and the
-// staging of x, 3.3 us), 1 x 4096 x 4096 4.8 (29 %: latency).
+// Measured on a GB300 (device us, share of the measured copy rate): 1 x 151937 x 2048 31.9 (81 %: HBM, without loads 27.1).
+// The others with weights that stay in L2 from call to call / with others than the last calls', from HBM: 5 x 12288 x 4096 11.0 /
+// 11.5 (38 / 37 %: about 4 us fixed; four warps along K make 96 turns of the 384 row groups, for 96 of 152 SMs), 16 x 4096 x 14336 16.7 /
+// 16.8 (30 %: about 10 us are launch, first loads, the staging of x (3.3) and the two meetings; the FP16 pipe is busy
+// 32 % of the whole), 1 x 4096 x 4096 4.7 / 5.0 (29 / 28 %: latency).
 #include "mx_internal.h"
 #include "mx_fragment.cuh"
 #include "mx_chain.cuh"
