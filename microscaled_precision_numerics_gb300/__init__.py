@@ -1,7 +1,7 @@
 """Python binding of libmxnum.so (block-scaled microscaling numerics on GB300, sm_103a).
 
 Argument marshalling only: every function passes ``tensor.data_ptr()`` values, sizes, seeds and the
-current CUDA stream to the C ABI declared in ``include/mxnum.h`` (and ``mxnum_generate.h``) and raises ``MXError`` on a non-OK
+current CUDA stream to the C ABI declared in ``include/mxnum.h`` (and ``mxnum_generate.h``, ``mxnum_layer.h``) and raises ``MXError`` on a non-OK
 status.  No arithmetic happens here and there is no CPU fallback: if the CUDA library is missing or
 a tensor is not on a CUDA device, the call raises.  ``alloc_*`` helpers only create output tensors
 of the right sizes (``torch.empty`` on the input's device; the key/value cache cleared).
@@ -83,6 +83,17 @@ def lib() -> ctypes.CDLL:
                 "mx_nvfp4_kv_attention": (I32, [P, I64, I64, I64, I64, P, P, I64, I64, P, I64, I64, P, I64, I64, I64,
                                                 I64, P, P, ctypes.c_float, I64, P, I64, I64, P, P, SZ, P]),
                 "mx_nvfp4_matvec": (I32, [P, I64, P, P, P, I32, I64, I64, I64, P, I64, I32, P]),
+                "mx_rmsnorm_mxfp8": (I32, [P, I64, P, I64, P, I32, ctypes.c_float, I64, I64, P, I64, P, I64, P, P, P, P, P]),
+                "mx_rmsnorm_workspace_bytes": (SZ, [I64, I64]),
+                "mx_rmsnorm_backward": (I32, [P, I64, P, I64, P, I32, ctypes.c_float, I64, I64, P, I64, P, I64, P, P, SZ, P]),
+                "mx_moe_route": (I32, [P, I32, I64, I64, I64, I64, I32, P, P, P]),
+                "mx_moe_route_backward": (I32, [P, I32, I64, I64, I64, I64, I32, P, P, P, I64, P]),
+                "mx_moe_sort_workspace_bytes": (SZ, [I64, I64]),
+                "mx_moe_sort": (I32, [P, I64, I64, I64, P, P, P, P, SZ, P]),
+                "mx_moe_dispatch": (I32, [P, I64, I64, I64, P, I64, P, I64, I64, P]),
+                "mx_moe_dispatch_quantized": (I32, [I32, P, P, P, I64, I64, P, I64, I64, P, P, P, P, I64, P]),
+                "mx_moe_combine": (I32, [P, I64, I64, I64, P, P, I64, I64, P, I64, P, I64, P]),
+                "mx_moe_combine_backward": (I32, [P, I64, P, I64, I64, I64, P, P, I64, I64, P, I64, P, P]),
                 "mx_check_device_status": (I32, []),
                 "mx_check_stream_status": (I32, [P]),
                 "mx_watchdog_selftest": (I32, [I32, U64, P]),
@@ -674,6 +685,192 @@ def mx_nvfp4_matvec(x, q, s, s2, s2_scope: int, y, stream=None):
         _array(fn, "q", q, u8, N * K // 2, cur), _array(fn, "s", s, u8, (N + 127) // 128 * ((K // 16 + 3) // 4) * 512, cur),
         _array(fn, "s2", s2, torch.float32, _alpha_count(s2_scope, N), cur), s2_scope, M, N, K,
         y.data_ptr() if y.get_device() == cur else _p(y), y_step[0] if M > 1 else N, fp32, _stream_on(cur, stream)))
+
+
+# ------------------------------------------------------------------------------------------------
+# between the products of a layer: norm, expert choice, rows by expert and back (see include/mxnum_layer.h)
+# ------------------------------------------------------------------------------------------------
+
+MX_DTYPE_BF16, MX_DTYPE_FP32 = 0, 1
+MX_RMSNORM_MAX_COLS, MX_MOE_MAX_TOP_K = 16384, 32
+_DTYPES = {torch.bfloat16: MX_DTYPE_BF16, torch.float32: MX_DTYPE_FP32}
+
+
+def _rows2d(fn: str, name: str, t, dtype, rows, cols, cur: int):
+    """(pointer, row stride, rows, columns) of a [rows, cols] view with unit column stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{fn}: {name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols) or (
+            shape[1] > 1 and stride[1] != 1):
+        raise ValueError(f"{fn}: {name} must be [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}] with unit "
+                         f"column stride, got {tuple(shape)}")
+    return t.data_ptr() if t.get_device() == cur else _p(t), stride[0] if shape[0] > 1 else shape[1], shape[0], shape[1]
+
+
+def _maybe(f, fn, name, t, *args):
+    return None if t is None else f(fn, name, t, *args)
+
+
+def _ids2d(fn: str, name: str, t):
+    """(tokens, top_k) of a [tokens, top_k] tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{fn}: {name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{fn}: {name} must be [tokens, top_k], got {tuple(t.shape)}")
+    return t.shape
+
+
+def _workspace(fn: str, t, cur: int):
+    """(pointer, bytes) of a contiguous workspace."""
+    if not isinstance(t, torch.Tensor) or not t.is_contiguous() or t.get_device() != cur:
+        _need(fn, "workspace", t, 0)
+        _p(t)
+    return t.data_ptr(), t.nbytes
+
+
+def rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().mx_rmsnorm_workspace_bytes(rows, cols))
+
+
+def moe_sort_workspace_bytes(choices: int, experts: int) -> int:
+    return int(lib().mx_moe_sort_workspace_bytes(choices, experts))
+
+
+def _norm_weight(fn: str, weight, cols: int, cur: int):
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in _DTYPES:
+        raise TypeError(f"{fn}: weight must be a bfloat16 or float32 tensor")
+    return _array(fn, "weight", weight, weight.dtype, cols, cur), _DTYPES[weight.dtype]
+
+
+def mx_rmsnorm_mxfp8(x, weight, eps: float, residual=None, sum_out=None, y=None, q_row=None, s_row=None, q_col=None, s_col=None,
+                     stream=None):
+    """Root-mean-square norm of x + residual [rows, cols] (BF16, any row stride) times weight [cols] (BF16 or FP32): the sum into
+    sum_out (which may be x or residual), the output into y and as MXFP8 into q_row, s_row and q_col, s_col (alloc_mxfp8)."""
+    fn, bf = "mx_rmsnorm_mxfp8", torch.bfloat16
+    cur = _device_of(x)
+    xp, ldx, rows, cols = _rows2d(fn, "x", x, bf, None, None, cur)
+    wp, wt = _norm_weight(fn, weight, cols, cur)
+    rp, ldr = (None, 0) if residual is None else _rows2d(fn, "residual", residual, bf, rows, cols, cur)[:2]
+    sp, lds = (None, 0) if sum_out is None else _rows2d(fn, "sum_out", sum_out, bf, rows, cols, cur)[:2]
+    yp, ldy = (None, 0) if y is None else _rows2d(fn, "y", y, bf, rows, cols, cur)[:2]
+    u8, n = torch.uint8, rows * cols
+    _check(fn, lib().mx_rmsnorm_mxfp8(
+        xp, ldx, rp, ldr, wp, wt, eps, rows, cols, sp, lds, yp, ldy, _maybe(_array, fn, "q_row", q_row, u8, n, cur),
+        None if s_row is None else _array(fn, "s_row", s_row, u8, scale_bytes(rows, cols, 32), cur),
+        _maybe(_array, fn, "q_col", q_col, u8, n, cur),
+        None if s_col is None else _array(fn, "s_col", s_col, u8, scale_bytes(cols, rows, 32), cur), _stream_on(cur, stream)))
+
+
+def mx_rmsnorm_backward(dy, h, weight, eps: float, dx, dweight, workspace, dsum=None, stream=None):
+    """Gradient of mx_rmsnorm_mxfp8 from dy [rows, cols]: dx (of the norm's input h and, where it is a sum, of both summands, with dsum
+    added; it may be dsum or dy) and dweight [cols] (FP32)."""
+    fn, bf = "mx_rmsnorm_backward", torch.bfloat16
+    cur = _device_of(h)
+    hp, ldh, rows, cols = _rows2d(fn, "h", h, bf, None, None, cur)
+    wp, wt = _norm_weight(fn, weight, cols, cur)
+    gp, ldg = _rows2d(fn, "dy", dy, bf, rows, cols, cur)[:2]
+    sp, lds = (None, 0) if dsum is None else _rows2d(fn, "dsum", dsum, bf, rows, cols, cur)[:2]
+    xp, ldx = _rows2d(fn, "dx", dx, bf, rows, cols, cur)[:2]
+    ws, ws_bytes = _workspace(fn, workspace, cur)
+    _check(fn, lib().mx_rmsnorm_backward(gp, ldg, hp, ldh, wp, wt, eps, rows, cols, sp, lds, xp, ldx,
+                                         _array(fn, "dweight", dweight, torch.float32, cols, cur), ws, ws_bytes, _stream_on(cur, stream)))
+
+
+def _logits(fn: str, name: str, t, dtype, tokens, experts, cur: int):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+        raise TypeError(f"{fn}: {name} must be a bfloat16 or float32 tensor")
+    return _rows2d(fn, name, t, dtype or t.dtype, tokens, experts, cur)
+
+
+def mx_moe_route(logits, ids, weights, normalize: bool = True, stream=None):
+    """The top_k largest logits [tokens, experts] (BF16 or FP32) of each token into ids [tokens, top_k] (int32) and their softmax, over
+    the chosen ones or (normalize False) over all, into weights [tokens, top_k] (FP32)."""
+    fn, cur = "mx_moe_route", _device_of(logits)
+    T, k = _ids2d(fn, "ids", ids)
+    lp, ldl, _, E = _logits(fn, "logits", logits, None, T, None, cur)
+    _check(fn, lib().mx_moe_route(lp, _DTYPES[logits.dtype], ldl, T, E, k, int(normalize), _array(fn, "ids", ids, torch.int32, T * k, cur),
+                                  _array(fn, "weights", weights, torch.float32, T * k, cur), _stream_on(cur, stream)))
+
+
+def mx_moe_route_backward(logits, ids, dweights, dlogits, normalize: bool = True, stream=None):
+    """dlogits (of the logits' type) from the gradient of mx_moe_route's weights."""
+    fn, cur = "mx_moe_route_backward", _device_of(logits)
+    T, k = _ids2d(fn, "ids", ids)
+    lp, ldl, _, E = _logits(fn, "logits", logits, None, T, None, cur)
+    dp, ldd, _, _ = _logits(fn, "dlogits", dlogits, logits.dtype, T, E, cur)
+    _check(fn, lib().mx_moe_route_backward(
+        lp, _DTYPES[logits.dtype], ldl, T, E, k, int(normalize), _array(fn, "ids", ids, torch.int32, T * k, cur),
+        _array(fn, "dweights", dweights, torch.float32, T * k, cur), dp, ldd, _stream_on(cur, stream)))
+
+
+def mx_moe_sort(ids, group_offsets, rows, source, workspace, stream=None):
+    """The choices ids [tokens, top_k] sorted by expert: group_offsets [experts + 1] (int64), the row of each choice (rows [tokens, top_k],
+    -1 for an id outside the experts) and the choice of each row (source [tokens * top_k] or None)."""
+    fn, cur = "mx_moe_sort", _device_of(ids)
+    T, k = _ids2d(fn, "ids", ids)
+    i32, G = torch.int32, group_offsets.numel() - 1
+    ws, ws_bytes = _workspace(fn, workspace, cur)
+    _check(fn, lib().mx_moe_sort(
+        _array(fn, "ids", ids, i32, T * k, cur), T, k, G, _array(fn, "group_offsets", group_offsets, torch.int64, G + 1, cur),
+        _array(fn, "rows", rows, i32, T * k, cur), _maybe(_array, fn, "source", source, i32, T * k, cur), ws, ws_bytes,
+        _stream_on(cur, stream)))
+
+
+def mx_moe_dispatch(x, rows, y, stream=None):
+    """y[rows[t, j]] = x[t] for x [tokens, hidden] and y [total_rows, hidden] (BF16, any row stride)."""
+    fn, bf, cur = "mx_moe_dispatch", torch.bfloat16, _device_of(x)
+    T, k = _ids2d(fn, "rows", rows)
+    xp, ldx, _, H = _rows2d(fn, "x", x, bf, T, None, cur)
+    yp, ldy, R, _ = _rows2d(fn, "y", y, bf, None, H, cur)
+    _check(fn, lib().mx_moe_dispatch(xp, ldx, T, H, _array(fn, "rows", rows, torch.int32, T * k, cur), k, yp, ldy, R,
+                                     _stream_on(cur, stream)))
+
+
+def mx_moe_dispatch_quantized(fmt: int, q, s, rows, group_offsets, q_out, s_out, s2=None, s2_out=None, stream=None):
+    """mx_moe_dispatch of rows that are quantized already (q [tokens, hidden] E4M3 bytes or [tokens, hidden / 2] packed E2M1 with their
+    scales s, and s2 for NVFP4), the scales into the grouped layout."""
+    fn, u8, cur = "mx_moe_dispatch_quantized", torch.uint8, _device_of(q)
+    T, k = _ids2d(fn, "rows", rows)
+    fp4 = fmt == MX_FMT_NVFP4
+    if q.dim() != 2 or q.shape[0] != T or q_out.dim() != 2 or q_out.shape[1] != q.shape[1]:
+        raise ValueError(f"{fn}: q must be [{T}, bytes] and q_out [total_rows, bytes], got {tuple(q.shape)} and {tuple(q_out.shape)}")
+    nbytes, R, G, f32 = q.shape[1], q_out.shape[0], group_offsets.numel() - 1, torch.float32
+    H, block = (2 * nbytes, 16) if fp4 else (nbytes, 32)
+    _check(fn, lib().mx_moe_dispatch_quantized(
+        fmt, _array(fn, "q", q, u8, T * nbytes, cur), _array(fn, "s", s, u8, scale_bytes(T, H, block), cur),
+        _maybe(_array, fn, "s2", s2, f32, T, cur), T, H, _array(fn, "rows", rows, torch.int32, T * k, cur), k, G,
+        _array(fn, "group_offsets", group_offsets, torch.int64, G + 1, cur), _array(fn, "q_out", q_out, u8, R * nbytes, cur),
+        _array(fn, "s_out", s_out, u8, grouped_scale_bytes(R, G, H, block), cur), _maybe(_array, fn, "s2_out", s2_out, f32, R, cur), R,
+        _stream_on(cur, stream)))
+
+
+def mx_moe_combine(z, rows, y, weights=None, residual=None, stream=None):
+    """y[t] = sum_j weights[t, j] * z[rows[t, j]] + residual[t] (BF16, any row stride; y may be residual).  Without weights all are 1:
+    the gradient of mx_moe_dispatch."""
+    fn, bf, cur = "mx_moe_combine", torch.bfloat16, _device_of(z)
+    T, k = _ids2d(fn, "rows", rows)
+    zp, ldz, R, H = _rows2d(fn, "z", z, bf, None, None, cur)
+    yp, ldy = _rows2d(fn, "y", y, bf, T, H, cur)[:2]
+    rp, ldr = (None, 0) if residual is None else _rows2d(fn, "residual", residual, bf, T, H, cur)[:2]
+    _check(fn, lib().mx_moe_combine(
+        zp, ldz, R, H, _array(fn, "rows", rows, torch.int32, T * k, cur), _maybe(_array, fn, "weights", weights, torch.float32, T * k, cur),
+        T, k, rp, ldr, yp, ldy, _stream_on(cur, stream)))
+
+
+def mx_moe_combine_backward(dy, z, rows, weights, dz, dweights, stream=None):
+    """Gradients of mx_moe_combine: dz[rows[t, j]] = weights[t, j] * dy[t] (dz may be z) and dweights[t, j] = dy[t] . z[rows[t, j]]."""
+    fn, bf, cur = "mx_moe_combine_backward", torch.bfloat16, _device_of(z)
+    T, k = _ids2d(fn, "rows", rows)
+    zp, ldz, R, H = _rows2d(fn, "z", z, bf, None, None, cur)
+    gp, ldg = _rows2d(fn, "dy", dy, bf, T, H, cur)[:2]
+    dp, ldd = _rows2d(fn, "dz", dz, bf, R, H, cur)[:2]
+    f32 = torch.float32
+    _check(fn, lib().mx_moe_combine_backward(
+        gp, ldg, zp, ldz, R, H, _array(fn, "rows", rows, torch.int32, T * k, cur), _array(fn, "weights", weights, f32, T * k, cur), T, k,
+        dp, ldd, _array(fn, "dweights", dweights, f32, T * k, cur), _stream_on(cur, stream)))
 
 
 def mx_count_mismatch(x, y, count, stream=None):

@@ -20,7 +20,8 @@ OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmxnum.so")
 
 SOURCES = ["mxnum_api.cu", "quant_mxfp8.cu", "quant_nvfp4.cu", "dequant.cu", "gemm_sm103.cu", "noalloc.cu",
-           "quant_fp8_blockwise.cu", "kv_cache.cu", "kv_attention.cu", "matvec_nvfp4.cu"]
+           "quant_fp8_blockwise.cu", "kv_cache.cu", "kv_attention.cu", "matvec_nvfp4.cu", "norm.cu", "moe_route.cu",
+           "moe_rows.cu"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",

@@ -1,0 +1,200 @@
+// moe_route.cu -- the router's choice of experts for each token, and the gradient of its logits.
+//
+//   ids = the top_k largest logits;  w = softmax over the chosen, or their entries of the softmax over all
+//   dz[id_j] = w_j (dw_j - sum_i w_i dw_i)   or   dz[e] = p_e (dw_j where e = id_j, else 0, - sum_i w_i dw_i)
+//
+// A warp takes a token: its logits stay in registers, expert e in lane e % 32, and are read once.  A choice is two warp
+// reductions over 32-bit keys (the largest key, then the lowest index among the lanes that hold it).
+#include "../../include/mxnum.h"
+#include "../../include/mxnum_layer.h"
+#include "mx_internal.h"
+#include "mx_chain.cuh"
+
+namespace mxk {
+
+namespace {
+
+constexpr int ROUTE_WARPS = 4;
+
+template <bool F32>
+__device__ __forceinline__ float logit(const void* p, int64_t i) {
+    if (F32) return load_global(static_cast<const float*>(p) + i);
+    return __uint_as_float((uint32_t)load_global(static_cast<const uint16_t*>(p) + i) << 16);
+}
+
+// Keys in the order of the logits: NaN above all, zeros of both signs alike, 0 for -inf and for what is taken already.
+__device__ __forceinline__ uint32_t key_of(float z) {
+    if (z != z) return 0xFFFFFFFFu;
+    const uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));
+    if (b == 0xFF800000u) return 0u;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+    if (key == 0xFFFFFFFFu) return __uint_as_float(0x7FC00000u);
+    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// EPL: experts a lane.
+template <int EPL, bool F32>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS)
+moe_route_kernel(const void* logits, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize, int32_t* ids, float* weights) {
+    chain_begin();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
+    if (t >= tokens) return;
+    uint32_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = i * 32 + lane;
+        key[i] = e < experts ? key_of(logit<F32>(logits, t * ldl + e)) : 0u;
+    }
+    float all = 0.0f, top = 0.0f, mine = 0.0f;
+    int my_id = -1;
+    for (int j = 0; j < top_k; ++j) {
+        uint32_t best = key[0];
+        int at = lane;
+#pragma unroll
+        for (int i = 1; i < EPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i * 32 + lane;
+            }
+        const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, best);
+        if (most == 0u) break;                             // none left but -inf
+        const int id = (int)__reduce_min_sync(0xFFFFFFFFu, best == most ? (uint32_t)at : 0xFFFFFFFFu);
+        if (j == 0) {
+            top = value_of(most);
+            if (!normalize) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) s += key[i] != 0u ? expf(value_of(key[i]) - top) : 0.0f;
+                all = warp_add(s);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (i * 32 + lane == id) key[i] = 0u;
+        if (lane == j) {
+            my_id = id;
+            mine = expf(value_of(most) - top);
+        }
+    }
+    const float total = normalize ? warp_add(mine) : all;
+    if (lane < top_k) {
+        ids[t * top_k + lane] = my_id;
+        weights[t * top_k + lane] = my_id >= 0 ? __fdiv_rn(mine, total) : 0.0f;
+    }
+}
+
+template <int EPL, bool F32>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS)
+moe_route_backward_kernel(const void* logits, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize, const int32_t* ids,
+                          const float* dweights, void* dlogits, int64_t ldd) {
+    chain_begin();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
+    if (t >= tokens) return;
+    int id = -1;
+    float dw = 0.0f, z = -INFINITY;
+    if (lane < top_k) {
+        id = load_global(ids + t * top_k + lane);
+        if (id < 0 || id >= experts) id = -1;
+        else {
+            dw = load_global(dweights + t * top_k + lane);
+            z = logit<F32>(logits, t * ldl + id);
+        }
+    }
+    float p[EPL];                                          // all logits, then the softmax over all, then the gradient
+    float top = z;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = i * 32 + lane;
+        p[i] = -INFINITY;
+        if (!normalize && e < experts) p[i] = logit<F32>(logits, t * ldl + e);
+        top = fmaxf(top, p[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float sum = 0.0f;
+    float w = id >= 0 && (z != -INFINITY) ? expf(z - top) : 0.0f;
+    if (normalize) sum = w;
+    else
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            p[i] = p[i] == -INFINITY ? 0.0f : expf(p[i] - top);
+            sum += p[i];
+        }
+    sum = warp_add(sum);                                   // a NaN passes the maximum and reaches the sum
+    const bool none = sum == 0.0f;                         // nothing chosen, or nothing but -inf
+    w = none || w == 0.0f ? 0.0f : __fdiv_rn(w, sum);
+    const float inner = warp_add(__fmul_rn(w, dw));
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        p[i] = normalize || none || p[i] == 0.0f ? 0.0f : -__fmul_rn(__fdiv_rn(p[i], sum), inner);
+    const float part = normalize ? __fmul_rn(w, __fsub_rn(dw, inner)) : __fmul_rn(w, dw);
+    for (int j = 0; j < top_k; ++j) {
+        const int e = __shfl_sync(0xFFFFFFFFu, id, j);
+        const float d = __shfl_sync(0xFFFFFFFFu, part, j);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (i * 32 + lane == e) p[i] += d;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        const int e = i * 32 + lane;
+        if (e < experts) {
+            if (F32) static_cast<float*>(dlogits)[t * ldd + e] = p[i];
+            else static_cast<uint16_t*>(dlogits)[t * ldd + e] = (uint16_t)pack_bf16x2(p[i], 0.0f);
+        }
+    }
+}
+
+}  // namespace
+
+template <bool F32>
+static cudaError_t route(const void* logits, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize, int32_t* ids,
+                         float* weights, cudaStream_t stream) {
+    auto go = [&](auto kernel) {
+        return launch_chained(kernel, dim3((unsigned)((tokens + ROUTE_WARPS - 1) / ROUTE_WARPS)), dim3(32 * ROUTE_WARPS), 0, 0, stream,
+                              logits, ldl, tokens, experts, top_k, normalize, ids, weights);
+    };
+    if (experts <= 64) return go(moe_route_kernel<2, F32>);
+    if (experts <= 128) return go(moe_route_kernel<4, F32>);
+    if (experts <= 256) return go(moe_route_kernel<8, F32>);
+    if (experts <= 512) return go(moe_route_kernel<16, F32>);
+    return go(moe_route_kernel<32, F32>);
+}
+
+template <bool F32>
+static cudaError_t route_backward(const void* logits, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize,
+                                  const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd, cudaStream_t stream) {
+    auto go = [&](auto kernel) {
+        return launch_chained(kernel, dim3((unsigned)((tokens + ROUTE_WARPS - 1) / ROUTE_WARPS)), dim3(32 * ROUTE_WARPS), 0, 0, stream,
+                              logits, ldl, tokens, experts, top_k, normalize, ids, dweights, dlogits, ldd);
+    };
+    if (experts <= 64) return go(moe_route_backward_kernel<2, F32>);
+    if (experts <= 128) return go(moe_route_backward_kernel<4, F32>);
+    if (experts <= 256) return go(moe_route_backward_kernel<8, F32>);
+    if (experts <= 512) return go(moe_route_backward_kernel<16, F32>);
+    return go(moe_route_backward_kernel<32, F32>);
+}
+
+cudaError_t launch_moe_route(const void* logits, bool f32, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize,
+                             int32_t* ids, float* weights, cudaStream_t stream) {
+    return f32 ? route<true>(logits, ldl, tokens, experts, top_k, normalize, ids, weights, stream)
+               : route<false>(logits, ldl, tokens, experts, top_k, normalize, ids, weights, stream);
+}
+
+cudaError_t launch_moe_route_backward(const void* logits, bool f32, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize,
+                                      const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd, cudaStream_t stream) {
+    return f32 ? route_backward<true>(logits, ldl, tokens, experts, top_k, normalize, ids, dweights, dlogits, ldd, stream)
+               : route_backward<false>(logits, ldl, tokens, experts, top_k, normalize, ids, dweights, dlogits, ldd, stream);
+}
+
+}  // namespace mxk

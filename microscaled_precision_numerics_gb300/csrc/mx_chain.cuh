@@ -23,11 +23,11 @@ __device__ __forceinline__ T load_global(const T* p) {
 
 // cluster 0: a launch without clusters.
 template <typename... Params, typename... Args>
-inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+inline cudaError_t launch_chained(void (*kernel)(Params...), dim3 grid, dim3 threads, size_t smem, unsigned cluster,
                                   cudaStream_t stream, Args&&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[2] = {};

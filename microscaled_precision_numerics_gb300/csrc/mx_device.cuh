@@ -302,6 +302,17 @@ __device__ __forceinline__ uint32_t fold_halves(uint32_t m2) {
 }
 
 // ---------------------------------------------------------------------------------------------
+// MXFP8 block scale from the block's largest magnitude (BF16 bits).
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t e8m0_from_amax_bits(uint32_t amax16) {
+    const int ef = (int)((amax16 >> 7) & 0xFFu);   // BF16 exponent field (0 for zero/subnormal)
+    return (uint32_t)max(ef - 8, 0);                 // clamp e = ef - 127 - 8 at -127
+}
+
+// 2^-e for scale byte s (e = s - 127): exponent field 254 - s, always a normal FP32.
+__device__ __forceinline__ float inv_scale_from_e8m0(uint32_t s) { return __uint_as_float((254u - s) << 23); }
+
+// ---------------------------------------------------------------------------------------------
 // Expert-group tables for the grouped scale layout: group g's rows [off[g], off[g+1]) start at
 // padded 128-row tile ptile[g] = sum over j < g of ceil(m_j / 128).  Built by a whole block:
 // offsets copied to shared memory, tile counts scanned in parallel (warp shuffles + one pass over

@@ -195,6 +195,35 @@ struct MatvecArgs {
 };
 cudaError_t launch_matvec_nvfp4(const MatvecArgs& a, cudaStream_t stream);
 
+// Norm with residual and MXFP8 output, and its gradient (norm.cu).
+cudaError_t launch_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, const void* w, bool w32,
+                           float eps, int64_t rows, int64_t cols, uint16_t* sum, int64_t lds, uint16_t* y, int64_t ldy,
+                           uint8_t* q_row, uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, cudaStream_t stream);
+size_t rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
+cudaError_t launch_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* h, int64_t ldh, const void* w, bool w32,
+                                    float eps, int64_t rows, int64_t cols, const uint16_t* dsum, int64_t ldds, uint16_t* dx,
+                                    int64_t lddx, float* dweight, void* workspace, cudaStream_t stream);
+
+// The router's choice of experts and its gradient (moe_route.cu); tokens sorted by expert and back (moe_rows.cu).
+cudaError_t launch_moe_route(const void* logits, bool f32, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize,
+                             int32_t* ids, float* weights, cudaStream_t stream);
+cudaError_t launch_moe_route_backward(const void* logits, bool f32, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize,
+                                      const int32_t* ids, const float* dweights, void* dlogits, int64_t ldd, cudaStream_t stream);
+size_t moe_sort_workspace_bytes(int64_t choices, int64_t experts);
+cudaError_t launch_moe_sort(const int32_t* ids, int64_t choices, int experts, int64_t* offsets, int32_t* rows, int32_t* source,
+                            void* workspace, cudaStream_t stream);
+cudaError_t launch_moe_dispatch(const uint16_t* x, int64_t ldx, int64_t tokens, int64_t hidden, const int32_t* rows, int top_k,
+                                uint16_t* y, int64_t ldy, int64_t total_rows, cudaStream_t stream);
+cudaError_t launch_moe_dispatch_quantized(bool fp4, const uint8_t* q, const uint8_t* s, const float* s2, int64_t tokens, int64_t hidden,
+                                          const int32_t* rows, int top_k, int G, const int64_t* offsets, uint8_t* q_out, uint8_t* s_out,
+                                          float* s2_out, int64_t total_rows, cudaStream_t stream);
+cudaError_t launch_moe_combine(const uint16_t* z, int64_t ldz, int64_t total_rows, int64_t hidden, const int32_t* rows,
+                               const float* weights, int64_t tokens, int top_k, const uint16_t* residual, int64_t ldr, uint16_t* y,
+                               int64_t ldy, cudaStream_t stream);
+cudaError_t launch_moe_combine_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int64_t total_rows,
+                                        int64_t hidden, const int32_t* rows, const float* weights, int64_t tokens, int top_k,
+                                        uint16_t* dz, int64_t lddz, float* dweights, cudaStream_t stream);
+
 int device_sm_count();
 
 }  // namespace mxk

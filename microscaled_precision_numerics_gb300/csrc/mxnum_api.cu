@@ -1,6 +1,7 @@
-// mxnum_api.cu -- the C ABI of libmxnum.so: argument validation and launches (see include/mxnum.h and include/mxnum_generate.h).
+// mxnum_api.cu -- the C ABI of libmxnum.so: argument validation and launches (see include/mxnum.h, include/mxnum_generate.h and include/mxnum_layer.h).
 #include "../../include/mxnum.h"
 #include "../../include/mxnum_generate.h"
+#include "../../include/mxnum_layer.h"
 #include "mx_internal.h"
 #include "mx_kv.cuh"
 
@@ -559,6 +560,183 @@ mx_status mx_nvfp4_matvec(const void* x, int64_t ldx, const uint8_t* q, const ui
     a.q = q; a.s = s; a.s2 = s2; a.s2_per_row = s2_scope == MX_SCOPE_ROW;
     a.M = (int)M; a.N = N; a.K = K; a.y = y; a.ldy = ldy; a.y_fp32 = y_fp32 != 0;
     return from_cuda(mxk::launch_matvec_nvfp4(a, stream));
+}
+
+static mx_status check_weight(const void* weight, mx_dtype type) {
+    if (!weight || (type != MX_DTYPE_BF16 && type != MX_DTYPE_FP32)) return MX_ERR_INVALID_ARG;
+    return aligned16(weight) ? MX_OK : MX_ERR_ALIGNMENT;
+}
+
+// BF16 rows of `cols` elements `ld` apart, each on 16 bytes.
+static mx_status check_rows(const void* x, int64_t ld, int64_t cols) {
+    if (!x || ld < cols) return MX_ERR_INVALID_ARG;
+    return aligned16(x) && (ld % 8) == 0 && (cols % 8) == 0 ? MX_OK : MX_ERR_ALIGNMENT;
+}
+
+static bool norm_eps_taken(float eps) { return eps >= 0.0f && eps <= 3.402823466e38f; }
+
+mx_status mx_rmsnorm_mxfp8(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                           mx_dtype weight_type, float eps, int64_t rows, int64_t cols, void* sum, int64_t lds, void* y,
+                           int64_t ldy, uint8_t* q_row, uint8_t* s_row, uint8_t* q_col, uint8_t* s_col,
+                           cudaStream_t stream) {
+    if (rows <= 0 || cols <= 0 || !norm_eps_taken(eps) || (!y && !q_row && !q_col) || (q_row && !s_row) || (q_col && !s_col) ||
+        (sum && !residual))
+        return MX_ERR_INVALID_ARG;
+    mx_status st = check_weight(weight, weight_type);
+    if (st == MX_OK) st = check_rows(x, ldx, cols);
+    if (st == MX_OK && residual) st = check_rows(residual, ldr, cols);
+    if (st == MX_OK && sum) st = check_rows(sum, lds, cols);
+    if (st == MX_OK && y) st = check_rows(y, ldy, cols);
+    if (st == MX_OK && ((q_row && (!aligned16(q_row) || !aligned16(s_row))) || (q_col && (!aligned16(q_col) || !aligned16(s_col)))))
+        st = MX_ERR_ALIGNMENT;
+    if (st == MX_OK && (cols > MX_RMSNORM_MAX_COLS || rows > INT32_MAX || (q_row && (cols % 32) != 0) || (q_col && (rows % 32) != 0)))
+        st = MX_ERR_UNSUPPORTED;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_rmsnorm(static_cast<const uint16_t*>(x), ldx, static_cast<const uint16_t*>(residual), ldr, weight,
+                                         weight_type == MX_DTYPE_FP32, eps, rows, cols, static_cast<uint16_t*>(sum), lds,
+                                         static_cast<uint16_t*>(y), ldy, q_row, s_row, q_col, s_col, stream));
+}
+
+size_t mx_rmsnorm_workspace_bytes(int64_t rows, int64_t cols) {
+    if (rows <= 0 || cols <= 0 || cols > MX_RMSNORM_MAX_COLS) return 0;
+    return mxk::rmsnorm_workspace_bytes(rows, cols);
+}
+
+mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* weight,
+                              mx_dtype weight_type, float eps, int64_t rows, int64_t cols, const void* dsum, int64_t ldds,
+                              void* dx, int64_t lddx, float* dweight, void* workspace, size_t workspace_bytes,
+                              cudaStream_t stream) {
+    if (rows <= 0 || cols <= 0 || !norm_eps_taken(eps) || !dweight || !workspace) return MX_ERR_INVALID_ARG;
+    mx_status st = check_weight(weight, weight_type);
+    if (st == MX_OK) st = check_rows(dy, lddy, cols);
+    if (st == MX_OK) st = check_rows(h, ldh, cols);
+    if (st == MX_OK) st = check_rows(dx, lddx, cols);
+    if (st == MX_OK && dsum) st = check_rows(dsum, ldds, cols);
+    if (st == MX_OK && (!aligned4(dweight) || !aligned16(workspace))) st = MX_ERR_ALIGNMENT;
+    if (st == MX_OK && (cols > MX_RMSNORM_MAX_COLS || rows > INT32_MAX)) st = MX_ERR_UNSUPPORTED;
+    if (st == MX_OK && workspace_bytes < mx_rmsnorm_workspace_bytes(rows, cols)) st = MX_ERR_INVALID_ARG;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_rmsnorm_backward(static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(h), ldh, weight,
+                                                  weight_type == MX_DTYPE_FP32, eps, rows, cols, static_cast<const uint16_t*>(dsum),
+                                                  ldds, static_cast<uint16_t*>(dx), lddx, dweight, workspace, stream));
+}
+
+// Logits (or their gradient) [tokens, ld] by type, on their own alignment.
+static mx_status check_logits(const void* logits, mx_dtype type, int64_t ld, int64_t experts) {
+    if (!logits || ld < experts || (type != MX_DTYPE_BF16 && type != MX_DTYPE_FP32)) return MX_ERR_INVALID_ARG;
+    return aligned4(logits) ? MX_OK : MX_ERR_ALIGNMENT;
+}
+
+static mx_status check_choices(int64_t tokens, int64_t top_k) {
+    if (tokens <= 0 || top_k <= 0) return MX_ERR_INVALID_ARG;
+    return top_k <= MX_MOE_MAX_TOP_K && tokens <= INT32_MAX / top_k ? MX_OK : MX_ERR_UNSUPPORTED;
+}
+
+mx_status mx_moe_route(const void* logits, mx_dtype logits_type, int64_t ldl, int64_t tokens, int64_t experts, int64_t top_k,
+                       int normalize, int32_t* ids, float* weights, cudaStream_t stream) {
+    if (!ids || !weights || experts <= 0 || (normalize != 0 && normalize != 1) || top_k > experts) return MX_ERR_INVALID_ARG;
+    mx_status st = check_logits(logits, logits_type, ldl, experts);
+    if (st == MX_OK && (!aligned4(ids) || !aligned4(weights))) st = MX_ERR_ALIGNMENT;
+    if (st == MX_OK) st = check_choices(tokens, top_k);
+    if (st == MX_OK && experts > MX_MAX_GROUPS) st = MX_ERR_UNSUPPORTED;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_moe_route(logits, logits_type == MX_DTYPE_FP32, ldl, tokens, (int)experts, (int)top_k, normalize, ids,
+                                           weights, stream));
+}
+
+mx_status mx_moe_route_backward(const void* logits, mx_dtype logits_type, int64_t ldl, int64_t tokens, int64_t experts,
+                                int64_t top_k, int normalize, const int32_t* ids, const float* dweights, void* dlogits,
+                                int64_t ldd, cudaStream_t stream) {
+    if (!ids || !dweights || experts <= 0 || (normalize != 0 && normalize != 1) || top_k > experts) return MX_ERR_INVALID_ARG;
+    mx_status st = check_logits(logits, logits_type, ldl, experts);
+    if (st == MX_OK) st = check_logits(dlogits, logits_type, ldd, experts);
+    if (st == MX_OK && (!aligned4(ids) || !aligned4(dweights))) st = MX_ERR_ALIGNMENT;
+    if (st == MX_OK) st = check_choices(tokens, top_k);
+    if (st == MX_OK && experts > MX_MAX_GROUPS) st = MX_ERR_UNSUPPORTED;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_moe_route_backward(logits, logits_type == MX_DTYPE_FP32, ldl, tokens, (int)experts, (int)top_k, normalize,
+                                                    ids, dweights, dlogits, ldd, stream));
+}
+
+size_t mx_moe_sort_workspace_bytes(int64_t choices, int64_t experts) {
+    if (choices <= 0 || choices > INT32_MAX || experts <= 0 || experts > MX_MAX_GROUPS) return 0;
+    return mxk::moe_sort_workspace_bytes(choices, experts);
+}
+
+mx_status mx_moe_sort(const int32_t* ids, int64_t tokens, int64_t top_k, int64_t experts, int64_t* group_offsets,
+                      int32_t* rows, int32_t* source, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (!ids || !group_offsets || !rows || !workspace || experts <= 0) return MX_ERR_INVALID_ARG;
+    mx_status st = aligned4(ids) && aligned16(group_offsets) && aligned4(rows) && aligned4(source) && aligned16(workspace)
+                       ? MX_OK : MX_ERR_ALIGNMENT;
+    if (st == MX_OK) st = check_choices(tokens, top_k);
+    if (st == MX_OK && experts > MX_MAX_GROUPS) st = MX_ERR_UNSUPPORTED;
+    if (st == MX_OK && workspace_bytes < mx_moe_sort_workspace_bytes(tokens * top_k, experts)) st = MX_ERR_INVALID_ARG;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_moe_sort(ids, tokens * top_k, (int)experts, group_offsets, rows, source, workspace, stream));
+}
+
+// What dispatch and combine share: the choices' rows and the sizes.
+static mx_status check_moe_rows(const int32_t* rows, int64_t tokens, int64_t top_k, int64_t hidden, int64_t total_rows) {
+    if (!rows || hidden <= 0 || total_rows <= 0) return MX_ERR_INVALID_ARG;
+    if (!aligned4(rows)) return MX_ERR_ALIGNMENT;
+    const mx_status st = check_choices(tokens, top_k);
+    if (st != MX_OK) return st;
+    return hidden <= (int64_t(1) << 23) && total_rows <= INT32_MAX ? MX_OK : MX_ERR_UNSUPPORTED;
+}
+
+mx_status mx_moe_dispatch(const void* x, int64_t ldx, int64_t tokens, int64_t hidden, const int32_t* rows, int64_t top_k,
+                          void* y, int64_t ldy, int64_t total_rows, cudaStream_t stream) {
+    mx_status st = check_moe_rows(rows, tokens, top_k, hidden, total_rows);
+    if (st == MX_OK) st = check_rows(x, ldx, hidden);
+    if (st == MX_OK) st = check_rows(y, ldy, hidden);
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_moe_dispatch(static_cast<const uint16_t*>(x), ldx, tokens, hidden, rows, (int)top_k,
+                                              static_cast<uint16_t*>(y), ldy, total_rows, stream));
+}
+
+mx_status mx_moe_dispatch_quantized(mx_format fmt, const uint8_t* q, const uint8_t* s, const float* s2, int64_t tokens,
+                                    int64_t hidden, const int32_t* rows, int64_t top_k, int64_t G,
+                                    const int64_t* group_offsets, uint8_t* q_out, uint8_t* s_out, float* s2_out,
+                                    int64_t total_rows, cudaStream_t stream) {
+    if ((fmt != MX_FMT_MXFP8 && fmt != MX_FMT_NVFP4) || !q || !s || !q_out || !s_out || !group_offsets || G <= 0 || G > MX_MAX_GROUPS ||
+        (fmt == MX_FMT_NVFP4) != (s2 != nullptr) || (fmt == MX_FMT_NVFP4) != (s2_out != nullptr))
+        return MX_ERR_INVALID_ARG;
+    mx_status st = check_moe_rows(rows, tokens, top_k, hidden, total_rows);
+    if (st == MX_OK && (!aligned16(q) || !aligned16(s) || !aligned4(s2) || !aligned16(q_out) || !aligned16(s_out) || !aligned4(s2_out) ||
+                        !aligned16(group_offsets)))
+        st = MX_ERR_ALIGNMENT;
+    if (st == MX_OK && (hidden % 32) != 0) st = MX_ERR_UNSUPPORTED;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_moe_dispatch_quantized(fmt == MX_FMT_NVFP4, q, s, s2, tokens, hidden, rows, (int)top_k, (int)G,
+                                                        group_offsets, q_out, s_out, s2_out, total_rows, stream));
+}
+
+mx_status mx_moe_combine(const void* z, int64_t ldz, int64_t total_rows, int64_t hidden, const int32_t* rows,
+                         const float* weights, int64_t tokens, int64_t top_k, const void* residual, int64_t ldr, void* y,
+                         int64_t ldy, cudaStream_t stream) {
+    mx_status st = check_moe_rows(rows, tokens, top_k, hidden, total_rows);
+    if (st == MX_OK) st = check_rows(z, ldz, hidden);
+    if (st == MX_OK) st = check_rows(y, ldy, hidden);
+    if (st == MX_OK && residual) st = check_rows(residual, ldr, hidden);
+    if (st == MX_OK && !aligned4(weights)) st = MX_ERR_ALIGNMENT;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_moe_combine(static_cast<const uint16_t*>(z), ldz, total_rows, hidden, rows, weights, tokens, (int)top_k,
+                                             static_cast<const uint16_t*>(residual), ldr, static_cast<uint16_t*>(y), ldy, stream));
+}
+
+mx_status mx_moe_combine_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz, int64_t total_rows, int64_t hidden,
+                                  const int32_t* rows, const float* weights, int64_t tokens, int64_t top_k, void* dz,
+                                  int64_t lddz, float* dweights, cudaStream_t stream) {
+    mx_status st = check_moe_rows(rows, tokens, top_k, hidden, total_rows);
+    if (st == MX_OK && (!weights || !dweights)) st = MX_ERR_INVALID_ARG;
+    if (st == MX_OK) st = check_rows(dy, lddy, hidden);
+    if (st == MX_OK) st = check_rows(z, ldz, hidden);
+    if (st == MX_OK) st = check_rows(dz, lddz, hidden);
+    if (st == MX_OK && (!aligned4(weights) || !aligned4(dweights))) st = MX_ERR_ALIGNMENT;
+    if (st != MX_OK) return st;
+    return from_cuda(mxk::launch_moe_combine_backward(static_cast<const uint16_t*>(dy), lddy, static_cast<const uint16_t*>(z), ldz,
+                                                      total_rows, hidden, rows, weights, tokens, (int)top_k, static_cast<uint16_t*>(dz),
+                                                      lddz, dweights, stream));
 }
 
 mx_status mx_check_device_status(void) {

@@ -26,14 +26,6 @@ constexpr int QT_ROWS = 128;
 constexpr int QT_COLS = 128;
 constexpr int QT_THREADS = 256;
 
-__device__ __forceinline__ uint32_t e8m0_from_amax_bits(uint32_t amax16) {
-    const int ef = (int)((amax16 >> 7) & 0xFFu);   // BF16 exponent field (0 for zero/subnormal)
-    return (uint32_t)max(ef - 8, 0);                 // clamp e = ef - 127 - 8 at -127
-}
-
-// 2^-e for scale byte s (e = s - 127): exponent field 254 - s, always a normal FP32.
-__device__ __forceinline__ float inv_scale_from_e8m0(uint32_t s) { return __uint_as_float((254u - s) << 23); }
-
 // Quantize 32 BF16 values held as 16 packed words; writes 32 code bytes into out[8] words.
 __device__ __forceinline__ uint32_t mxfp8_block32(const uint32_t w[16], uint32_t out[8], uint32_t& amax16) {
     uint32_t m2 = absmax_bf16x2(w[0], w[1]);
