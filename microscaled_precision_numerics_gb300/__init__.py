@@ -696,22 +696,45 @@ MX_RMSNORM_MAX_COLS, MX_MOE_MAX_TOP_K = 16384, 32
 _DTYPES = {torch.bfloat16: MX_DTYPE_BF16, torch.float32: MX_DTYPE_FP32}
 
 
-def _rows2d(fn: str, name: str, t, dtype, rows, cols, cur: int):
-    """(pointer, row stride, rows, columns) of a [rows, cols] view with unit column stride."""
+def _refuse_rows(fn: str, name: str, t, dtype, rows, cols):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{fn}: {name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols) or (
-            shape[1] > 1 and stride[1] != 1):
-        raise ValueError(f"{fn}: {name} must be [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}] with unit "
-                         f"column stride, got {tuple(shape)}")
-    return t.data_ptr() if t.get_device() == cur else _p(t), stride[0] if shape[0] > 1 else shape[1], shape[0], shape[1]
+    raise ValueError(f"{fn}: {name} must be [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}] with unit "
+                     f"column stride, got {tuple(t.shape)}")
 
 
-def _maybe(f, fn, name, t, *args):
-    return None if t is None else f(fn, name, t, *args)
+def _rows2d(fn: str, name: str, t, dtype, rows, cols, cur: int):
+    """(pointer, row stride, rows, columns) of a [rows, cols] view with unit column stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != 2:
+        _refuse_rows(fn, name, t, dtype, rows, cols)
+    (n, m), (step, unit) = t.shape, t.stride()
+    if (rows is not None and n != rows) or (cols is not None and m != cols) or (unit != 1 and m > 1):
+        _refuse_rows(fn, name, t, dtype, rows, cols)
+    return t.data_ptr() if t.get_device() == cur else _p(t), step if n > 1 else m, n, m
+
+
+def _like(fn: str, name: str, t, dtype, shape, cur: int):
+    """(pointer, row stride) of a view of this type and 2-D shape with unit column stride; (None, 0) of None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+        _refuse_rows(fn, name, t, dtype, *shape)
+    step, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        _refuse_rows(fn, name, t, dtype, *shape)
+    return t.data_ptr() if t.get_device() == cur else _p(t), step if shape[0] > 1 else shape[1]
+
+
+def _bytes_in(fn: str, name: str, t, n: int, cur: int):
+    """The pointer of a contiguous uint8 array of at least n elements, or None."""
+    return None if t is None else _array(fn, name, t, torch.uint8, n, cur)
+
+
+def _scale_layout_bytes(rows: int, columns: int) -> int:
+    """mx_scale_bytes for a count of scale columns."""
+    return (rows + 127) // 128 * ((columns + 3) // 4) * 512
 
 
 def _ids2d(fn: str, name: str, t):
@@ -749,73 +772,73 @@ def mx_rmsnorm_mxfp8(x, weight, eps: float, residual=None, sum_out=None, y=None,
                      stream=None):
     """Root-mean-square norm of x + residual [rows, cols] (BF16, any row stride) times weight [cols] (BF16 or FP32): the sum into
     sum_out (which may be x or residual), the output into y and as MXFP8 into q_row, s_row and q_col, s_col (alloc_mxfp8)."""
-    fn, bf = "mx_rmsnorm_mxfp8", torch.bfloat16
-    cur = _device_of(x)
+    fn, bf, cur = "mx_rmsnorm_mxfp8", torch.bfloat16, _device_of(x)
     xp, ldx, rows, cols = _rows2d(fn, "x", x, bf, None, None, cur)
+    shape = x.shape
     wp, wt = _norm_weight(fn, weight, cols, cur)
-    rp, ldr = (None, 0) if residual is None else _rows2d(fn, "residual", residual, bf, rows, cols, cur)[:2]
-    sp, lds = (None, 0) if sum_out is None else _rows2d(fn, "sum_out", sum_out, bf, rows, cols, cur)[:2]
-    yp, ldy = (None, 0) if y is None else _rows2d(fn, "y", y, bf, rows, cols, cur)[:2]
-    u8, n = torch.uint8, rows * cols
+    rp, ldr = _like(fn, "residual", residual, bf, shape, cur)
+    sp, lds = _like(fn, "sum_out", sum_out, bf, shape, cur)
+    yp, ldy = _like(fn, "y", y, bf, shape, cur)
+    n = rows * cols
     _check(fn, lib().mx_rmsnorm_mxfp8(
-        xp, ldx, rp, ldr, wp, wt, eps, rows, cols, sp, lds, yp, ldy, _maybe(_array, fn, "q_row", q_row, u8, n, cur),
-        None if s_row is None else _array(fn, "s_row", s_row, u8, scale_bytes(rows, cols, 32), cur),
-        _maybe(_array, fn, "q_col", q_col, u8, n, cur),
-        None if s_col is None else _array(fn, "s_col", s_col, u8, scale_bytes(cols, rows, 32), cur), _stream_on(cur, stream)))
+        xp, ldx, rp, ldr, wp, wt, eps, rows, cols, sp, lds, yp, ldy, _bytes_in(fn, "q_row", q_row, n, cur),
+        _bytes_in(fn, "s_row", s_row, _scale_layout_bytes(rows, cols // 32), cur), _bytes_in(fn, "q_col", q_col, n, cur),
+        _bytes_in(fn, "s_col", s_col, _scale_layout_bytes(cols, rows // 32), cur), _stream_on(cur, stream)))
 
 
 def mx_rmsnorm_backward(dy, h, weight, eps: float, dx, dweight, workspace, dsum=None, stream=None):
     """Gradient of mx_rmsnorm_mxfp8 from dy [rows, cols]: dx (of the norm's input h and, where it is a sum, of both summands, with dsum
     added; it may be dsum or dy) and dweight [cols] (FP32)."""
-    fn, bf = "mx_rmsnorm_backward", torch.bfloat16
-    cur = _device_of(h)
+    fn, bf, cur = "mx_rmsnorm_backward", torch.bfloat16, _device_of(h)
     hp, ldh, rows, cols = _rows2d(fn, "h", h, bf, None, None, cur)
+    shape = h.shape
     wp, wt = _norm_weight(fn, weight, cols, cur)
-    gp, ldg = _rows2d(fn, "dy", dy, bf, rows, cols, cur)[:2]
-    sp, lds = (None, 0) if dsum is None else _rows2d(fn, "dsum", dsum, bf, rows, cols, cur)[:2]
-    xp, ldx = _rows2d(fn, "dx", dx, bf, rows, cols, cur)[:2]
+    gp, ldg, _, _ = _rows2d(fn, "dy", dy, bf, rows, cols, cur)
+    sp, lds = _like(fn, "dsum", dsum, bf, shape, cur)
+    xp, ldx, _, _ = _rows2d(fn, "dx", dx, bf, rows, cols, cur)
     ws, ws_bytes = _workspace(fn, workspace, cur)
     _check(fn, lib().mx_rmsnorm_backward(gp, ldg, hp, ldh, wp, wt, eps, rows, cols, sp, lds, xp, ldx,
                                          _array(fn, "dweight", dweight, torch.float32, cols, cur), ws, ws_bytes, _stream_on(cur, stream)))
 
 
-def _logits(fn: str, name: str, t, dtype, tokens, experts, cur: int):
-    if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+def _logits_type(fn: str, name: str, t) -> int:
+    kind = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if kind is None:
         raise TypeError(f"{fn}: {name} must be a bfloat16 or float32 tensor")
-    return _rows2d(fn, name, t, dtype or t.dtype, tokens, experts, cur)
+    return kind
 
 
 def mx_moe_route(logits, ids, weights, normalize: bool = True, stream=None):
     """The top_k largest logits [tokens, experts] (BF16 or FP32) of each token into ids [tokens, top_k] (int32) and their softmax, over
     the chosen ones or (normalize False) over all, into weights [tokens, top_k] (FP32)."""
-    fn, cur = "mx_moe_route", _device_of(logits)
+    fn, cur, kind = "mx_moe_route", _device_of(logits), _logits_type("mx_moe_route", "logits", logits)
     T, k = _ids2d(fn, "ids", ids)
-    lp, ldl, _, E = _logits(fn, "logits", logits, None, T, None, cur)
-    _check(fn, lib().mx_moe_route(lp, _DTYPES[logits.dtype], ldl, T, E, k, int(normalize), _array(fn, "ids", ids, torch.int32, T * k, cur),
+    lp, ldl, _, E = _rows2d(fn, "logits", logits, logits.dtype, T, None, cur)
+    _check(fn, lib().mx_moe_route(lp, kind, ldl, T, E, k, 1 if normalize else 0, _array(fn, "ids", ids, torch.int32, T * k, cur),
                                   _array(fn, "weights", weights, torch.float32, T * k, cur), _stream_on(cur, stream)))
 
 
 def mx_moe_route_backward(logits, ids, dweights, dlogits, normalize: bool = True, stream=None):
     """dlogits (of the logits' type) from the gradient of mx_moe_route's weights."""
-    fn, cur = "mx_moe_route_backward", _device_of(logits)
+    fn, cur, kind = "mx_moe_route_backward", _device_of(logits), _logits_type("mx_moe_route_backward", "logits", logits)
     T, k = _ids2d(fn, "ids", ids)
-    lp, ldl, _, E = _logits(fn, "logits", logits, None, T, None, cur)
-    dp, ldd, _, _ = _logits(fn, "dlogits", dlogits, logits.dtype, T, E, cur)
+    lp, ldl, _, E = _rows2d(fn, "logits", logits, logits.dtype, T, None, cur)
+    dp, ldd, _, _ = _rows2d(fn, "dlogits", dlogits, logits.dtype, T, E, cur)
     _check(fn, lib().mx_moe_route_backward(
-        lp, _DTYPES[logits.dtype], ldl, T, E, k, int(normalize), _array(fn, "ids", ids, torch.int32, T * k, cur),
+        lp, kind, ldl, T, E, k, 1 if normalize else 0, _array(fn, "ids", ids, torch.int32, T * k, cur),
         _array(fn, "dweights", dweights, torch.float32, T * k, cur), dp, ldd, _stream_on(cur, stream)))
 
 
 def mx_moe_sort(ids, group_offsets, rows, source, workspace, stream=None):
     """The choices ids [tokens, top_k] sorted by expert: group_offsets [experts + 1] (int64), the row of each choice (rows [tokens, top_k],
     -1 for an id outside the experts) and the choice of each row (source [tokens * top_k] or None)."""
-    fn, cur = "mx_moe_sort", _device_of(ids)
+    fn, i32, cur = "mx_moe_sort", torch.int32, _device_of(ids)
     T, k = _ids2d(fn, "ids", ids)
-    i32, G = torch.int32, group_offsets.numel() - 1
+    n, G = T * k, group_offsets.numel() - 1
     ws, ws_bytes = _workspace(fn, workspace, cur)
     _check(fn, lib().mx_moe_sort(
-        _array(fn, "ids", ids, i32, T * k, cur), T, k, G, _array(fn, "group_offsets", group_offsets, torch.int64, G + 1, cur),
-        _array(fn, "rows", rows, i32, T * k, cur), _maybe(_array, fn, "source", source, i32, T * k, cur), ws, ws_bytes,
+        _array(fn, "ids", ids, i32, n, cur), T, k, G, _array(fn, "group_offsets", group_offsets, torch.int64, G + 1, cur),
+        _array(fn, "rows", rows, i32, n, cur), None if source is None else _array(fn, "source", source, i32, n, cur), ws, ws_bytes,
         _stream_on(cur, stream)))
 
 
@@ -832,19 +855,18 @@ def mx_moe_dispatch(x, rows, y, stream=None):
 def mx_moe_dispatch_quantized(fmt: int, q, s, rows, group_offsets, q_out, s_out, s2=None, s2_out=None, stream=None):
     """mx_moe_dispatch of rows that are quantized already (q [tokens, hidden] E4M3 bytes or [tokens, hidden / 2] packed E2M1 with their
     scales s, and s2 for NVFP4), the scales into the grouped layout."""
-    fn, u8, cur = "mx_moe_dispatch_quantized", torch.uint8, _device_of(q)
+    fn, u8, f32, cur = "mx_moe_dispatch_quantized", torch.uint8, torch.float32, _device_of(q)
     T, k = _ids2d(fn, "rows", rows)
-    fp4 = fmt == MX_FMT_NVFP4
-    if q.dim() != 2 or q.shape[0] != T or q_out.dim() != 2 or q_out.shape[1] != q.shape[1]:
+    nbytes, R, G = q.shape[-1], q_out.shape[0] if q_out.dim() else 0, group_offsets.numel() - 1
+    if q.shape != (T, nbytes) or q_out.shape != (R, nbytes):
         raise ValueError(f"{fn}: q must be [{T}, bytes] and q_out [total_rows, bytes], got {tuple(q.shape)} and {tuple(q_out.shape)}")
-    nbytes, R, G, f32 = q.shape[1], q_out.shape[0], group_offsets.numel() - 1, torch.float32
-    H, block = (2 * nbytes, 16) if fp4 else (nbytes, 32)
+    H, columns = (2 * nbytes, nbytes // 8) if fmt == MX_FMT_NVFP4 else (nbytes, nbytes // 32)
     _check(fn, lib().mx_moe_dispatch_quantized(
-        fmt, _array(fn, "q", q, u8, T * nbytes, cur), _array(fn, "s", s, u8, scale_bytes(T, H, block), cur),
-        _maybe(_array, fn, "s2", s2, f32, T, cur), T, H, _array(fn, "rows", rows, torch.int32, T * k, cur), k, G,
+        fmt, _array(fn, "q", q, u8, T * nbytes, cur), _array(fn, "s", s, u8, _scale_layout_bytes(T, columns), cur),
+        None if s2 is None else _array(fn, "s2", s2, f32, T, cur), T, H, _array(fn, "rows", rows, torch.int32, T * k, cur), k, G,
         _array(fn, "group_offsets", group_offsets, torch.int64, G + 1, cur), _array(fn, "q_out", q_out, u8, R * nbytes, cur),
-        _array(fn, "s_out", s_out, u8, grouped_scale_bytes(R, G, H, block), cur), _maybe(_array, fn, "s2_out", s2_out, f32, R, cur), R,
-        _stream_on(cur, stream)))
+        _array(fn, "s_out", s_out, u8, _scale_layout_bytes(R + 127 * G, columns), cur),
+        None if s2_out is None else _array(fn, "s2_out", s2_out, f32, R, cur), R, _stream_on(cur, stream)))
 
 
 def mx_moe_combine(z, rows, y, weights=None, residual=None, stream=None):
@@ -853,21 +875,21 @@ def mx_moe_combine(z, rows, y, weights=None, residual=None, stream=None):
     fn, bf, cur = "mx_moe_combine", torch.bfloat16, _device_of(z)
     T, k = _ids2d(fn, "rows", rows)
     zp, ldz, R, H = _rows2d(fn, "z", z, bf, None, None, cur)
-    yp, ldy = _rows2d(fn, "y", y, bf, T, H, cur)[:2]
-    rp, ldr = (None, 0) if residual is None else _rows2d(fn, "residual", residual, bf, T, H, cur)[:2]
+    yp, ldy, _, _ = _rows2d(fn, "y", y, bf, T, H, cur)
+    rp, ldr = _like(fn, "residual", residual, bf, y.shape, cur)
     _check(fn, lib().mx_moe_combine(
-        zp, ldz, R, H, _array(fn, "rows", rows, torch.int32, T * k, cur), _maybe(_array, fn, "weights", weights, torch.float32, T * k, cur),
-        T, k, rp, ldr, yp, ldy, _stream_on(cur, stream)))
+        zp, ldz, R, H, _array(fn, "rows", rows, torch.int32, T * k, cur),
+        None if weights is None else _array(fn, "weights", weights, torch.float32, T * k, cur), T, k, rp, ldr, yp, ldy,
+        _stream_on(cur, stream)))
 
 
 def mx_moe_combine_backward(dy, z, rows, weights, dz, dweights, stream=None):
     """Gradients of mx_moe_combine: dz[rows[t, j]] = weights[t, j] * dy[t] (dz may be z) and dweights[t, j] = dy[t] . z[rows[t, j]]."""
-    fn, bf, cur = "mx_moe_combine_backward", torch.bfloat16, _device_of(z)
+    fn, bf, f32, cur = "mx_moe_combine_backward", torch.bfloat16, torch.float32, _device_of(z)
     T, k = _ids2d(fn, "rows", rows)
     zp, ldz, R, H = _rows2d(fn, "z", z, bf, None, None, cur)
-    gp, ldg = _rows2d(fn, "dy", dy, bf, T, H, cur)[:2]
-    dp, ldd = _rows2d(fn, "dz", dz, bf, R, H, cur)[:2]
-    f32 = torch.float32
+    gp, ldg, _, _ = _rows2d(fn, "dy", dy, bf, T, H, cur)
+    dp, ldd, _, _ = _rows2d(fn, "dz", dz, bf, R, H, cur)
     _check(fn, lib().mx_moe_combine_backward(
         gp, ldg, zp, ldz, R, H, _array(fn, "rows", rows, torch.int32, T * k, cur), _array(fn, "weights", weights, f32, T * k, cur), T, k,
         dp, ldd, _array(fn, "dweights", dweights, f32, T * k, cur), _stream_on(cur, stream)))
