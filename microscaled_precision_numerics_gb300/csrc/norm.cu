@@ -23,21 +23,36 @@ namespace {
 constexpr int SEG = 256;                                  // elements of a segment: 32 lanes of 8
 constexpr int MAX_SEGS = MX_RMSNORM_MAX_COLS / SEG;       // 64
 
-struct RowNorm {                                          // 1 / sqrt(mean + eps) of a row
+struct RowNorm {                                          // 1 / sqrt(mean + eps) of a row as p * r
+    float p;                                              // a power of two, 1 unless the row was summed in FP64
     float r;
-    double wide;                                          // used in place of r where it is not zero
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = bf16_lo(w[i]);
-        f[2 * i + 1] = bf16_hi(w[i]);
-    }
+using Pairs = uint64_t[4];                                // eight FP32 values as packed pairs
+__device__ __forceinline__ void unpack8(const uint4& v, Pairs& f) {
+    f[0] = f2_pack(bf16_lo(v.x), bf16_hi(v.x));
+    f[1] = f2_pack(bf16_lo(v.y), bf16_hi(v.y));
+    f[2] = f2_pack(bf16_lo(v.z), bf16_hi(v.z));
+    f[3] = f2_pack(bf16_lo(v.w), bf16_hi(v.w));
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ uint4 pack8(const Pairs& f) {
+    return make_uint4(pack_pair(f[0]), pack_pair(f[1]), pack_pair(f[2]), pack_pair(f[3]));
+}
+__device__ __forceinline__ void times8(Pairs& f, float s) {
+    const uint64_t ss = f2_pack(s, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = f2_mul(f[i], ss);
+}
+__device__ __forceinline__ uint32_t cvt_e4m3_pairs(uint64_t a, uint64_t b) {
+    float a0, a1, b0, b1;
+    f2_unpack(a, a0, a1);
+    f2_unpack(b, b0, b1);
+    return cvt_e4m3x4(a0, a1, b0, b1);
 }
 
 template <typename T>
@@ -47,29 +62,66 @@ __device__ __forceinline__ T butterfly(T v) {
     return v;
 }
 
-// BF16(a + b) of eight pairs.
-__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
-    float x[8], y[8];
-    unpack8(a, x);
-    unpack8(b, y);
+// The butterfly sums of N values of every lane at once (N = 1, 2, 4, 8): lane l gets that of value l / (32 / N).  As long as
+// a lane has more than one it keeps half of them and gives the other half to its partner, so eight sums take 9 exchanges
+// instead of 40, and each is added up in the butterfly's order.
+template <int N>
+__device__ __forceinline__ float butterfly_of(const float (&v)[N]) {
+    const int lane = threadIdx.x & 31;
+    float w[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(x[i], y[i]);
-    return pack8(x);
+    for (int i = 0; i < N; ++i) w[i] = v[i];
+    int o = 16;
+#pragma unroll
+    for (int n = N; n > 1; n >>= 1, o >>= 1) {
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = upper ? w[i + n / 2] : w[i], give = upper ? w[i] : w[i + n / 2];
+            w[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+        }
+    }
+#pragma unroll
+    for (; o > 0; o >>= 1) w[0] += __shfl_xor_sync(0xFFFFFFFFu, w[0], o);
+    return w[0];
+}
+template <int N>
+__device__ __forceinline__ int value_of_lane() { return (threadIdx.x & 31) / (32 / N); }
+template <int N>
+__device__ __forceinline__ bool first_of_value() { return (threadIdx.x & (32 / N - 1)) == 0; }
+
+// BF16(a + b) of eight pairs: one rounding, the same as that of the FP32 sum (two BF16 values that are further apart than FP32 is
+// wide do not come near a BF16 rounding boundary).
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
+    return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
 }
 
+__device__ __forceinline__ float sum_pair(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return __fadd_rn(lo, hi);
+}
 __device__ __forceinline__ float squares8(const uint4& v) {
-    float f[8], s = 0.0f;
+    Pairs f;
     unpack8(v, f);
+    uint64_t s = f2_mul(f[0], f[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = __fmaf_rn(f[i], f[i], s);
-    return s;
+    for (int i = 1; i < 4; ++i) s = f2_fma(f[i], f[i], s);
+    return sum_pair(s);
 }
 __device__ __forceinline__ double squares8_wide(const uint4& v) {
-    float f[8];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     double s = 0.0;
-    unpack8(v, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = __fma_rn((double)f[i], (double)f[i], s);
+    for (int i = 0; i < 4; ++i) {
+        s = __fma_rn((double)bf16_lo(w[i]), (double)bf16_lo(w[i]), s);
+        s = __fma_rn((double)bf16_hi(w[i]), (double)bf16_hi(w[i]), s);
+    }
     return s;
 }
 
@@ -79,31 +131,27 @@ __device__ __forceinline__ bool fp32_holds(float ss, float eps) {
     return ss <= FLT_MAX && (ss >= 8.27180613e-25f || eps >= 8.67361738e-19f);        // 2^-80, 2^-60
 }
 __device__ __forceinline__ RowNorm norm_of(float ss, float inv_cols, float eps) {
-    return RowNorm{__fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(ss, inv_cols), eps))), 0.0};
+    return RowNorm{1.0f, __frsqrt_rn(__fadd_rn(__fmul_rn(ss, inv_cols), eps))};
 }
+// The same from FP64, split so that neither factor leaves FP32's normal range where the product does.
 __device__ __forceinline__ RowNorm norm_of_wide(double ss, double cols, float eps) {
-    return RowNorm{0.0f, 1.0 / sqrt(ss / cols + (double)eps)};
+    const double r = 1.0 / sqrt(ss / cols + (double)eps);
+    if (!(r > 0.0) || isinf(r)) return RowNorm{1.0f, (float)r};
+    const int e = max(-126, min(127, ilogb(r)));
+    return RowNorm{__uint_as_float((uint32_t)(e + 127) << 23), (float)(r * exp2(-(double)e))};
 }
-// A call, so that FP64 stays behind a branch: as a selection between both products it cost 600 us of 8192 x 4096's 680.
-__device__ __noinline__ float times_wide(float h, double r) { return (float)((double)h * r); }
-__device__ __forceinline__ void normed8(float (&f)[8], const RowNorm& n) {
-    if (n.wide == 0.0) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], n.r);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = times_wide(f[j], n.wide);
-    }
+__device__ __forceinline__ void normed8(Pairs& f, const RowNorm& n) {
+    if (n.p != 1.0f) times8(f, n.p);
+    times8(f, n.r);
 }
 
 // Eight weights from column c on.
 template <bool W32>
-__device__ __forceinline__ void weights8(const void* w, int c, float (&f)[8]) {
+__device__ __forceinline__ void weights8(const void* w, int c, Pairs& f) {
     if (W32) {
-        const float4 a = load_global(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c));
-        const float4 b = load_global(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c) + 1);
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+        const ulonglong2 a = load_global(reinterpret_cast<const ulonglong2*>(static_cast<const float*>(w) + c));
+        const ulonglong2 b = load_global(reinterpret_cast<const ulonglong2*>(static_cast<const float*>(w) + c) + 1);
+        f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
     } else {
         unpack8(load_global(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c)), f);
     }
@@ -114,16 +162,10 @@ __device__ __forceinline__ void row_sync(int row, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(row + 1), "r"(threads) : "memory");
 }
 
-// The sum over a row of per-lane parts, part[i] of segment warp + i * warps: in shared memory sm[segments], in the fixed order.
-template <int NV, typename T>
-__device__ __forceinline__ T row_sum(const T (&part)[NV], T* sm, int row, int threads, int nseg) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = threads >> 5;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const T s = butterfly(part[i]);
-        if (lane == 0 && warp + i * warps < nseg) sm[warp + i * warps] = s;
-    }
-    row_sync(row, threads);
+// The sum over a row's segments in sm, in the fixed order.
+template <typename T>
+__device__ __forceinline__ T segments_sum(const T* sm, int nseg) {
+    const int lane = threadIdx.x & 31;
     T v = lane < nseg ? sm[lane] : T(0);
     if (lane + 32 < nseg) v += sm[lane + 32];
     return butterfly(v);
@@ -147,23 +189,21 @@ __device__ __forceinline__ void quantize_row8(const NormArgs& a, int64_t row, in
     m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     const uint32_t s = e8m0_from_amax_bits(fold_halves(m));
-    const float inv = inv_scale_from_e8m0(s);
     if (c < a.cols) {
-        float f[8];
+        Pairs f;
         unpack8(y, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], inv);
-        *reinterpret_cast<uint2*>(a.q_row + row * a.cols + c) =
-            make_uint2(cvt_e4m3x4(f[0], f[1], f[2], f[3]), cvt_e4m3x4(f[4], f[5], f[6], f[7]));
+        times8(f, inv_scale_from_e8m0(s));
+        *reinterpret_cast<uint2*>(a.q_row + row * a.cols + c) = make_uint2(cvt_e4m3_pairs(f[0], f[1]), cvt_e4m3_pairs(f[2], f[3]));
     }
     if ((c & 31) == 0 && (c >> 5) < 4 * nct) a.s_row[sf_offset(row, c >> 5, nct)] = c < a.cols ? (uint8_t)s : (uint8_t)0;
 }
 
-constexpr int NR_THREADS = 256;
-
 // Without column-wise codes: one row a group of blockDim.x threads, blockDim.y rows a CTA; NV vectors of eight elements a thread.
+// At most four a thread and 64 registers: with eight, one CTA an SM ran through 32 KB of straight-line code for every row
+// (1003 x 14336 took 54 us).
+constexpr int NR_THREADS = 512;
 template <int NV, bool W32>
-__global__ void __launch_bounds__(NR_THREADS) norm_rows_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs a) {
     __shared__ double sm_all[8][MAX_SEGS];
     chain_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, ty = threadIdx.y;
@@ -178,39 +218,56 @@ __global__ void __launch_bounds__(NR_THREADS) norm_rows_kernel(const NormArgs a)
     }
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + ty;
     if (row >= a.rows) return;
+    const int c0 = (warp * 32 + lane) * 8, step = warps * SEG;
     uint4 h[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        h[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c0 + i * step < a.cols) h[i] = load_global(reinterpret_cast<const uint4*>(a.x + row * a.ldx + c0 + i * step));
+    }
+    if (a.residual) {
+        uint4 r[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (c0 + i * step < a.cols) r[i] = load_global(reinterpret_cast<const uint4*>(a.residual + row * a.ldr + c0 + i * step));
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (c0 + i * step < a.cols) {
+                h[i] = add8(h[i], r[i]);
+                if (a.sum) *reinterpret_cast<uint4*>(a.sum + row * a.lds + c0 + i * step) = h[i];
+            }
+    }
     float part[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = ((warp + i * warps) * 32 + lane) * 8;
-        h[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (c < a.cols) {
-            h[i] = load_global(reinterpret_cast<const uint4*>(a.x + row * a.ldx + c));
-            if (a.residual) h[i] = add8(h[i], load_global(reinterpret_cast<const uint4*>(a.residual + row * a.ldr + c)));
-            if (a.sum) *reinterpret_cast<uint4*>(a.sum + row * a.lds + c) = h[i];
-        }
-        part[i] = squares8(h[i]);
-    }
-    const float ss = row_sum(part, reinterpret_cast<float*>(sm_all[ty]), ty, blockDim.x, nseg);
+    for (int i = 0; i < NV; ++i) part[i] = squares8(h[i]);
+    float* sm = reinterpret_cast<float*>(sm_all[ty]);
+    const float mine = butterfly_of(part);
+    const int my_seg = warp + value_of_lane<NV>() * warps;
+    if (first_of_value<NV>() && my_seg < nseg) sm[my_seg] = mine;
+    row_sync(ty, blockDim.x);
+    const float ss = segments_sum(sm, nseg);
     RowNorm n = norm_of(ss, a.inv_cols, a.eps);
     if (!fp32_holds(ss, a.eps)) {                          // the same for all threads of the row
-        double wide[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) wide[i] = squares8_wide(h[i]);
         row_sync(ty, blockDim.x);                          // the FP32 sums have been read
-        n = norm_of_wide(row_sum(wide, sm_all[ty], ty, blockDim.x, nseg), a.cols, a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const double s = butterfly(squares8_wide(h[i]));
+            if (lane == 0 && warp + i * warps < nseg) sm_all[ty][warp + i * warps] = s;
+        }
+        row_sync(ty, blockDim.x);
+        n = norm_of_wide(segments_sum(sm_all[ty], nseg), a.cols, a.eps);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = ((warp + i * warps) * 32 + lane) * 8;
+        const int c = c0 + i * step;
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
         if (c < a.cols) {
-            float f[8], w[8];
+            Pairs f, w;
             unpack8(h[i], f);
             weights8<W32>(a.w, c, w);
             normed8(f, n);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], w[j]);
+            for (int j = 0; j < 4; ++j) f[j] = f2_mul(f[j], w[j]);
             y = pack8(f);
             if (a.y) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = y;
         }
@@ -245,21 +302,22 @@ __device__ __forceinline__ uint32_t peer_address(const void* mine, uint32_t peer
 }
 
 constexpr int TILE_ROWS = 32;
+constexpr int PART = MAX_SEGS + 1;                         // pitch of the sums of a row, odd against bank conflicts
 template <int SEGS>
 struct TileCfg {
     static constexpr int THREADS = 128 * SEGS;             // 4 * SEGS warps, each eight of the 32 * SEGS (row, segment) pairs
     static constexpr int COLS = SEG * SEGS;
     static constexpr int TILE = TILE_ROWS * COLS * 2;      // bytes; the FP64 sums of a slow tile lie there before it is written
-    static constexpr int SMEM = TILE + TILE_ROWS * MAX_SEGS * 4;
-    static_assert(TILE >= TILE_ROWS * MAX_SEGS * 8, "the FP64 sums fit the tile");
+    static constexpr int SMEM = TILE + TILE_ROWS * PART * 4;
+    static_assert(TILE >= TILE_ROWS * PART * 8, "the FP64 sums fit the tile");
 };
 
 template <int SEGS, bool W32>
 __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, SEGS == 2 ? 3 : 1) norm_tile_kernel(const NormArgs a) {
     using C = TileCfg<SEGS>;
-    constexpr int WARPS = C::THREADS / 32, ITEMS = 8;
+    constexpr int WARPS = C::THREADS / 32, ITEMS = 8, ROWS_A_WARP = TILE_ROWS / WARPS;
     extern __shared__ __align__(16) uint8_t sm_tile[];
-    float* part = reinterpret_cast<float*>(sm_tile + C::TILE);            // [32][MAX_SEGS]
+    float* part = reinterpret_cast<float*>(sm_tile + C::TILE);            // [32][PART]
     double* part_wide = reinterpret_cast<double*>(sm_tile);               // the same in FP64
     __shared__ RowNorm s_norm[TILE_ROWS];
     cluster_arrive();                                      // this CTA runs: the others may write into its shared memory
@@ -269,78 +327,76 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, SEGS == 2 ? 3 : 1) nor
     const int nseg = (a.cols + SEG - 1) / SEG;
     const int64_t r0 = (int64_t)(blockIdx.x / peers) * TILE_ROWS;
     const int c_cta = (int)rank * C::COLS;
-    // item i of a warp: row (warp + i * WARPS) / SEGS, segment (warp + i * WARPS) % SEGS of the CTA; WARPS is a multiple of SEGS
-    const int seg = warp % SEGS, c = c_cta + seg * SEG + lane * 8, gseg = (int)rank * SEGS + seg;
+    // item i of a warp: row warp / SEGS + 4 i, segment warp % SEGS of the CTA
+    const int seg = warp % SEGS, c = c_cta + seg * SEG + lane * 8, gseg = (int)rank * SEGS + seg, row0 = warp / SEGS;
     const bool in = c < a.cols;
-    auto row_of = [&](int i) { return (warp + i * WARPS) / SEGS; };
     uint4 h[ITEMS];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
         h[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (in) h[i] = load_global(reinterpret_cast<const uint4*>(a.x + (r0 + row_of(i)) * a.ldx + c));
+        if (in) h[i] = load_global(reinterpret_cast<const uint4*>(a.x + (r0 + row0 + 4 * i) * a.ldx + c));
     }
     if (a.residual && in) {
         uint4 r[ITEMS];
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) r[i] = load_global(reinterpret_cast<const uint4*>(a.residual + (r0 + row_of(i)) * a.ldr + c));
+        for (int i = 0; i < ITEMS; ++i) r[i] = load_global(reinterpret_cast<const uint4*>(a.residual + (r0 + row0 + 4 * i) * a.ldr + c));
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) h[i] = add8(h[i], r[i]);
         if (a.sum)
 #pragma unroll
-            for (int i = 0; i < ITEMS; ++i) *reinterpret_cast<uint4*>(a.sum + (r0 + row_of(i)) * a.lds + c) = h[i];
+            for (int i = 0; i < ITEMS; ++i) *reinterpret_cast<uint4*>(a.sum + (r0 + row0 + 4 * i) * a.lds + c) = h[i];
     }
-    cluster_wait();
-    const uint32_t there = (uint32_t)lane < peers ? peer_address(part, lane) : 0u;
+    float sums[ITEMS];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const float s = butterfly(squares8(h[i]));
-        if ((uint32_t)lane < peers && gseg < nseg)
-            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(there + (row_of(i) * MAX_SEGS + gseg) * 4), "f"(s) : "memory");
+    for (int i = 0; i < ITEMS; ++i) sums[i] = squares8(h[i]);
+    const float mine = butterfly_of(sums);                 // that of row row0 + 4 * (lane / 4)
+    cluster_wait();
+    if (gseg < nseg) {
+        const float* at = part + (row0 + 4 * value_of_lane<ITEMS>()) * PART + gseg;
+        for (uint32_t p = lane & 3; p < peers; p += 4)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(peer_address(at, p)), "f"(mine) : "memory");
     }
     cluster_sync();
-    bool fine = true;
-    for (int r = warp; r < TILE_ROWS; r += WARPS) {
-        float v = lane < nseg ? part[r * MAX_SEGS + lane] : 0.0f;
-        if (lane + 32 < nseg) v += part[r * MAX_SEGS + lane + 32];
-        const float ss = butterfly(v);
-        fine = fine && fp32_holds(ss, a.eps);
-        if (lane == 0) s_norm[r] = norm_of(ss, a.inv_cols, a.eps);
+    float v[ROWS_A_WARP];
+#pragma unroll
+    for (int i = 0; i < ROWS_A_WARP; ++i) {
+        const float* at = part + (warp + i * WARPS) * PART + lane;
+        v[i] = lane < nseg ? at[0] : 0.0f;
+        if (lane + 32 < nseg) v[i] += at[32];
     }
+    const float ss = butterfly_of(v);
+    const int my_row = warp + value_of_lane<ROWS_A_WARP>() * WARPS;
+    const bool fine = fp32_holds(ss, a.eps);
+    if (first_of_value<ROWS_A_WARP>()) s_norm[my_row] = norm_of(ss, a.inv_cols, a.eps);
     if (__syncthreads_or(!fine)) {                         // the same in every CTA of the cluster: all have the same sums
-        const uint32_t wide_there = (uint32_t)lane < peers ? peer_address(part_wide, lane) : 0u;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
             const double s = butterfly(squares8_wide(h[i]));
             if ((uint32_t)lane < peers && gseg < nseg)
-                asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(wide_there + (row_of(i) * MAX_SEGS + gseg) * 8), "d"(s) : "memory");
+                asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(peer_address(part_wide + (row0 + 4 * i) * PART + gseg, lane)), "d"(s)
+                             : "memory");
         }
         cluster_sync();
         for (int r = warp; r < TILE_ROWS; r += WARPS) {
-            float v = lane < nseg ? part[r * MAX_SEGS + lane] : 0.0f;
-            double w = lane < nseg ? part_wide[r * MAX_SEGS + lane] : 0.0;
-            if (lane + 32 < nseg) {
-                v += part[r * MAX_SEGS + lane + 32];
-                w += part_wide[r * MAX_SEGS + lane + 32];
-            }
-            const bool row_fine = fp32_holds(butterfly(v), a.eps);
-            const double ss = butterfly(w);
-            if (lane == 0 && !row_fine) s_norm[r] = norm_of_wide(ss, a.cols, a.eps);
+            const bool row_fine = fp32_holds(segments_sum(part + r * PART, nseg), a.eps);
+            const double wide = segments_sum(part_wide + r * PART, nseg);
+            if (lane == 0 && !row_fine) s_norm[r] = norm_of_wide(wide, a.cols, a.eps);
         }
         __syncthreads();
     }
     const int64_t nct_row = sf_col_tiles(a.cols, 32);
-    float w[8];
+    Pairs w;
     if (in) weights8<W32>(a.w, c, w);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        const int r = row_of(i);
+        const int r = row0 + 4 * i;
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
         if (in) {
-            float f[8];
+            Pairs f;
             unpack8(h[i], f);
             normed8(f, s_norm[r]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], w[j]);
+            for (int j = 0; j < 4; ++j) f[j] = f2_mul(f[j], w[j]);
             y = pack8(f);
             if (a.y) *reinterpret_cast<uint4*>(a.y + (r0 + r) * a.ldy + c) = y;
         }
@@ -360,34 +416,34 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, SEGS == 2 ? 3 : 1) nor
     const int padded_cols = (a.cols + 127) & ~127;
     if (warp * 64 >= C::COLS || c_cta + warp * 64 >= padded_cols) return;
     const bool gin = gc < a.cols;
-    uint4 v[8];
+    uint32_t t[4][8];                                      // word k holds columns 2 k and 2 k + 1 of eight rows
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(sm_tile + ((q * 8 + i) * C::COLS + cc) * 2);
-    uint32_t m[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        m[0] = absmax_bf16x2(m[0], v[i].x); m[1] = absmax_bf16x2(m[1], v[i].y);
-        m[2] = absmax_bf16x2(m[2], v[i].z); m[3] = absmax_bf16x2(m[3], v[i].w);
+    for (int i = 0; i < 8; ++i) {
+        const uint4 y = *reinterpret_cast<const uint4*>(sm_tile + ((q * 8 + i) * C::COLS + cc) * 2);
+        t[0][i] = y.x; t[1][i] = y.y; t[2][i] = y.z; t[3][i] = y.w;
     }
+    uint8_t* q_col = a.q_col + (int64_t)gc * a.rows + r0 + q * 8;
+    uint8_t* s_col = a.s_col + sf_offset(gc, r0 / 32, nct);               // eight columns of a tile are 16 bytes apart
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        m[k] = absmax_bf16x2(m[k], __shfl_xor_sync(0xFFFFFFFFu, m[k], 8));
-        m[k] = abs_halves(absmax_bf16x2(m[k], __shfl_xor_sync(0xFFFFFFFFu, m[k], 16)));
-    }
+        uint32_t m = t[k][0];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t s = e8m0_from_amax_bits((j & 1) ? (m[j >> 1] >> 16) : (m[j >> 1] & 0xFFFFu));
-        const float inv = inv_scale_from_e8m0(s);
-        float f[8];
+        for (int i = 1; i < 8; ++i) m = absmax_bf16x2(m, t[k][i]);
+        m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+        m = abs_halves(absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16)));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t word = (j >> 1) == 0 ? v[i].x : ((j >> 1) == 1 ? v[i].y : ((j >> 1) == 2 ? v[i].z : v[i].w));
-            f[i] = __fmul_rn((j & 1) ? bf16_hi(word) : bf16_lo(word), inv);
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t s = e8m0_from_amax_bits(j ? m >> 16 : m & 0xFFFFu);
+            const float inv = inv_scale_from_e8m0(s);
+            Pairs f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                f[i] = j ? f2_pack(bf16_hi(t[k][2 * i]), bf16_hi(t[k][2 * i + 1])) : f2_pack(bf16_lo(t[k][2 * i]), bf16_lo(t[k][2 * i + 1]));
+            times8(f, inv);
+            if (gin)
+                *reinterpret_cast<uint2*>(q_col + (int64_t)(2 * k + j) * a.rows) = make_uint2(cvt_e4m3_pairs(f[0], f[1]), cvt_e4m3_pairs(f[2], f[3]));
+            if (q == 0) s_col[(2 * k + j) * 16] = gin ? (uint8_t)s : (uint8_t)0;
         }
-        if (gin)
-            *reinterpret_cast<uint2*>(a.q_col + (int64_t)(gc + j) * a.rows + r0 + q * 8) =
-                make_uint2(cvt_e4m3x4(f[0], f[1], f[2], f[3]), cvt_e4m3x4(f[4], f[5], f[6], f[7]));
-        if (q == 0) a.s_col[sf_offset(gc + j, r0 / 32, nct)] = gin ? (uint8_t)s : (uint8_t)0;
     }
     // scale columns from rows / 32 up to a whole word: zeros
     if (r0 + TILE_ROWS == a.rows && q == 0)
@@ -396,8 +452,8 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, SEGS == 2 ? 3 : 1) nor
 }
 
 // ------------------------------------------------------------------------------------------------
-// Gradient.  A CTA walks rows; each thread keeps the sums of dw for its columns in registers, and the CTAs' sums meet in the
-// workspace, where a second kernel adds them in the order of the CTAs.
+// Gradient.  A CTA walks rows; each thread keeps the sums of dw for its columns in registers.  The CTAs of a cluster add theirs
+// up through shared memory, and a second kernel adds the clusters' sums in their order.
 // ------------------------------------------------------------------------------------------------
 struct NormBackwardArgs {
     const uint16_t* dy; int64_t lddy;
@@ -411,10 +467,11 @@ struct NormBackwardArgs {
 };
 
 constexpr int NB_THREADS = 256;
-constexpr int NB_CTAS = 304;                               // most partial sums of a column
-// Stages of the ring: two for wide rows (four vectors a thread and more), where three would leave room for one CTA or none.
+constexpr int NB_PARTS = 76;                               // most partial sums of a column: clusters that run at once on 152 SMs
+// CTAs of an SM by the registers and shared memory that NV vectors a thread take, and as many CTAs in a cluster twice over.
 template <int NV>
-constexpr int NB_STAGES = NV <= 2 ? 3 : 2;
+constexpr int NB_PER_SM = NV <= 2 ? 4 : NV == 4 ? 2 : 1;
+constexpr int NB_STAGES = 2;
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
@@ -425,24 +482,23 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
 }
 
-// A thread fetches its own vectors of the rows to come into shared memory (nobody else reads them there, so no barrier guards
-// them), one or two rows ahead: the loads wait in no registers, and a row's sums do not hold up the next row's.
+// A thread fetches its own vectors of the next row into shared memory (nobody else reads them there, so no barrier guards
+// them) while it works on this one: the loads wait in no registers, and a row's sums do not hold up the next row's.
 template <int NV, bool W32>
-__global__ void __launch_bounds__(NB_THREADS) norm_backward_kernel(const NormBackwardArgs a) {
-    constexpr int STAGES = NB_STAGES<NV>;
+__global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kernel(const NormBackwardArgs a) {
     extern __shared__ __align__(16) uint8_t sm_rows[];     // [stage][dy, h, dsum][NV][thread] of 16 bytes
     __shared__ double sm_all[2][2][MAX_SEGS];
     chain_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int nseg = (a.cols + SEG - 1) / SEG, tensors = a.dsum ? 3 : 2;
-    const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm_rows) + threadIdx.x * 16;
     const uint32_t vector = blockDim.x * 16, tensor = NV * vector, stage_bytes = tensors * tensor;
-    auto col = [&](int i) { return ((warp + i * warps) * 32 + lane) * 8; };
+    const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm_rows) + threadIdx.x * 16;
+    const int c0 = (warp * 32 + lane) * 8, step = warps * SEG;
     auto fetch = [&](int64_t row, uint32_t stage) {
         if (row < a.rows) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = col(i);
+                const int c = c0 + i * step;
                 if (c >= a.cols) continue;
                 const uint32_t at = sm0 + stage * stage_bytes + i * vector;
                 copy16(at, a.dy + row * a.lddy + c);
@@ -455,114 +511,127 @@ __global__ void __launch_bounds__(NB_THREADS) norm_backward_kernel(const NormBac
     auto fetched = [&](uint32_t stage, int which, int i) {
         return *reinterpret_cast<const uint4*>(sm_rows + stage * stage_bytes + which * tensor + i * vector + threadIdx.x * 16);
     };
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-    float dw[NV][8] = {};
-    int turn = 0;
-    uint32_t stage = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1, stage = stage + 1 == STAGES ? 0 : stage + 1) {
-        // the stage that this fills was read in the turn before, by this thread
-        fetch(row + (int64_t)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
-        copies_wait<STAGES - 1>();
-        uint4 h[NV], g[NV];
-        float* sm_s = reinterpret_cast<float*>(sm_all[turn][0]);
-        float* sm_c = reinterpret_cast<float*>(sm_all[turn][1]);
+    fetch(blockIdx.x, 0);
+    Pairs dw[NV] = {};
+    uint32_t turn = 0;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
+        fetch(row + gridDim.x, turn ^ 1);                  // into the stage that this thread read in the turn before
+        copies_wait<1>();
+        float parts[2 * NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = col(i);
-            h[i] = g[i] = make_uint4(0u, 0u, 0u, 0u);
-            float inner = 0.0f;
-            if (c < a.cols) {
-                g[i] = fetched(stage, 0, i);
-                h[i] = fetched(stage, 1, i);
-                float x[8], d[8], w[8];
-                unpack8(h[i], x);
-                unpack8(g[i], d);
-                weights8<W32>(a.w, c, w);
+            const int c = c0 + i * step;
+            parts[i] = parts[NV + i] = 0.0f;
+            if (c >= a.cols) continue;
+            const uint4 h = fetched(turn, 1, i);
+            Pairs x, d, w;
+            unpack8(h, x);
+            unpack8(fetched(turn, 0, i), d);
+            weights8<W32>(a.w, c, w);
+            uint64_t inner = f2_mul(f2_mul(d[0], w[0]), x[0]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) inner = __fmaf_rn(__fmul_rn(d[j], w[j]), x[j], inner);
-            }
-            const float s = butterfly(squares8(h[i]));
-            inner = butterfly(inner);
-            if (lane == 0 && warp + i * warps < nseg) {
-                sm_s[warp + i * warps] = s;
-                sm_c[warp + i * warps] = inner;
-            }
+            for (int j = 1; j < 4; ++j) inner = f2_fma(f2_mul(d[j], w[j]), x[j], inner);
+            parts[i] = squares8(h);
+            parts[NV + i] = sum_pair(inner);
         }
+        float* sm_s = reinterpret_cast<float*>(sm_all[turn][0]);
+        float* sm_c = reinterpret_cast<float*>(sm_all[turn][1]);
+        const float mine = butterfly_of(parts);
+        const int value = value_of_lane<2 * NV>(), my_seg = warp + (value % NV) * warps;
+        if (first_of_value<2 * NV>() && my_seg < nseg) (value < NV ? sm_s : sm_c)[my_seg] = mine;
         __syncthreads();
-        float ss = lane < nseg ? sm_s[lane] : 0.0f, cc = lane < nseg ? sm_c[lane] : 0.0f;
+        float v[2] = {lane < nseg ? sm_s[lane] : 0.0f, lane < nseg ? sm_c[lane] : 0.0f};
         if (lane + 32 < nseg) {
-            ss += sm_s[lane + 32];
-            cc += sm_c[lane + 32];
+            v[0] += sm_s[lane + 32];
+            v[1] += sm_c[lane + 32];
         }
-        ss = butterfly(ss);
-        cc = butterfly(cc);
+        const float ss = butterfly(v[0]), cc = butterfly(v[1]);
         RowNorm n = norm_of(ss, a.inv_cols, a.eps);
         float mean = __fmul_rn(__fmul_rn(cc, a.inv_cols), n.r);          // mean(dn n)
         // the products dn h likewise: too large, or so small that subnormals would decide (where eps does not)
         if (!fp32_holds(ss, a.eps) || !(fabsf(cc) <= FLT_MAX) || (fabsf(cc) < 7.88860905e-31f && a.eps < 9.09494702e-13f)) {
             __syncthreads();                                             // the FP32 sums have been read
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < NV; ++i) {
-                const int c = col(i);
-                double inner = 0.0;
+                const int c = c0 + i * step;
+                double inner = 0.0, squares = 0.0;
                 if (c < a.cols) {
-                    float x[8], d[8], w[8];
-                    unpack8(h[i], x);
-                    unpack8(g[i], d);
+                    const uint4 h = fetched(turn, 1, i);
+                    Pairs x, d, w;
+                    unpack8(h, x);
+                    unpack8(fetched(turn, 0, i), d);
                     weights8<W32>(a.w, c, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) inner = __fma_rn((double)d[j] * (double)w[j], (double)x[j], inner);
+                    for (int j = 0; j < 4; ++j) {
+                        float x0, x1, d0, d1, w0, w1;
+                        f2_unpack(x[j], x0, x1);
+                        f2_unpack(d[j], d0, d1);
+                        f2_unpack(w[j], w0, w1);
+                        inner = __fma_rn((double)d0 * (double)w0, (double)x0, inner);
+                        inner = __fma_rn((double)d1 * (double)w1, (double)x1, inner);
+                    }
+                    squares = squares8_wide(h);
                 }
-                const double s = butterfly(squares8_wide(h[i]));
+                squares = butterfly(squares);
                 inner = butterfly(inner);
                 if (lane == 0 && warp + i * warps < nseg) {
-                    sm_all[turn][0][warp + i * warps] = s;
+                    sm_all[turn][0][warp + i * warps] = squares;
                     sm_all[turn][1][warp + i * warps] = inner;
                 }
             }
             __syncthreads();
-            double s_wide = 0.0, c_wide = 0.0;
-            for (int s = lane; s < nseg; s += 32) {
-                s_wide += sm_all[turn][0][s];
-                c_wide += sm_all[turn][1][s];
-            }
-            n = norm_of_wide(butterfly(s_wide), a.cols, a.eps);
-            mean = (float)(butterfly(c_wide) * n.wide / a.cols);
+            n = norm_of_wide(segments_sum(sm_all[turn][0], nseg), a.cols, a.eps);
+            mean = (float)(segments_sum(sm_all[turn][1], nseg) / a.cols * n.p * n.r);
         }
+        const uint64_t minus_mean = f2_pack(-mean, -mean);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = col(i);
+            const int c = c0 + i * step;
             if (c >= a.cols) continue;
-            float x[8], d[8], w[8], o[8];
-            unpack8(h[i], x);
-            unpack8(g[i], d);
+            Pairs x, d, w, o;
+            unpack8(fetched(turn, 1, i), x);
+            unpack8(fetched(turn, 0, i), d);
             weights8<W32>(a.w, c, w);
             normed8(x, n);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                o[j] = __fmaf_rn(-x[j], mean, __fmul_rn(d[j], w[j]));
-                dw[i][j] = __fmaf_rn(d[j], x[j], dw[i][j]);
+            for (int j = 0; j < 4; ++j) {
+                o[j] = f2_fma(x[j], minus_mean, f2_mul(d[j], w[j]));
+                dw[i][j] = f2_fma(d[j], x[j], dw[i][j]);
             }
-            normed8(o, n);
+            times8(o, n.r);
+            if (n.p != 1.0f) times8(o, n.p);
             if (a.dsum) {
-                float s[8];
-                unpack8(fetched(stage, 2, i), s);
+                unpack8(fetched(turn, 2, i), x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = __fadd_rn(o[j], s[j]);
+                for (int j = 0; j < 4; ++j) o[j] = f2_add(o[j], x[j]);
             }
             *reinterpret_cast<uint4*>(a.dx + row * a.lddx + c) = pack8(o);
         }
     }
+    // the cluster's sums: each CTA's in its shared memory (the ring is free: 8 bytes a column and more), a share of the columns each
+    float* sm_dw = reinterpret_cast<float*>(sm_rows);
+    __syncthreads();                                       // the last row has been read
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = col(i);
+        const int c = c0 + i * step;
         if (c < a.cols) {
-            float4* p = reinterpret_cast<float4*>(a.partial + (int64_t)blockIdx.x * a.cols + c);
-            p[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-            p[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+            reinterpret_cast<ulonglong2*>(sm_dw + c)[0] = make_ulonglong2(dw[i][0], dw[i][1]);
+            reinterpret_cast<ulonglong2*>(sm_dw + c)[1] = make_ulonglong2(dw[i][2], dw[i][3]);
         }
     }
+    cluster_sync();
+    const int peers = (int)cluster_size();
+    for (int c = ((int)cluster_rank() * blockDim.x + threadIdx.x) * 4; c < a.cols; c += peers * blockDim.x * 4) {
+        uint64_t s0 = 0, s1 = 0;
+        for (int p = 0; p < peers; ++p) {
+            uint64_t v0, v1;
+            asm volatile("ld.shared::cluster.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(peer_address(sm_dw + c, p)) : "memory");
+            s0 = f2_add(s0, v0);
+            s1 = f2_add(s1, v1);
+        }
+        *reinterpret_cast<ulonglong2*>(a.partial + (int64_t)(blockIdx.x / peers) * a.cols + c) = make_ulonglong2(s0, s1);
+    }
+    cluster_sync();                                        // nobody leaves while the others read its sums
 }
 
 // dw[c] = the sum of `parts` partial sums: 32 columns a CTA, 32 warps a share of the parts each.
@@ -593,17 +662,16 @@ template <bool W32>
 cudaError_t norm_rows(const NormArgs& a, cudaStream_t stream) {
     // many rows: four vectors a thread, so that more bytes are on their way for every row's meeting of its warps; few rows: as
     // many threads a row as have work
-    const bool many = a.rows >= 4 * device_sm_count();
+    const bool many = a.rows >= 512;
     int nv;
-    const int threads = row_threads(a.cols, many ? max(32, (int)min64(NR_THREADS, (a.cols / 32 + 31) / 32 * 32)) : NR_THREADS, nv);
-    const int per = NR_THREADS / threads > 8 ? 8 : max(1, NR_THREADS / threads);
+    const int threads = row_threads(a.cols, many ? (int)min64(NR_THREADS, max64(32, (a.cols / 32 + 31) / 32 * 32)) : NR_THREADS, nv);
+    const int per = max(1, 256 / threads);
     auto go = [&](auto kernel) {
         return launch_chained(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(threads, per), 0, 0, stream, a);
     };
     if (nv == 1) return go(norm_rows_kernel<1, W32>);
     if (nv == 2) return go(norm_rows_kernel<2, W32>);
-    if (nv == 4) return go(norm_rows_kernel<4, W32>);
-    return go(norm_rows_kernel<8, W32>);
+    return go(norm_rows_kernel<4, W32>);
 }
 
 template <int SEGS, bool W32>
@@ -625,17 +693,19 @@ template <int NV, bool W32>
 cudaError_t norm_backward(const NormBackwardArgs& a, int threads, cudaStream_t stream) {
     auto kernel = norm_backward_kernel<NV, W32>;
     static PerDevice pd;
-    int unused = 0;
-    const cudaError_t e = per_device_once(pd, unused, [kernel](int&) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_STAGES<NV> * 3 * NV * NB_THREADS * 16);
+    int sms = 0;
+    const cudaError_t e = per_device_once(pd, sms, [kernel](int& n) {
+        n = device_sm_count();
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_STAGES * 3 * NV * NB_THREADS * 16);
     });
     if (e != cudaSuccess) return e;
-    const int ctas = (int)min64(a.rows, min(NB_CTAS, (NV == 8 ? 1 : 2) * device_sm_count()));   // that run at once
-    const cudaError_t e2 = launch_chained(kernel, dim3(ctas), dim3(threads), (size_t)NB_STAGES<NV> * (a.dsum ? 3 : 2) * NV * threads * 16, 0,
-                                          stream, a);
+    const int cluster = 2 * NB_PER_SM<NV>;
+    const int parts = (int)min64((a.rows + cluster - 1) / cluster, min(NB_PARTS, sms / 2));
+    const cudaError_t e2 = launch_chained(kernel, dim3(parts * cluster), dim3(threads), (size_t)NB_STAGES * (a.dsum ? 3 : 2) * NV * threads * 16,
+                                          cluster, stream, a);
     if (e2 != cudaSuccess) return e2;
     return launch_chained(norm_dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(32 * ND_WARPS), 0, 0, stream,
-                          static_cast<const float*>(a.partial), ctas, a.cols, a.dw);
+                          static_cast<const float*>(a.partial), parts, a.cols, a.dw);
 }
 
 template <bool W32>
@@ -661,7 +731,7 @@ cudaError_t launch_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* resid
 }
 
 size_t rmsnorm_workspace_bytes(int64_t rows, int64_t cols) {
-    return (size_t)min64(rows, NB_CTAS) * (size_t)cols * sizeof(float);
+    return (size_t)min64(rows, NB_PARTS) * (size_t)cols * sizeof(float);
 }
 
 cudaError_t launch_rmsnorm_backward(const uint16_t* dy, int64_t lddy, const uint16_t* h, int64_t ldh, const void* w, bool w32,
