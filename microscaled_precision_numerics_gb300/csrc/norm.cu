@@ -275,10 +275,10 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
     }
 }
 
-// With column-wise codes: a cluster takes 32 rows, its CTAs T_SEGS segments of them each.  A warp holds whole segments of rows
-// in registers (eight a thread), so the sums of squares of a segment are one butterfly; the CTAs write theirs into each other's
-// shared memory and meet once.  The output goes through shared memory, where a thread finds the 8 x 8 elements whose columns
-// it quantizes.
+// With column-wise codes: a cluster takes 32 rows, its CTAs T_SEGS segments of them each.  A warp takes whole segments of rows
+// (eight a thread), so the sums of squares of a segment are one butterfly; the CTAs write theirs into each other's shared memory
+// and meet once.  The tile waits in shared memory, where the output takes its place and a thread then finds the 8 x 8 elements
+// whose columns it quantizes.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -291,7 +291,7 @@ __device__ __forceinline__ uint32_t cluster_size() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_sync() {           // also orders the shared memory writes before it for the peers
     cluster_arrive();
     cluster_wait();
 }
@@ -307,18 +307,43 @@ template <int SEGS>
 struct TileCfg {
     static constexpr int THREADS = 128 * SEGS;             // 4 * SEGS warps, each eight of the 32 * SEGS (row, segment) pairs
     static constexpr int COLS = SEG * SEGS;
-    static constexpr int TILE = TILE_ROWS * COLS * 2;      // bytes; the FP64 sums of a slow tile lie there before it is written
-    static constexpr int SMEM = TILE + TILE_ROWS * PART * 4;
-    static_assert(TILE >= TILE_ROWS * PART * 8, "the FP64 sums fit the tile");
+    static constexpr int TILE = TILE_ROWS * COLS * 2;      // bytes
+    static constexpr int SMEM = TILE + TILE_ROWS * PART * 4;              // and the rows' sums by segments
 };
 
+// The rows of a tile that FP32 does not hold (their p is 0 so far).  Every CTA of the cluster calls it with all its threads; the
+// FP64 sums of 16 rows at a time take the place of the FP32 ones.
+template <int SEGS>
+__device__ __noinline__ void slow_rows(const NormArgs& a, const uint8_t* sm_tile, float* part, RowNorm* s_norm, int gseg, int nseg,
+                                       uint32_t peers) {
+    constexpr int WARPS = TileCfg<SEGS>::THREADS / 32, HALF = TILE_ROWS / 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seg = warp % SEGS;
+    double* wide = reinterpret_cast<double*>(part);        // [HALF][PART]
+    for (int first = 0; first < TILE_ROWS; first += HALF) {
+        cluster_sync();                                    // what stands there has been read
+#pragma unroll 1
+        for (int r = warp / SEGS; r < HALF; r += 4) {
+            const double s = butterfly(squares8_wide(*reinterpret_cast<const uint4*>(
+                sm_tile + ((first + r) * TileCfg<SEGS>::COLS + seg * SEG + lane * 8) * 2)));
+            if ((uint32_t)lane < peers && gseg < nseg)
+                asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(peer_address(wide + r * PART + gseg, lane)), "d"(s) : "memory");
+        }
+        cluster_sync();
+#pragma unroll 1
+        for (int r = warp; r < HALF; r += WARPS) {
+            const double s = segments_sum(wide + r * PART, nseg);
+            if (lane == 0 && s_norm[first + r].p == 0.0f) s_norm[first + r] = norm_of_wide(s, a.cols, a.eps);
+        }
+    }
+    __syncthreads();
+}
+
 template <int SEGS, bool W32>
-__global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, SEGS == 2 ? 3 : 1) norm_tile_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_kernel(const NormArgs a) {
     using C = TileCfg<SEGS>;
     constexpr int WARPS = C::THREADS / 32, ITEMS = 8, ROWS_A_WARP = TILE_ROWS / WARPS;
     extern __shared__ __align__(16) uint8_t sm_tile[];
     float* part = reinterpret_cast<float*>(sm_tile + C::TILE);            // [32][PART]
-    double* part_wide = reinterpret_cast<double*>(sm_tile);               // the same in FP64
     __shared__ RowNorm s_norm[TILE_ROWS];
     cluster_arrive();                                      // this CTA runs: the others may write into its shared memory
     chain_begin();
@@ -330,25 +355,25 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, SEGS == 2 ? 3 : 1) nor
     // item i of a warp: row warp / SEGS + 4 i, segment warp % SEGS of the CTA
     const int seg = warp % SEGS, c = c_cta + seg * SEG + lane * 8, gseg = (int)rank * SEGS + seg, row0 = warp / SEGS;
     const bool in = c < a.cols;
-    uint4 h[ITEMS];
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        h[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (in) h[i] = load_global(reinterpret_cast<const uint4*>(a.x + (r0 + row0 + 4 * i) * a.ldx + c));
-    }
-    if (a.residual && in) {
-        uint4 r[ITEMS];
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) r[i] = load_global(reinterpret_cast<const uint4*>(a.residual + (r0 + row0 + 4 * i) * a.ldr + c));
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) h[i] = add8(h[i], r[i]);
-        if (a.sum)
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) *reinterpret_cast<uint4*>(a.sum + (r0 + row0 + 4 * i) * a.lds + c) = h[i];
-    }
+    auto place = [&](int i) { return reinterpret_cast<uint4*>(sm_tile + ((row0 + 4 * i) * C::COLS + seg * SEG + lane * 8) * 2); };
     float sums[ITEMS];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) sums[i] = squares8(h[i]);
+    for (int half = 0; half < ITEMS; half += 4) {
+        uint4 h[4], r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (in) h[i] = load_global(reinterpret_cast<const uint4*>(a.x + (r0 + row0 + 4 * (half + i)) * a.ldx + c));
+            if (in && a.residual)
+                r[i] = load_global(reinterpret_cast<const uint4*>(a.residual + (r0 + row0 + 4 * (half + i)) * a.ldr + c));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (a.residual) h[i] = add8(h[i], r[i]);
+            *place(half + i) = h[i];
+            sums[half + i] = squares8(h[i]);
+        }
+    }
     const float mine = butterfly_of(sums);                 // that of row row0 + 4 * (lane / 4)
     cluster_wait();
     if (gseg < nseg) {
@@ -367,22 +392,10 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, SEGS == 2 ? 3 : 1) nor
     const float ss = butterfly_of(v);
     const int my_row = warp + value_of_lane<ROWS_A_WARP>() * WARPS;
     const bool fine = fp32_holds(ss, a.eps);
-    if (first_of_value<ROWS_A_WARP>()) s_norm[my_row] = norm_of(ss, a.inv_cols, a.eps);
-    if (__syncthreads_or(!fine)) {                         // the same in every CTA of the cluster: all have the same sums
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const double s = butterfly(squares8_wide(h[i]));
-            if ((uint32_t)lane < peers && gseg < nseg)
-                asm volatile("st.shared::cluster.f64 [%0], %1;" :: "r"(peer_address(part_wide + (row0 + 4 * i) * PART + gseg, lane)), "d"(s)
-                             : "memory");
-        }
-        cluster_sync();
-        for (int r = warp; r < TILE_ROWS; r += WARPS) {
-            const bool row_fine = fp32_holds(segments_sum(part + r * PART, nseg), a.eps);
-            const double wide = segments_sum(part_wide + r * PART, nseg);
-            if (lane == 0 && !row_fine) s_norm[r] = norm_of_wide(wide, a.cols, a.eps);
-        }
-        __syncthreads();
+    if (first_of_value<ROWS_A_WARP>()) s_norm[my_row] = fine ? norm_of(ss, a.inv_cols, a.eps) : RowNorm{0.0f, 0.0f};
+    if (__syncthreads_or(!fine)) {
+        // the same in every CTA of the cluster, as all have the same sums
+        slow_rows<SEGS>(a, sm_tile, part, s_norm, gseg, nseg, peers);
     }
     const int64_t nct_row = sf_col_tiles(a.cols, 32);
     Pairs w;
@@ -392,15 +405,18 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, SEGS == 2 ? 3 : 1) nor
         const int r = row0 + 4 * i;
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
         if (in) {
+            const uint4 h = *place(i);
+            // (only now: the meeting of the cluster would have waited for earlier stores to reach memory)
+            if (a.sum) *reinterpret_cast<uint4*>(a.sum + (r0 + r) * a.lds + c) = h;
             Pairs f;
-            unpack8(h[i], f);
+            unpack8(h, f);
             normed8(f, s_norm[r]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = f2_mul(f[j], w[j]);
             y = pack8(f);
             if (a.y) *reinterpret_cast<uint4*>(a.y + (r0 + r) * a.ldy + c) = y;
         }
-        *reinterpret_cast<uint4*>(sm_tile + (r * C::COLS + seg * SEG + lane * 8) * 2) = y;
+        *place(i) = y;
         if (a.q_row) quantize_row8(a, r0 + r, c, nct_row, y);
     }
     __syncthreads();
@@ -467,10 +483,11 @@ struct NormBackwardArgs {
 };
 
 constexpr int NB_THREADS = 256;
-constexpr int NB_PARTS = 76;                               // most partial sums of a column: clusters that run at once on 152 SMs
-// CTAs of an SM by the registers and shared memory that NV vectors a thread take, and as many CTAs in a cluster twice over.
+// CTAs of an SM by the registers and shared memory that NV vectors a thread take.
 template <int NV>
-constexpr int NB_PER_SM = NV <= 2 ? 4 : NV == 4 ? 2 : 1;
+constexpr int NB_PER_SM = NV <= 2 ? 3 : NV == 4 ? 2 : 1;
+constexpr int NB_CLUSTER = 2;                              // wider clusters leave SMs idle (four: 72 us where two take 57)
+constexpr int NB_PARTS = 228;                              // most partial sums of a column
 constexpr int NB_STAGES = 2;
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
@@ -512,7 +529,20 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
         return *reinterpret_cast<const uint4*>(sm_rows + stage * stage_bytes + which * tensor + i * vector + threadIdx.x * 16);
     };
     fetch(blockIdx.x, 0);
-    Pairs dw[NV] = {};
+    constexpr bool KEEP_W = NV <= 2;                       // weights in registers
+    Pairs dw[NV] = {}, kept[KEEP_W ? NV : 1];
+    if (KEEP_W)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (c0 + i * step < a.cols) weights8<W32>(a.w, c0 + i * step, kept[i]);
+    auto weights = [&](int i, Pairs& w) {
+        if (KEEP_W) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = kept[KEEP_W ? i : 0][j];
+        } else {
+            weights8<W32>(a.w, c0 + i * step, w);
+        }
+    };
     uint32_t turn = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         fetch(row + gridDim.x, turn ^ 1);                  // into the stage that this thread read in the turn before
@@ -527,7 +557,7 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
             Pairs x, d, w;
             unpack8(h, x);
             unpack8(fetched(turn, 0, i), d);
-            weights8<W32>(a.w, c, w);
+            weights(i, w);
             uint64_t inner = f2_mul(f2_mul(d[0], w[0]), x[0]);
 #pragma unroll
             for (int j = 1; j < 4; ++j) inner = f2_fma(f2_mul(d[j], w[j]), x[j], inner);
@@ -583,7 +613,9 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
             n = norm_of_wide(segments_sum(sm_all[turn][0], nseg), a.cols, a.eps);
             mean = (float)(segments_sum(sm_all[turn][1], nseg) / a.cols * n.p * n.r);
         }
-        const uint64_t minus_mean = f2_pack(-mean, -mean);
+        // with x = h p: dx = p (r dy w - x r^2 mean) + dsum, dw += (r dy) x
+        const float by_x = -__fmul_rn(__fmul_rn(mean, n.r), n.r);
+        const uint64_t rr = f2_pack(n.r, n.r), bx = f2_pack(by_x, by_x);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = c0 + i * step;
@@ -591,14 +623,14 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
             Pairs x, d, w, o;
             unpack8(fetched(turn, 1, i), x);
             unpack8(fetched(turn, 0, i), d);
-            weights8<W32>(a.w, c, w);
-            normed8(x, n);
+            weights(i, w);
+            if (n.p != 1.0f) times8(x, n.p);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                o[j] = f2_fma(x[j], minus_mean, f2_mul(d[j], w[j]));
+                d[j] = f2_mul(d[j], rr);
+                o[j] = f2_fma(x[j], bx, f2_mul(d[j], w[j]));
                 dw[i][j] = f2_fma(d[j], x[j], dw[i][j]);
             }
-            times8(o, n.r);
             if (n.p != 1.0f) times8(o, n.p);
             if (a.dsum) {
                 unpack8(fetched(turn, 2, i), x);
@@ -699,10 +731,9 @@ cudaError_t norm_backward(const NormBackwardArgs& a, int threads, cudaStream_t s
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_STAGES * 3 * NV * NB_THREADS * 16);
     });
     if (e != cudaSuccess) return e;
-    const int cluster = 2 * NB_PER_SM<NV>;
-    const int parts = (int)min64((a.rows + cluster - 1) / cluster, min(NB_PARTS, sms / 2));
-    const cudaError_t e2 = launch_chained(kernel, dim3(parts * cluster), dim3(threads), (size_t)NB_STAGES * (a.dsum ? 3 : 2) * NV * threads * 16,
-                                          cluster, stream, a);
+    const int parts = (int)min64((a.rows + NB_CLUSTER - 1) / NB_CLUSTER, min(NB_PARTS, NB_PER_SM<NV> * sms / NB_CLUSTER));
+    const cudaError_t e2 = launch_chained(kernel, dim3(parts * NB_CLUSTER), dim3(threads),
+                                          (size_t)NB_STAGES * (a.dsum ? 3 : 2) * NV * threads * 16, NB_CLUSTER, stream, a);
     if (e2 != cudaSuccess) return e2;
     return launch_chained(norm_dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(32 * ND_WARPS), 0, 0, stream,
                           static_cast<const float*>(a.partial), parts, a.cols, a.dw);
