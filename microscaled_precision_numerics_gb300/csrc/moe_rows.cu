@@ -15,212 +15,319 @@ namespace mxk {
 namespace {
 
 // ------------------------------------------------------------------------------------------------
-// Sort: a stable counting sort.  The choices are cut into chunks, a CTA each.  A first kernel counts every chunk's choices of
-// each expert; in the second each CTA adds up what the chunks before it hold, and places its own tile by tile: a warp finds
-// the equal experts among its 32 choices by a match and ranks them behind its own count so far.
+// Sort: a stable counting sort.  A warp finds the equal experts among its 32 choices by a match and ranks them behind its own
+// count so far; the warps' counts of an expert are summed in their order, then the CTAs', then the experts'.
+//
+// Up to SORT_CLUSTER_MAX choices one cluster does it all in one launch, the choices in registers and the CTAs' counts exchanged
+// through shared memory: a chain of a few latencies.  Beyond, the choices are cut into chunks, a CTA each: a first kernel counts
+// every chunk's choices of each expert, in the second each CTA adds up what the chunks before it hold.
 // ------------------------------------------------------------------------------------------------
-constexpr int SORT_THREADS = 512, SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_ROUNDS = 8;                             // choices of a thread in a tile
+constexpr int SORT_THREADS = 1024, SORT_WARPS = SORT_THREADS / 32;
+constexpr int SORT_ROUNDS = 8;                             // most choices of a thread at once
+constexpr int SORT_CTAS = 16;                              // most CTAs of the cluster
+constexpr int64_t SORT_CLUSTER_MAX = (int64_t)SORT_CTAS * SORT_THREADS * SORT_ROUNDS;
 constexpr int SORT_TILE = SORT_THREADS * SORT_ROUNDS;
 constexpr int SORT_MAX_CHUNKS = 256;
 
 struct SortArgs {
     const int32_t* ids;
-    int64_t n, chunk;
+    int64_t n, chunk;                                      // choices, choices of a CTA
     int experts, chunks;
     int64_t* offsets;
     int32_t *rows, *source, *counts;
 };
 
+// A choice's expert, -1 where it has none.
+__device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i, int64_t last) {
+    const int id = i < last ? load_global(a.ids + i) : -1;
+    return id >= 0 && id < a.experts ? id : -1;
+}
+
+// Ranks the choices of a warp (ROUNDS times 32 neighbouring ones) among its own of the same expert; `mine` counts them.
+template <int ROUNDS>
+__device__ __forceinline__ void rank_in_warp(const int (&id)[ROUNDS], int (&rank)[ROUNDS], uint16_t* mine) {
+    const unsigned before = (1u << (threadIdx.x & 31)) - 1u;
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const unsigned peers = __match_any_sync(0xFFFFFFFFu, id[r]);
+        const int at = __popc(peers & before), so_far = id[r] >= 0 ? mine[id[r]] : 0;
+        __syncwarp();
+        if (id[r] >= 0 && at == 0) mine[id[r]] = (uint16_t)(so_far + __popc(peers));
+        __syncwarp();
+        rank[r] = so_far + at;
+    }
+}
+
+// The counts of expert g by warp become the counts of the warps before; returns their total.
+__device__ __forceinline__ int sum_over_warps(uint16_t* count, int experts, int g) {
+    int run = 0;
+#pragma unroll 1
+    for (int w0 = 0; w0 < SORT_WARPS; w0 += 8) {           // eight loads side by side
+        int v[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v[w] = count[(w0 + w) * experts + g];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            count[(w0 + w) * experts + g] = (uint16_t)run;
+            run += v[w];
+        }
+    }
+    return run;
+}
+
+// Exclusive sum over the threads of a CTA, and the total.
+__device__ __forceinline__ int sum_before(int v, int* s_warp, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    const unsigned w = (unsigned)s_warp[lane];
+    total = (int)__reduce_add_sync(0xFFFFFFFFu, w);
+    return (int)__reduce_add_sync(0xFFFFFFFFu, lane < warp ? w : 0u) + incl - v;
+}
+
+__device__ __forceinline__ void clear_counts(uint16_t* count, int experts) {
+    for (int i = threadIdx.x; i < SORT_WARPS * experts / 2; i += SORT_THREADS) reinterpret_cast<uint32_t*>(count)[i] = 0u;
+}
+
+template <int ROUNDS>
+__global__ void __launch_bounds__(SORT_THREADS) moe_sort_kernel(const SortArgs a) {
+    extern __shared__ int sm[];
+    int* s_next = sm;                                      // [experts] next row of each expert
+    int* s_total = s_next + a.experts;                     // [CTAs][experts] counts of each CTA
+    __shared__ int s_warp[32];
+    uint32_t me, peers;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(me));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(peers));
+    uint16_t* count = reinterpret_cast<uint16_t*>(s_total + peers * a.experts);       // [warps][experts]
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");             // this CTA runs
+    clear_counts(count, a.experts);
+    chain_begin();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.experts;
+    const int64_t first = me * a.chunk, last = min64(a.n, first + a.chunk), at = first + (warp * ROUNDS) * 32 + lane;
+    int id[ROUNDS], rank[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) id[r] = expert_of(a, at + r * 32, last);
+    __syncthreads();
+    rank_in_warp(id, rank, count + warp * G);
+    __syncthreads();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (tid < G) {
+        const int total = sum_over_warps(count, G, tid);
+        const uint32_t mine = (uint32_t)__cvta_generic_to_shared(s_total + me * G + tid);
+        for (uint32_t p = 0; p < peers; ++p) {
+            uint32_t there;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(p));
+            asm volatile("st.shared::cluster.s32 [%0], %1;" :: "r"(there), "r"(total) : "memory");
+        }
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    int before = 0, total = 0, placed;
+    if (tid < G)
+        for (uint32_t p = 0; p < peers; ++p) {
+            const int v = s_total[p * G + tid];
+            total += v;
+            if (p < me) before += v;
+        }
+    const int start = sum_before(total, s_warp, placed);
+    if (tid < G) {
+        s_next[tid] = start + before;
+        if (me == 0) a.offsets[tid] = start;
+    }
+    if (me == 0 && tid == 0) a.offsets[G] = placed;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        const int64_t i = at + r * 32;
+        if (i >= last) continue;
+        const int row = id[r] >= 0 ? s_next[id[r]] + count[warp * G + id[r]] + rank[r] : -1;
+        a.rows[i] = row;
+        if (a.source && row >= 0) a.source[row] = (int32_t)i;
+    }
+    if (a.source)
+        for (int64_t r = placed + (int64_t)me * SORT_THREADS + tid; r < a.n; r += (int64_t)peers * SORT_THREADS) a.source[r] = -1;
+}
+
 __global__ void __launch_bounds__(SORT_THREADS) moe_count_kernel(const SortArgs a) {
-    extern __shared__ int hist[];
-    for (int g = threadIdx.x; g < a.experts; g += SORT_THREADS) hist[g] = 0;
+    extern __shared__ int sm[];
+    for (int g = threadIdx.x; g < a.experts; g += SORT_THREADS) sm[g] = 0;
     __syncthreads();
     chain_begin();
     const int64_t first = blockIdx.x * a.chunk, last = min64(a.n, first + a.chunk);
     for (int64_t i = first + threadIdx.x; i < last; i += SORT_THREADS) {
-        const int id = load_global(a.ids + i);
-        if (id >= 0 && id < a.experts) atomicAdd(&hist[id], 1);
+        const int id = expert_of(a, i, last);
+        if (id >= 0) atomicAdd(&sm[id], 1);
     }
     __syncthreads();
-    for (int g = threadIdx.x; g < a.experts; g += SORT_THREADS) a.counts[(int64_t)blockIdx.x * a.experts + g] = hist[g];
+    for (int g = threadIdx.x; g < a.experts; g += SORT_THREADS) a.counts[(int64_t)blockIdx.x * a.experts + g] = sm[g];
 }
 
 __global__ void __launch_bounds__(SORT_THREADS) moe_place_kernel(const SortArgs a) {
     extern __shared__ int sm[];
     int* s_next = sm;                                      // [experts] next row of each expert
-    int* s_count = s_next + a.experts;                     // [warps][experts]
-    __shared__ int s_warp[SORT_WARPS];
+    uint16_t* count = reinterpret_cast<uint16_t*>(s_next + a.experts);                // [warps][experts]
+    __shared__ int s_warp[32];
     chain_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.experts;
     const int64_t first = blockIdx.x * a.chunk, last = min64(a.n, first + a.chunk);
-    if (a.chunks == 1) {                                   // no counts: made here
-        for (int g = tid; g < G; g += SORT_THREADS) s_next[g] = 0;
-        __syncthreads();
-        for (int64_t i = first + tid; i < last; i += SORT_THREADS) {
-            const int id = load_global(a.ids + i);
-            if (id >= 0 && id < G) atomicAdd(&s_next[id], 1);
+    int total = 0, before = 0, placed;
+    if (tid < G)
+        for (int c = 0; c < a.chunks; ++c) {
+            const int v = load_global(a.counts + (int64_t)c * G + tid);
+            total += v;
+            if (c < (int)blockIdx.x) before += v;
         }
-        __syncthreads();
-    }
-    // exclusive sum of the experts' totals; a thread owns `per` neighbouring experts (at most two)
-    const int per = (G + SORT_THREADS - 1) / SORT_THREADS;
-    int total[2] = {0, 0}, before[2] = {0, 0}, sum = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int g = tid * per + k;
-        if (k < per && g < G) {
-            if (a.chunks == 1) total[k] = s_next[g];
-            else
-                for (int c = 0; c < a.chunks; ++c) {
-                    const int v = load_global(a.counts + (int64_t)c * G + g);
-                    total[k] += v;
-                    if (c < (int)blockIdx.x) before[k] += v;
-                }
-            sum += total[k];
-        }
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    const int ahead = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)(lane < warp ? s_warp[lane] : 0));
-    const int placed = (int)__reduce_add_sync(0xFFFFFFFFu, (unsigned)(lane < SORT_WARPS ? s_warp[lane] : 0));
-    int run = ahead + incl - sum;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int g = tid * per + k;
-        if (k < per && g < G) {
-            if (blockIdx.x == 0) a.offsets[g] = run;
-            s_next[g] = run + before[k];
-            run += total[k];
-        }
+    const int start = sum_before(total, s_warp, placed);
+    if (tid < G) {
+        s_next[tid] = start + before;
+        if (blockIdx.x == 0) a.offsets[tid] = start;
     }
     if (blockIdx.x == 0 && tid == 0) a.offsets[G] = placed;
     if (a.source)
         for (int64_t r = placed + (int64_t)blockIdx.x * SORT_THREADS + tid; r < a.n; r += (int64_t)gridDim.x * SORT_THREADS) a.source[r] = -1;
-
     for (int64_t tile = first; tile < last; tile += SORT_TILE) {
-        for (int i = tid; i < SORT_WARPS * G; i += SORT_THREADS) s_count[i] = 0;
-        __syncthreads();
-        int* mine = s_count + warp * G;
+        clear_counts(count, G);
+        const int64_t at = tile + (warp * SORT_ROUNDS) * 32 + lane;
         int id[SORT_ROUNDS], rank[SORT_ROUNDS];
 #pragma unroll
-        for (int r = 0; r < SORT_ROUNDS; ++r) {
-            const int64_t i = tile + (warp * SORT_ROUNDS + r) * 32 + lane;
-            id[r] = i < last ? load_global(a.ids + i) : -1;
-            if (id[r] >= G) id[r] = -1;
-            id[r] = max(id[r], -1);
-        }
-#pragma unroll
-        for (int r = 0; r < SORT_ROUNDS; ++r) {
-            const unsigned peers = __match_any_sync(0xFFFFFFFFu, id[r]);
-            const int at = __popc(peers & ((1u << lane) - 1u));
-            const int so_far = id[r] >= 0 ? mine[id[r]] : 0;
-            __syncwarp();
-            if (id[r] >= 0 && at == 0) mine[id[r]] = so_far + __popc(peers);
-            __syncwarp();
-            rank[r] = so_far + at;
-        }
+        for (int r = 0; r < SORT_ROUNDS; ++r) id[r] = expert_of(a, at + r * 32, last);
         __syncthreads();
-        for (int g = tid; g < G; g += SORT_THREADS) {      // counts to first rows of each warp
-            int next = s_next[g];
-            for (int w = 0; w < SORT_WARPS; ++w) {
-                const int v = s_count[w * G + g];
-                s_count[w * G + g] = next;
-                next += v;
-            }
-            s_next[g] = next;
-        }
+        rank_in_warp(id, rank, count + warp * G);
+        __syncthreads();
+        const int here = tid < G ? sum_over_warps(count, G, tid) : 0;
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < SORT_ROUNDS; ++r) {
-            const int64_t i = tile + (warp * SORT_ROUNDS + r) * 32 + lane;
+            const int64_t i = at + r * 32;
             if (i >= last) continue;
-            const int row = id[r] >= 0 ? mine[id[r]] + rank[r] : -1;
+            const int row = id[r] >= 0 ? s_next[id[r]] + count[warp * G + id[r]] + rank[r] : -1;
             a.rows[i] = row;
             if (a.source && row >= 0) a.source[row] = (int32_t)i;
         }
         __syncthreads();
+        if (tid < G) s_next[tid] += here;
     }
 }
 
 // ------------------------------------------------------------------------------------------------
-// Dispatch: a warp takes 1 KB of a token's row (32 bytes a lane in two coalesced halves) to its top_k rows.
+// Dispatch: a warp takes 1 KB of a token's row (32 bytes a lane in two coalesced halves) to its top_k rows.  For rows in few
+// bits the first CTAs of the launch move the scale bytes meanwhile, by words of four scale columns: a warp a token, the groups'
+// tables in shared memory, and zeros between the groups.
 // ------------------------------------------------------------------------------------------------
-constexpr int MOVE_TOKENS = 8;                             // tokens (warps) of a CTA
+constexpr int MOVE_WARPS = 8, MOVE_THREADS = 32 * MOVE_WARPS;
 constexpr int MOVE_BYTES = 1024;
+constexpr int MOVE_SCALE_CTAS = 304;                       // most CTAs for the scales
 
-__global__ void __launch_bounds__(32 * MOVE_TOKENS)
-moe_dispatch_kernel(const uint8_t* x, int64_t pitch, int64_t tokens, int64_t row_bytes, const int32_t* rows, int top_k, uint8_t* y,
-                    int64_t y_pitch, int64_t total_rows) {
-    chain_begin();
-    const int lane = threadIdx.x;
-    const int64_t t = (int64_t)blockIdx.x * MOVE_TOKENS + threadIdx.y;
-    if (t >= tokens) return;
-    const int64_t b0 = (int64_t)blockIdx.y * MOVE_BYTES + lane * 16, b1 = b0 + 512;
-    const int row = lane < top_k ? load_global(rows + t * top_k + lane) : -1;
-    uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
-    if (b0 < row_bytes) v0 = load_global(reinterpret_cast<const uint4*>(x + t * pitch + b0));
-    if (b1 < row_bytes) v1 = load_global(reinterpret_cast<const uint4*>(x + t * pitch + b1));
-    for (int j = 0; j < top_k; ++j) {
-        const int r = __shfl_sync(0xFFFFFFFFu, row, j);
-        if (r < 0 || r >= total_rows) continue;
-        if (b0 < row_bytes) *reinterpret_cast<uint4*>(y + r * y_pitch + b0) = v0;
-        if (b1 < row_bytes) *reinterpret_cast<uint4*>(y + r * y_pitch + b1) = v1;
-    }
-}
-
-struct ScaleArgs {
+struct MoveArgs {
+    const uint8_t* x; int64_t pitch;
+    uint8_t* y; int64_t y_pitch;
+    int64_t tokens, row_bytes, total_rows;
+    const int32_t* rows;
+    int top_k;
+    unsigned groups, scale_ctas;                           // CTAs along the tokens; 0 scale CTAs: rows alone
+    int side;                                              // log2 of the warps side by side on a token
     const uint8_t* s;
     const float* s2;
-    int64_t tokens, columns;                               // scale columns
-    const int32_t* rows;
-    int top_k, G;
+    int64_t columns;                                       // scale columns
+    int G;
     const int64_t* offsets;
     uint8_t* s_out;
     float* s2_out;
-    int64_t total_rows;
 };
 
-// The scale bytes of the dispatched rows, by 4-byte words (four scale columns of a row), a warp a token.
-__global__ void __launch_bounds__(256) moe_dispatch_scales_kernel(const ScaleArgs a) {
+// Zeros the grouped layout's rows behind each group's last and its tiles behind the last group, 512 bytes (128 rows of four scale
+// columns) a warp and step; lane l has the rows l, l + 32, l + 64 and l + 96 of a tile side by side.
+__device__ __forceinline__ void zero_between_groups(uint8_t* s, const int64_t* s_off, const int* s_ptile, int G, int nct,
+                                                    int64_t tile_bound, int64_t me, int64_t warps) {
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = me; i < (int64_t)G * nct; i += warps) {
+        const int g = (int)(i / nct), c = (int)(i - (int64_t)g * nct);
+        const int used = (int)((s_off[g + 1] - s_off[g]) & 127);
+        const int64_t tile = (int64_t)s_ptile[g + 1] - 1;
+        if (used == 0 || tile < 0 || tile >= tile_bound) continue;        // full or empty (offsets out of order: nothing outside)
+        uint32_t* at = reinterpret_cast<uint32_t*>(s + (tile * nct + c) * 512 + lane * 16);
+        if (lane >= used) {
+            *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+                if (lane + 32 * q >= used) at[q] = 0u;
+        }
+    }
+    const int64_t filled = min64(max64(0, (int64_t)s_ptile[G]), tile_bound);
+    uint4* tail = reinterpret_cast<uint4*>(s + filled * nct * 512);
+    for (int64_t i = me * 32 + lane; i < (tile_bound - filled) * nct * 32; i += warps * 32) tail[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+__device__ __forceinline__ void move_scales(const MoveArgs& a) {
     extern __shared__ int64_t s_off[];                     // [G + 1], then the tiles before each group and a scan's scratch
     int* s_ptile = reinterpret_cast<int*>(s_off + a.G + 1);
     int* s_scratch = s_ptile + a.G + 1;
-    chain_begin();
-    for (int i = threadIdx.x; i <= a.G; i += blockDim.x) s_off[i] = load_global(a.offsets + i);
+    for (int i = threadIdx.x; i <= a.G; i += MOVE_THREADS) s_off[i] = load_global(a.offsets + i);
     __syncthreads();
     scan_group_tiles(s_off, a.G, s_ptile, s_scratch);
     const int lane = threadIdx.x & 31;
-    const int64_t me = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), warps = (int64_t)gridDim.x * 8;
+    const int64_t me = (int64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5), warps = (int64_t)a.scale_ctas * MOVE_WARPS;
     const int64_t nct = (a.columns + 3) / 4, tile_bound = (a.total_rows + 127 * (int64_t)a.G + 127) / 128;
     const uint32_t last_mask = (a.columns & 3) ? (1u << (8 * (a.columns & 3))) - 1u : 0xFFFFFFFFu;
+    // `width` lanes (a power of two) a choice, 32 / width choices side by side
+    const int width = nct >= 32 ? 32 : 1 << (32 - __clz((int)nct - 1)), mine = lane & (width - 1), j0 = lane / width, js = 32 / width;
+    auto row_of = [&](int64_t t) { return t < a.tokens && lane < a.top_k ? load_global(a.rows + t * a.top_k + lane) : -1; };
+    auto word_of = [&](int64_t t, int64_t c) {
+        return t < a.tokens && c < nct ? load_global(reinterpret_cast<const uint32_t*>(a.s + sf_offset(t, 4 * c, nct))) : 0u;
+    };
+    int row = row_of(me);
+    uint32_t word = word_of(me, mine);
     for (int64_t t = me; t < a.tokens; t += warps) {
+        const int r = row;
+        uint32_t first = word;
+        row = row_of(t + warps);                           // the next token's, on their way meanwhile
+        word = word_of(t + warps, mine);
         int64_t place = -1;                                // row in the grouped layout of choice `lane`
-        if (lane < a.top_k) {
-            const int r = load_global(a.rows + t * a.top_k + lane);
-            if (r >= 0 && r < a.total_rows) {
-                const int64_t p = grouped_scale_row(s_off, s_ptile, a.G, r);
-                if (p >= 0 && p < tile_bound * 128) place = p;
-                if (a.s2_out) a.s2_out[r] = load_global(a.s2 + t);
-            }
+        if (r >= 0 && r < a.total_rows) {
+            const int64_t p = grouped_scale_row(s_off, s_ptile, a.G, r);
+            if (p >= 0 && p < tile_bound * 128) place = p;
+            if (a.s2_out) a.s2_out[r] = load_global(a.s2 + t);
         }
-        for (int64_t c = lane; c < ((nct + 31) & ~int64_t(31)); c += 32) {
-            uint32_t word = 0u;
-            if (c < nct) word = load_global(reinterpret_cast<const uint32_t*>(a.s + sf_offset(t, 4 * c, nct)));
-            if (c == nct - 1) word &= last_mask;
-            for (int j = 0; j < a.top_k; ++j) {
-                const int64_t p = __shfl_sync(0xFFFFFFFFu, place, j);
-                if (c < nct && p >= 0) *reinterpret_cast<uint32_t*>(a.s_out + sf_offset(p, 4 * c, nct)) = word;
+        for (int64_t c0 = 0; c0 < nct; c0 += width) {
+            const int64_t c = c0 + mine;
+            uint32_t w = c0 == 0 ? first : word_of(t, c);
+            if (c == nct - 1) w &= last_mask;
+            for (int j = 0; j < a.top_k; j += js) {
+                const int64_t p = __shfl_sync(0xFFFFFFFFu, place, min(31, j + j0));
+                if (c < nct && j + j0 < a.top_k && p >= 0) *reinterpret_cast<uint32_t*>(a.s_out + sf_offset(p, 4 * c, nct)) = w;
             }
         }
     }
-    zero_grouped_padding(a.s_out, s_off, s_ptile, a.G, nct, tile_bound, me, warps);
+    zero_between_groups(a.s_out, s_off, s_ptile, a.G, (int)nct, tile_bound, me, warps);
+}
+
+__global__ void __launch_bounds__(MOVE_THREADS) moe_dispatch_kernel(const MoveArgs a) {
+    chain_begin();
+    if (blockIdx.x < a.scale_ctas) {
+        move_scales(a);
+        return;
+    }
+    const unsigned b = blockIdx.x - a.scale_ctas, far = b / a.groups, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int64_t t = (int64_t)(b - far * a.groups) * (MOVE_WARPS >> a.side) + (warp >> a.side);
+    if (t >= a.tokens) return;
+    const int64_t b0 = (((int64_t)far << a.side) + (warp & ((1u << a.side) - 1u))) * MOVE_BYTES + lane * 16, b1 = b0 + 512;
+    const int row = lane < a.top_k ? load_global(a.rows + t * a.top_k + lane) : -1;
+    uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
+    if (b0 < a.row_bytes) v0 = load_global(reinterpret_cast<const uint4*>(a.x + t * a.pitch + b0));
+    if (b1 < a.row_bytes) v1 = load_global(reinterpret_cast<const uint4*>(a.x + t * a.pitch + b1));
+    for (int j = 0; j < a.top_k; ++j) {
+        const int r = __shfl_sync(0xFFFFFFFFu, row, j);
+        if (r < 0 || r >= a.total_rows) continue;
+        if (b0 < a.row_bytes) *reinterpret_cast<uint4*>(a.y + r * a.y_pitch + b0) = v0;
+        if (b1 < a.row_bytes) *reinterpret_cast<uint4*>(a.y + r * a.y_pitch + b1) = v1;
+    }
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -240,14 +347,14 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 constexpr int COMBINE_ROWS = 8;                            // rows fetched side by side
 
-__global__ void __launch_bounds__(32 * MOVE_TOKENS)
+__global__ void __launch_bounds__(32 * MOVE_WARPS)
 moe_combine_kernel(const uint16_t* z, int64_t ldz, int64_t total_rows, int64_t hidden, const int32_t* rows, const float* weights,
-                   int64_t tokens, int top_k, const uint16_t* residual, int64_t ldr, uint16_t* y, int64_t ldy) {
+                   int64_t tokens, int top_k, const uint16_t* residual, int64_t ldr, uint16_t* y, int64_t ldy, int side) {
     chain_begin();
-    const int lane = threadIdx.x;
-    const int64_t t = (int64_t)blockIdx.x * MOVE_TOKENS + threadIdx.y;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * (MOVE_WARPS >> side) + (warp >> side);
     if (t >= tokens) return;
-    const int64_t c = (int64_t)blockIdx.y * 256 + lane * 8;
+    const int64_t c = (((int64_t)blockIdx.y << side) + (warp & ((1 << side) - 1))) * 256 + lane * 8;
     const bool in = c < hidden;
     int row = -1;
     float weight = 0.0f;
@@ -349,66 +456,111 @@ moe_combine_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* z,
     }
 }
 
+// Choices of a chunk: whole tiles, at most SORT_MAX_CHUNKS chunks.
 int64_t sort_chunk(int64_t choices) {
     const int64_t tiles = (choices + SORT_TILE - 1) / SORT_TILE;
     return (tiles + SORT_MAX_CHUNKS - 1) / SORT_MAX_CHUNKS * SORT_TILE;
 }
 
+template <int ROUNDS>
+cudaError_t sort_in_cluster(SortArgs a, cudaStream_t stream) {
+    auto kernel = moe_sort_kernel<ROUNDS>;
+    static PerDevice pd;
+    int unused = 0;
+    const cudaError_t e = per_device_once(pd, unused, [kernel](int&) {
+        const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (1 + SORT_CTAS + SORT_WARPS / 2) * MX_MAX_GROUPS * (int)sizeof(int));
+        return s != cudaSuccess ? s : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    });
+    if (e != cudaSuccess) return e;
+    a.chunk = ROUNDS * SORT_THREADS;
+    const unsigned ctas = (unsigned)((a.n + a.chunk - 1) / a.chunk);
+    return launch_chained(kernel, dim3(ctas), dim3(SORT_THREADS), (size_t)(1 + ctas + SORT_WARPS / 2) * a.experts * sizeof(int), ctas, stream, a);
+}
+
 }  // namespace
 
 size_t moe_sort_workspace_bytes(int64_t choices, int64_t experts) {
+    if (choices <= SORT_CLUSTER_MAX) return 16;
     const int64_t chunk = sort_chunk(choices);
     return (size_t)((choices + chunk - 1) / chunk) * (size_t)experts * sizeof(int32_t);
 }
 
 cudaError_t launch_moe_sort(const int32_t* ids, int64_t choices, int experts, int64_t* offsets, int32_t* rows, int32_t* source,
                             void* workspace, cudaStream_t stream) {
+    SortArgs a{ids, choices, 0, experts, 0, offsets, rows, source, static_cast<int32_t*>(workspace)};
+    // as few choices a thread as the cluster allows: each is a step of the chain
+    if (choices <= SORT_CLUSTER_MAX / 8) return sort_in_cluster<1>(a, stream);
+    if (choices <= SORT_CLUSTER_MAX / 4) return sort_in_cluster<2>(a, stream);
+    if (choices <= SORT_CLUSTER_MAX / 2) return sort_in_cluster<4>(a, stream);
+    if (choices <= SORT_CLUSTER_MAX) return sort_in_cluster<8>(a, stream);
     static PerDevice pd;
     int unused = 0;
     cudaError_t e = per_device_once(pd, unused, [](int&) {
         return cudaFuncSetAttribute(moe_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (SORT_WARPS + 1) * MX_MAX_GROUPS * (int)sizeof(int));
+                                    (1 + SORT_WARPS / 2) * MX_MAX_GROUPS * (int)sizeof(int));
     });
     if (e != cudaSuccess) return e;
-    SortArgs a{ids, choices, sort_chunk(choices), experts, 0, offsets, rows, source, static_cast<int32_t*>(workspace)};
+    a.chunk = sort_chunk(choices);
     a.chunks = (int)((choices + a.chunk - 1) / a.chunk);
-    if (a.chunks > 1) {
-        e = launch_chained(moe_count_kernel, dim3(a.chunks), dim3(SORT_THREADS), (size_t)experts * sizeof(int), 0, stream, a);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_chained(moe_place_kernel, dim3(a.chunks), dim3(SORT_THREADS), (size_t)(SORT_WARPS + 1) * experts * sizeof(int), 0, stream, a);
+    e = launch_chained(moe_count_kernel, dim3(a.chunks), dim3(SORT_THREADS), (size_t)experts * sizeof(int), 0, stream, a);
+    if (e != cudaSuccess) return e;
+    return launch_chained(moe_place_kernel, dim3(a.chunks), dim3(SORT_THREADS), (size_t)(1 + SORT_WARPS / 2) * experts * sizeof(int), 0, stream, a);
 }
 
-static cudaError_t dispatch_bytes(const uint8_t* x, int64_t pitch, int64_t tokens, int64_t row_bytes, const int32_t* rows, int top_k,
-                                  uint8_t* y, int64_t y_pitch, int64_t total_rows, cudaStream_t stream) {
-    const dim3 grid((unsigned)((tokens + MOVE_TOKENS - 1) / MOVE_TOKENS), (unsigned)((row_bytes + MOVE_BYTES - 1) / MOVE_BYTES));
-    return launch_chained(moe_dispatch_kernel, grid, dim3(32, MOVE_TOKENS), 0, 0, stream, x, pitch, tokens, row_bytes, rows, top_k, y,
-                          y_pitch, total_rows);
+// Warps of a CTA side by side on a token of `pieces` pieces, as a power of two: the pieces of a row are on their way together,
+// which keeps memory pages open.
+static int warps_side_by_side(int64_t pieces) {
+    int side = 0;
+    while (side < 3 && (2 << side) <= pieces) ++side;
+    static_assert(MOVE_WARPS == 8, "eight warps at most");
+    return side;
+}
+
+static cudaError_t move_rows(MoveArgs a, cudaStream_t stream) {
+    const int64_t pieces = (a.row_bytes + MOVE_BYTES - 1) / MOVE_BYTES;
+    a.side = warps_side_by_side(pieces);
+    const int64_t tokens_a_cta = MOVE_WARPS >> a.side, groups = (a.tokens + tokens_a_cta - 1) / tokens_a_cta;
+    a.groups = (unsigned)groups;
+    const int64_t ctas = a.scale_ctas + groups * ((pieces + (1 << a.side) - 1) >> a.side);
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    return launch_chained(moe_dispatch_kernel, dim3((unsigned)ctas), dim3(MOVE_THREADS), a.scale_ctas ? (size_t)12 * (a.G + 1) + 128 : 0, 0,
+                          stream, a);
 }
 
 cudaError_t launch_moe_dispatch(const uint16_t* x, int64_t ldx, int64_t tokens, int64_t hidden, const int32_t* rows, int top_k,
                                 uint16_t* y, int64_t ldy, int64_t total_rows, cudaStream_t stream) {
-    return dispatch_bytes(reinterpret_cast<const uint8_t*>(x), 2 * ldx, tokens, 2 * hidden, rows, top_k, reinterpret_cast<uint8_t*>(y),
-                          2 * ldy, total_rows, stream);
+    MoveArgs a{};
+    a.x = reinterpret_cast<const uint8_t*>(x); a.pitch = 2 * ldx;
+    a.y = reinterpret_cast<uint8_t*>(y); a.y_pitch = 2 * ldy;
+    a.tokens = tokens; a.row_bytes = 2 * hidden; a.total_rows = total_rows;
+    a.rows = rows; a.top_k = top_k;
+    return move_rows(a, stream);
 }
 
 cudaError_t launch_moe_dispatch_quantized(bool fp4, const uint8_t* q, const uint8_t* s, const float* s2, int64_t tokens, int64_t hidden,
                                           const int32_t* rows, int top_k, int G, const int64_t* offsets, uint8_t* q_out, uint8_t* s_out,
                                           float* s2_out, int64_t total_rows, cudaStream_t stream) {
-    const int64_t bytes = fp4 ? hidden / 2 : hidden;
-    const cudaError_t e = dispatch_bytes(q, bytes, tokens, bytes, rows, top_k, q_out, bytes, total_rows, stream);
-    if (e != cudaSuccess) return e;
-    const ScaleArgs a{s, s2, tokens, hidden / (fp4 ? 16 : 32), rows, top_k, G, offsets, s_out, s2_out, total_rows};
-    const unsigned grid = (unsigned)min64((tokens + 7) / 8, 2 * device_sm_count());
-    return launch_chained(moe_dispatch_scales_kernel, dim3(grid), dim3(256), (size_t)12 * (G + 1) + 128, 0, stream, a);
+    MoveArgs a{};
+    a.x = q; a.y = q_out;
+    a.pitch = a.y_pitch = a.row_bytes = fp4 ? hidden / 2 : hidden;
+    a.tokens = tokens; a.total_rows = total_rows;
+    a.rows = rows; a.top_k = top_k;
+    a.s = s; a.s2 = s2; a.columns = hidden / (fp4 ? 16 : 32);
+    a.G = G; a.offsets = offsets; a.s_out = s_out; a.s2_out = s2_out;
+    // a warp a token and a group, up to two CTAs an SM
+    a.scale_ctas = (unsigned)min64(MOVE_SCALE_CTAS, (max64(tokens, G) + MOVE_WARPS - 1) / MOVE_WARPS);
+    return move_rows(a, stream);
 }
 
 cudaError_t launch_moe_combine(const uint16_t* z, int64_t ldz, int64_t total_rows, int64_t hidden, const int32_t* rows,
                                const float* weights, int64_t tokens, int top_k, const uint16_t* residual, int64_t ldr, uint16_t* y,
                                int64_t ldy, cudaStream_t stream) {
-    const dim3 grid((unsigned)((tokens + MOVE_TOKENS - 1) / MOVE_TOKENS), (unsigned)((hidden + 255) / 256));
-    return launch_chained(moe_combine_kernel, grid, dim3(32, MOVE_TOKENS), 0, 0, stream, z, ldz, total_rows, hidden, rows, weights, tokens,
-                          top_k, residual, ldr, y, ldy);
+    const int64_t pieces = (hidden + 255) / 256;
+    const int side = warps_side_by_side(pieces), tokens_a_cta = MOVE_WARPS >> side;
+    const dim3 grid((unsigned)((tokens + tokens_a_cta - 1) / tokens_a_cta), (unsigned)((pieces + (1 << side) - 1) >> side));
+    return launch_chained(moe_combine_kernel, grid, dim3(MOVE_THREADS), 0, 0, stream, z, ldz, total_rows, hidden, rows, weights, tokens, top_k,
+                          residual, ldr, y, ldy, side);
 }
 
 cudaError_t launch_moe_combine_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int64_t total_rows,

@@ -348,7 +348,7 @@ def run_sort(mx, ids, experts, source=True):
 
 
 SORT_SIZES = [(1, 1, 1), (1, 8, 128), (3, 2, 5), (61, 8, 128), (513, 8, 16), (4096, 1, 7), (4097, 1, 1024), (700, 6, 60), (8192, 8, 128),
-              (5000, 32, 1024), (2049, 2, 33), (150000, 8, 64)]
+              (5000, 32, 1024), (2049, 2, 33), (16385, 8, 40), (150000, 8, 64), (40000, 4, 1024)]
 
 
 @pytest.mark.parametrize("tokens,k,experts", SORT_SIZES)
