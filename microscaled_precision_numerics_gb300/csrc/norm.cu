@@ -182,21 +182,26 @@ struct NormArgs {
     uint8_t *q_row, *s_row, *q_col, *s_col;
 };
 
-// The codes of eight neighbouring elements of a row as the four lanes of a 32-block hold them (zeros beyond the row's end), and
-// the block's scale byte.  All lanes of the warp call it.
-__device__ __forceinline__ void quantize_row8(const NormArgs& a, int64_t row, int c, int64_t nct, const uint4& y) {
+// The codes of eight neighbouring elements of a row, to q, and the scale byte of the 32-block that four lanes hold, from the first
+// of them to s.  in: the elements lie inside the row; scaled: the block lies inside the scale layout, whose padding is zero.  All
+// lanes of the warp call it, with zeros where there are no elements.
+__device__ __forceinline__ void quantize_row8(const uint4& y, uint8_t* q, uint8_t* s, bool in, bool scaled) {
     uint32_t m = absmax_bf16x2(absmax_bf16x2(y.x, y.y), absmax_bf16x2(y.z, y.w));
     m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const uint32_t s = e8m0_from_amax_bits(fold_halves(m));
-    if (c < a.cols) {
-        Pairs f;
-        unpack8(y, f);
-        times8(f, inv_scale_from_e8m0(s));
-        *reinterpret_cast<uint2*>(a.q_row + row * a.cols + c) = make_uint2(cvt_e4m3_pairs(f[0], f[1]), cvt_e4m3_pairs(f[2], f[3]));
-    }
-    if ((c & 31) == 0 && (c >> 5) < 4 * nct) a.s_row[sf_offset(row, c >> 5, nct)] = c < a.cols ? (uint8_t)s : (uint8_t)0;
+    const uint32_t byte = e8m0_from_amax_bits(fold_halves(m));            // 0 for a block of zeros
+    Pairs f;
+    unpack8(y, f);
+    times8(f, inv_scale_from_e8m0(byte));
+    const uint2 codes = make_uint2(cvt_e4m3_pairs(f[0], f[1]), cvt_e4m3_pairs(f[2], f[3]));
+    if (in) *reinterpret_cast<uint2*>(q) = codes;
+    if (scaled) *s = (uint8_t)byte;
 }
+// Offset of (row, 32-block of column c) in the row-wise scale layout, split into the row's and the column's part.
+__device__ __forceinline__ int64_t scale_row_offset(int64_t row, int64_t nct) {
+    return ((row >> 7) * nct << 9) + ((row & 31) << 4) + ((row >> 5 & 3) << 2);
+}
+__device__ __forceinline__ int scale_col_offset(int c) { return (c >> 7 << 9) + (c >> 5 & 3); }
 
 // Without column-wise codes: one row a group of blockDim.x threads, blockDim.y rows a CTA; NV vectors of eight elements a thread.
 // At most four a thread and 64 registers: with eight, one CTA an SM ran through 32 KB of straight-line code for every row
@@ -219,22 +224,25 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + ty;
     if (row >= a.rows) return;
     const int c0 = (warp * 32 + lane) * 8, step = warps * SEG;
+    const uint16_t* x = a.x + row * a.ldx;
     uint4 h[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         h[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (c0 + i * step < a.cols) h[i] = load_global(reinterpret_cast<const uint4*>(a.x + row * a.ldx + c0 + i * step));
+        if (c0 + i * step < a.cols) h[i] = load_global(reinterpret_cast<const uint4*>(x + c0 + i * step));
     }
     if (a.residual) {
+        const uint16_t* residual = a.residual + row * a.ldr;
+        uint16_t* sum = a.sum + row * a.lds;
         uint4 r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (c0 + i * step < a.cols) r[i] = load_global(reinterpret_cast<const uint4*>(a.residual + row * a.ldr + c0 + i * step));
+            if (c0 + i * step < a.cols) r[i] = load_global(reinterpret_cast<const uint4*>(residual + c0 + i * step));
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (c0 + i * step < a.cols) {
                 h[i] = add8(h[i], r[i]);
-                if (a.sum) *reinterpret_cast<uint4*>(a.sum + row * a.lds + c0 + i * step) = h[i];
+                if (a.sum) *reinterpret_cast<uint4*>(sum + c0 + i * step) = h[i];
             }
     }
     float part[NV];
@@ -257,6 +265,8 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
         row_sync(ty, blockDim.x);
         n = norm_of_wide(segments_sum(sm_all[ty], nseg), a.cols, a.eps);
     }
+    uint16_t* to_y = a.y + row * a.ldy;
+    uint8_t *q = a.q_row + row * a.cols, *s = a.s_row + scale_row_offset(row, nct);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = c0 + i * step;
@@ -269,9 +279,9 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = f2_mul(f[j], w[j]);
             y = pack8(f);
-            if (a.y) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = y;
+            if (a.y) *reinterpret_cast<uint4*>(to_y + c) = y;
         }
-        if (a.q_row) quantize_row8(a, row, c, nct, y);
+        if (a.q_row) quantize_row8(y, q + c, s + scale_col_offset(c), c < a.cols, (c & 31) == 0 && c < 128 * nct);
     }
 }
 
@@ -355,6 +365,7 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
     // item i of a warp: row warp / SEGS + 4 i, segment warp % SEGS of the CTA
     const int seg = warp % SEGS, c = c_cta + seg * SEG + lane * 8, gseg = (int)rank * SEGS + seg, row0 = warp / SEGS;
     const bool in = c < a.cols;
+    const uint16_t *x = a.x + (r0 + row0) * a.ldx + c, *residual = a.residual + (r0 + row0) * a.ldr + c;
     auto place = [&](int i) { return reinterpret_cast<uint4*>(sm_tile + ((row0 + 4 * i) * C::COLS + seg * SEG + lane * 8) * 2); };
     float sums[ITEMS];
 #pragma unroll
@@ -363,9 +374,10 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             h[i] = r[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (in) h[i] = load_global(reinterpret_cast<const uint4*>(a.x + (r0 + row0 + 4 * (half + i)) * a.ldx + c));
-            if (in && a.residual)
-                r[i] = load_global(reinterpret_cast<const uint4*>(a.residual + (r0 + row0 + 4 * (half + i)) * a.ldr + c));
+            if (in) h[i] = load_global(reinterpret_cast<const uint4*>(x));
+            if (in && a.residual) r[i] = load_global(reinterpret_cast<const uint4*>(residual));
+            x += 4 * a.ldx;
+            residual += 4 * a.ldr;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -398,6 +410,9 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
         slow_rows<SEGS>(a, sm_tile, part, s_norm, gseg, nseg, peers);
     }
     const int64_t nct_row = sf_col_tiles(a.cols, 32);
+    const bool scaled = (c & 31) == 0 && c < 128 * nct_row;
+    uint16_t *to_sum = a.sum + (r0 + row0) * a.lds + c, *to_y = a.y + (r0 + row0) * a.ldy + c;
+    uint8_t *to_q = a.q_row + (r0 + row0) * a.cols + c, *to_s = a.s_row + scale_row_offset(r0 + row0, nct_row) + scale_col_offset(c);
     Pairs w;
     if (in) weights8<W32>(a.w, c, w);
 #pragma unroll
@@ -407,17 +422,20 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
         if (in) {
             const uint4 h = *place(i);
             // (only now: the meeting of the cluster would have waited for earlier stores to reach memory)
-            if (a.sum) *reinterpret_cast<uint4*>(a.sum + (r0 + r) * a.lds + c) = h;
+            if (a.sum) *reinterpret_cast<uint4*>(to_sum) = h;
             Pairs f;
             unpack8(h, f);
             normed8(f, s_norm[r]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[j] = f2_mul(f[j], w[j]);
             y = pack8(f);
-            if (a.y) *reinterpret_cast<uint4*>(a.y + (r0 + r) * a.ldy + c) = y;
+            if (a.y) *reinterpret_cast<uint4*>(to_y) = y;
         }
         *place(i) = y;
-        if (a.q_row) quantize_row8(a, r0 + r, c, nct_row, y);
+        if (a.q_row) quantize_row8(y, to_q, to_s + 64 * i, in, scaled);   // four rows on: 64 bytes of the tile
+        to_sum += 4 * a.lds;
+        to_y += 4 * a.ldy;
+        to_q += 4 * (int64_t)a.cols;
     }
     __syncthreads();
     if (a.q_row && r0 + TILE_ROWS == a.rows) {             // scale rows up to a whole tile: zeros, this CTA's columns
@@ -457,7 +475,8 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
                 f[i] = j ? f2_pack(bf16_hi(t[k][2 * i]), bf16_hi(t[k][2 * i + 1])) : f2_pack(bf16_lo(t[k][2 * i]), bf16_lo(t[k][2 * i + 1]));
             times8(f, inv);
             if (gin)
-                *reinterpret_cast<uint2*>(q_col + (int64_t)(2 * k + j) * a.rows) = make_uint2(cvt_e4m3_pairs(f[0], f[1]), cvt_e4m3_pairs(f[2], f[3]));
+                *reinterpret_cast<uint2*>(q_col) = make_uint2(cvt_e4m3_pairs(f[0], f[1]), cvt_e4m3_pairs(f[2], f[3]));
+            q_col += a.rows;
             if (q == 0) s_col[(2 * k + j) * 16] = gin ? (uint8_t)s : (uint8_t)0;
         }
     }
@@ -511,17 +530,21 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
     const uint32_t vector = blockDim.x * 16, tensor = NV * vector, stage_bytes = tensors * tensor;
     const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm_rows) + threadIdx.x * 16;
     const int c0 = (warp * 32 + lane) * 8, step = warps * SEG;
-    auto fetch = [&](int64_t row, uint32_t stage) {
+    const uint16_t *dy = a.dy + blockIdx.x * a.lddy + c0, *from_h = a.h + blockIdx.x * a.ldh + c0, *dsum = a.dsum + blockIdx.x * a.ldds + c0;
+    uint16_t* dx = a.dx + blockIdx.x * a.lddx + c0;
+    auto fetch = [&](int64_t row, uint32_t stage) {        // rows in turn
         if (row < a.rows) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = c0 + i * step;
-                if (c >= a.cols) continue;
+                if (c0 + i * step >= a.cols) continue;
                 const uint32_t at = sm0 + stage * stage_bytes + i * vector;
-                copy16(at, a.dy + row * a.lddy + c);
-                copy16(at + tensor, a.h + row * a.ldh + c);
-                if (a.dsum) copy16(at + 2 * tensor, a.dsum + row * a.ldds + c);
+                copy16(at, dy + i * step);
+                copy16(at + tensor, from_h + i * step);
+                if (a.dsum) copy16(at + 2 * tensor, dsum + i * step);
             }
+            dy += gridDim.x * a.lddy;
+            from_h += gridDim.x * a.ldh;
+            dsum += gridDim.x * a.ldds;
         }
         copies_commit();                                   // an empty group where there is no row, so that the count goes on
     };
@@ -575,7 +598,8 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
             v[0] += sm_s[lane + 32];
             v[1] += sm_c[lane + 32];
         }
-        const float ss = butterfly(v[0]), cc = butterfly(v[1]);
+        const float both = butterfly_of(v);                              // of the first in the lower half of the warp
+        const float ss = __shfl_sync(0xFFFFFFFFu, both, 0), cc = __shfl_sync(0xFFFFFFFFu, both, 16);
         RowNorm n = norm_of(ss, a.inv_cols, a.eps);
         float mean = __fmul_rn(__fmul_rn(cc, a.inv_cols), n.r);          // mean(dn n)
         // the products dn h likewise: too large, or so small that subnormals would decide (where eps does not)
@@ -637,8 +661,9 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
 #pragma unroll
                 for (int j = 0; j < 4; ++j) o[j] = f2_add(o[j], x[j]);
             }
-            *reinterpret_cast<uint4*>(a.dx + row * a.lddx + c) = pack8(o);
+            *reinterpret_cast<uint4*>(dx + i * step) = pack8(o);
         }
+        dx += gridDim.x * a.lddx;
     }
     // the cluster's sums: each CTA's in its shared memory (the ring is free: 8 bytes a column and more), a share of the columns each
     float* sm_dw = reinterpret_cast<float*>(sm_rows);
