@@ -43,13 +43,24 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i, int64_t l
     return id >= 0 && id < a.experts ? id : -1;
 }
 
-// Ranks the choices of a warp (ROUNDS times 32 neighbouring ones) among its own of the same expert; `mine` counts them.
+// Ranks the choices of a warp (ROUNDS times 32 neighbouring ones) among its own of the same expert; `mine` counts them.  The lanes
+// of the same expert are those whose numbers agree in every bit, by a vote a bit (65536 choices of 128 experts: 8.1 us, and
+// 9.9 with __match_any_sync).
 template <int ROUNDS>
-__device__ __forceinline__ void rank_in_warp(const int (&id)[ROUNDS], int (&rank)[ROUNDS], uint16_t* mine) {
+__device__ __forceinline__ void rank_in_warp(const int (&id)[ROUNDS], int (&rank)[ROUNDS], uint16_t* mine, int experts) {
     const unsigned before = (1u << (threadIdx.x & 31)) - 1u;
+    unsigned same[ROUNDS];
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) same[r] = __ballot_sync(0xFFFFFFFFu, id[r] >= 0);
+    for (int bit = 1; bit < experts; bit <<= 1)
+#pragma unroll
+        for (int r = 0; r < ROUNDS; ++r) {
+            const unsigned set = __ballot_sync(0xFFFFFFFFu, (id[r] & bit) != 0);
+            same[r] &= (id[r] & bit) ? set : ~set;
+        }
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
-        const unsigned peers = __match_any_sync(0xFFFFFFFFu, id[r]);
+        const unsigned peers = same[r];                    // (of a choice without an expert: not used)
         const int at = __popc(peers & before), so_far = id[r] >= 0 ? mine[id[r]] : 0;
         __syncwarp();
         if (id[r] >= 0 && at == 0) mine[id[r]] = (uint16_t)(so_far + __popc(peers));
@@ -114,7 +125,7 @@ __global__ void __launch_bounds__(SORT_THREADS) moe_sort_kernel(const SortArgs a
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) id[r] = expert_of(a, at + r * 32, last);
     __syncthreads();
-    rank_in_warp(id, rank, count + warp * G);
+    rank_in_warp(id, rank, count + warp * G, G);
     __syncthreads();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (tid < G) {
@@ -197,7 +208,7 @@ __global__ void __launch_bounds__(SORT_THREADS) moe_place_kernel(const SortArgs 
 #pragma unroll
         for (int r = 0; r < SORT_ROUNDS; ++r) id[r] = expert_of(a, at + r * 32, last);
         __syncthreads();
-        rank_in_warp(id, rank, count + warp * G);
+        rank_in_warp(id, rank, count + warp * G, G);
         __syncthreads();
         const int here = tid < G ? sum_over_warps(count, G, tid) : 0;
         __syncthreads();
@@ -221,7 +232,8 @@ __global__ void __launch_bounds__(SORT_THREADS) moe_place_kernel(const SortArgs 
 // ------------------------------------------------------------------------------------------------
 constexpr int MOVE_WARPS = 8, MOVE_THREADS = 32 * MOVE_WARPS;
 constexpr int MOVE_BYTES = 1024;
-constexpr int MOVE_SCALE_CTAS = 304;                       // most CTAs for the scales
+// Most CTAs for the scales (8192 tokens: 33 us with 152, 27 with 304 to 1024; the rows alone take 22).
+constexpr int MOVE_SCALE_CTAS = 304;
 
 struct MoveArgs {
     const uint8_t* x; int64_t pitch;
@@ -245,8 +257,8 @@ struct MoveArgs {
 __device__ __forceinline__ void zero_between_groups(uint8_t* s, const int64_t* s_off, const int* s_ptile, int G, int nct,
                                                     int64_t tile_bound, int64_t me, int64_t warps) {
     const int lane = threadIdx.x & 31;
-    for (int64_t i = me; i < (int64_t)G * nct; i += warps) {
-        const int g = (int)(i / nct), c = (int)(i - (int64_t)g * nct);
+    for (int i = (int)me; i < G * nct; i += (int)warps) {
+        const int g = i / nct, c = i - g * nct;
         const int used = (int)((s_off[g + 1] - s_off[g]) & 127);
         const int64_t tile = (int64_t)s_ptile[g + 1] - 1;
         if (used == 0 || tile < 0 || tile >= tile_bound) continue;        // full or empty (offsets out of order: nothing outside)
@@ -268,9 +280,6 @@ __device__ __forceinline__ void move_scales(const MoveArgs& a) {
     extern __shared__ int64_t s_off[];                     // [G + 1], then the tiles before each group and a scan's scratch
     int* s_ptile = reinterpret_cast<int*>(s_off + a.G + 1);
     int* s_scratch = s_ptile + a.G + 1;
-    for (int i = threadIdx.x; i <= a.G; i += MOVE_THREADS) s_off[i] = load_global(a.offsets + i);
-    __syncthreads();
-    scan_group_tiles(s_off, a.G, s_ptile, s_scratch);
     const int lane = threadIdx.x & 31;
     const int64_t me = (int64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5), warps = (int64_t)a.scale_ctas * MOVE_WARPS;
     const int64_t nct = (a.columns + 3) / 4, tile_bound = (a.total_rows + 127 * (int64_t)a.G + 127) / 128;
@@ -281,8 +290,11 @@ __device__ __forceinline__ void move_scales(const MoveArgs& a) {
     auto word_of = [&](int64_t t, int64_t c) {
         return t < a.tokens && c < nct ? load_global(reinterpret_cast<const uint32_t*>(a.s + sf_offset(t, 4 * c, nct))) : 0u;
     };
-    int row = row_of(me);
+    int row = row_of(me);                                  // on their way while the tables are made
     uint32_t word = word_of(me, mine);
+    for (int i = threadIdx.x; i <= a.G; i += MOVE_THREADS) s_off[i] = load_global(a.offsets + i);
+    __syncthreads();
+    scan_group_tiles(s_off, a.G, s_ptile, s_scratch);
     for (int64_t t = me; t < a.tokens; t += warps) {
         const int r = row;
         uint32_t first = word;
@@ -548,8 +560,9 @@ cudaError_t launch_moe_dispatch_quantized(bool fp4, const uint8_t* q, const uint
     a.rows = rows; a.top_k = top_k;
     a.s = s; a.s2 = s2; a.columns = hidden / (fp4 ? 16 : 32);
     a.G = G; a.offsets = offsets; a.s_out = s_out; a.s2_out = s2_out;
-    // a warp a token and a group, up to two CTAs an SM
-    a.scale_ctas = (unsigned)min64(MOVE_SCALE_CTAS, (max64(tokens, G) + MOVE_WARPS - 1) / MOVE_WARPS);
+    // a warp a token and four of the pieces between groups, up to two CTAs an SM
+    const int64_t pieces = (int64_t)G * ((a.columns + 3) / 4);
+    a.scale_ctas = (unsigned)min64(MOVE_SCALE_CTAS, (max64(tokens, pieces / 4) + MOVE_WARPS - 1) / MOVE_WARPS);
     return move_rows(a, stream);
 }
 
