@@ -4,6 +4,7 @@
  * sorted by expert for the grouped products and back, and the gradients.  The conventions of mxnum.h hold for every entry
  * point (device pointers, caller-owned buffers, host-side checks, asynchronous launches on the caller's stream).  BF16
  * tensors, codes, scales, group offsets and workspaces must be 16-byte aligned, 32-bit arrays 4-byte aligned.
+ * Calls that may overlap on the GPU (other streams, other captured graphs) need workspaces of their own.
  * The kernels of these calls may be set up while the one before in the stream still runs; each waits for the earlier work
  * before it touches memory, so the order of a stream holds as ever.
  *
@@ -37,7 +38,7 @@ typedef enum { MX_DTYPE_BF16 = 0, MX_DTYPE_FP32 = 1 } mx_dtype;
  *   y        [rows, ldy] BF16 (NULL: not written)
  *   q_row, s_row, q_col, s_col as in mx_quantize_mxfp8 (NULL: skip)
  * At least one of y, q_row and q_col.  No other two buffers may overlap.  Requires cols % 8 == 0, for row-wise codes cols % 32
- * == 0, for column-wise ones rows % 32 == 0; cols <= MX_RMSNORM_MAX_COLS; eps >= 0 and finite.  A row's values do not
+ * == 0, for column-wise ones rows % 32 == 0; cols <= MX_RMSNORM_MAX_COLS; eps >= 0 and finite; weights below 2^60.  A row's values do not
  * depend on the other rows, their number or which outputs are asked for.  Rows whose squares leave FP32's range are summed in
  * FP64.  A NaN makes its row NaN; an infinity too where it stands, and zeros elsewhere. */
 mx_status mx_rmsnorm_mxfp8(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
@@ -61,7 +62,7 @@ mx_status mx_rmsnorm_backward(const void* dy, int64_t lddy, const void* h, int64
 
 /* The experts of each token: the top_k largest logits, largest first, of equal ones the lowest index first.
  *   weights = softmax over the chosen logits (normalize = 1) or the chosen entries of the softmax over all (0)
- *   logits [tokens, ldl], BF16 or FP32 by logits_type;  ids [tokens, top_k] int32, weights [tokens, top_k] FP32
+ *   logits [tokens, ldl], BF16 or FP32 by logits_type, 4-byte aligned;  ids [tokens, top_k] int32, weights [tokens, top_k] FP32
  * A logit of -inf is never chosen: where fewer than top_k are left the others' ids are -1 and their weights zero.  A NaN counts
  * as the largest and makes the row's weights NaN, as +inf does.  experts <= MX_MAX_GROUPS, top_k <= experts and
  * <= MX_MOE_MAX_TOP_K. */

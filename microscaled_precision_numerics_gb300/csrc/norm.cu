@@ -649,6 +649,11 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
             n = norm_of_wide(segments_sum(sm_all[turn][0], nseg), a.cols, a.eps);
             mean = (float)(segments_sum(sm_all[turn][1], nseg) / a.cols * n.p * n.r);
         }
+        // a factor far from 1 is split as a slow row's is, so that dy r keeps its bits where dy n has them
+        if (n.r < 9.53674316e-7f || n.r > 1048576.0f) {                  // 2^-20, 2^20; neither for a slow row
+            n.p = __uint_as_float(__float_as_uint(n.r) & 0x7F800000u);
+            n.r = __uint_as_float((__float_as_uint(n.r) & 0x007FFFFFu) | 0x3F800000u);
+        }
         // with x = h p: dx = p (r dy w - x r^2 mean) + dsum, dw += (r dy) x
         const float by_x = -__fmul_rn(__fmul_rn(mean, n.r), n.r);
 #pragma unroll
