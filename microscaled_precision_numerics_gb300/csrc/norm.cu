@@ -211,9 +211,11 @@ __device__ __forceinline__ int scale_col_offset(int c) { return (c >> 7 << 9) + 
 
 // Without column-wise codes: one row a group of blockDim.x threads, blockDim.y rows a CTA; NV vectors of eight elements a thread.
 // At most four a thread and 64 registers: with eight, one CTA an SM ran through 32 KB of straight-line code for every row
-// (1003 x 14336 took 54 us).
+// (1003 x 14336 took 54 us, now 17: three turns of two CTAs an SM, each a row's loads, meeting and stores after one another).
+// FULL: the threads' vectors are the row exactly, no comparisons (8192 x 4096 to codes 29.8 to 27.3 us).  With residual, sum and codes
+// 8192 x 4096 takes 36 us, 97 % of the measured copy rate.
 constexpr int NR_THREADS = 512;
-template <int NV, bool W32>
+template <int NV, bool W32, bool FULL>
 __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs a) {
     __shared__ double sm_all[8][MAX_SEGS];
     chain_begin();
@@ -230,12 +232,13 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + ty;
     if (row >= a.rows) return;
     const int c0 = (warp * 32 + lane) * 8, step = warps * SEG;
+    auto inside = [&](int i) { return FULL || c0 + i * step < a.cols; };
     const uint16_t* x = a.x + row * a.ldx;
     uint4 h[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         h[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (c0 + i * step < a.cols) h[i] = load_global(reinterpret_cast<const uint4*>(x + c0 + i * step));
+        if (inside(i)) h[i] = load_global(reinterpret_cast<const uint4*>(x + c0 + i * step));
     }
     if (a.residual) {
         const uint16_t* residual = a.residual + row * a.ldr;
@@ -243,10 +246,10 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
         uint4 r[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (c0 + i * step < a.cols) r[i] = load_global(reinterpret_cast<const uint4*>(residual + c0 + i * step));
+            if (inside(i)) r[i] = load_global(reinterpret_cast<const uint4*>(residual + c0 + i * step));
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (c0 + i * step < a.cols) {
+            if (inside(i)) {
                 h[i] = add8(h[i], r[i]);
                 if (a.sum) *reinterpret_cast<uint4*>(sum + c0 + i * step) = h[i];
             }
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
     for (int i = 0; i < NV; ++i) {
         const int c = c0 + i * step;
         uint4 y = make_uint4(0u, 0u, 0u, 0u);
-        if (c < a.cols) {
+        if (inside(i)) {
             Pairs f, w;
             unpack8(h[i], f);
             weights8<W32>(a.w, c, w);
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
             y = pack8(f);
             if (a.y) *reinterpret_cast<uint4*>(to_y + c) = y;
         }
-        if (a.q_row) quantize_row8(y, q + c, s + scale_col_offset(c), c < a.cols, (c & 31) == 0 && c < 128 * nct);
+        if (a.q_row) quantize_row8(y, q + c, s + scale_col_offset(c), inside(i), (c & 31) == 0 && (FULL || c < 128 * nct));
     }
 }
 
@@ -293,6 +296,10 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
 // (eight a thread), so the sums of squares of a segment are one butterfly; the CTAs write theirs into each other's shared memory
 // and meet once.  The tile waits in shared memory, where the output takes its place and a thread then finds the 8 x 8 elements
 // whose columns it quantizes.
+// 8192 x 4096 with residual, sum and both orientations: 56 us, 72 % of the measured copy rate.  The transposed codes leave in
+// pieces of 32 bytes and their scales in single bytes (without them 48 us), and of the rest 7 us are the cluster: eight CTAs
+// start and meet together, and 5 % of the SMs fit no cluster of eight.  No quicker: four CTAs of 1024 columns (57), five CTAs an SM with
+// fewer registers (61), the sums sent asynchronously to a barrier in place of the meeting (57), all loads at once (55 to 56).
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -760,9 +767,10 @@ cudaError_t norm_rows(const NormArgs& a, cudaStream_t stream) {
     auto go = [&](auto kernel) {
         return launch_chained(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(threads, per), 0, 0, stream, a);
     };
-    if (nv == 1) return go(norm_rows_kernel<1, W32>);
-    if (nv == 2) return go(norm_rows_kernel<2, W32>);
-    return go(norm_rows_kernel<4, W32>);
+    const bool full = a.cols == nv * threads * 8;
+    if (nv == 1) return full ? go(norm_rows_kernel<1, W32, true>) : go(norm_rows_kernel<1, W32, false>);
+    if (nv == 2) return full ? go(norm_rows_kernel<2, W32, true>) : go(norm_rows_kernel<2, W32, false>);
+    return full ? go(norm_rows_kernel<4, W32, true>) : go(norm_rows_kernel<4, W32, false>);
 }
 
 template <int SEGS, bool W32>
