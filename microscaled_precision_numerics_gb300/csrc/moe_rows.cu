@@ -19,7 +19,7 @@ namespace {
 // count so far; the warps' counts of an expert are summed in their order, then the CTAs', then the experts'.
 //
 // Up to SORT_CLUSTER_MAX choices one cluster does it all in one launch, the choices in registers and the CTAs' counts exchanged
-// through shared memory: a chain of a few latencies (65536 choices 8.1 us; in two launches, as below, 13).  Beyond, the choices are cut into chunks, a CTA each: a first kernel counts
+// through shared memory: a chain of a few latencies (65536 choices 7.5 us; in two launches, as below, 13).  Beyond, the choices are cut into chunks, a CTA each: a first kernel counts
 // every chunk's choices of each expert, in the second each CTA adds up what the chunks before it hold.
 // ------------------------------------------------------------------------------------------------
 constexpr int SORT_THREADS = 1024, SORT_WARPS = SORT_THREADS / 32;
@@ -44,8 +44,8 @@ __device__ __forceinline__ int expert_of(const SortArgs& a, int64_t i, int64_t l
 }
 
 // Ranks the choices of a warp (ROUNDS times 32 neighbouring ones) among its own of the same expert; `mine` counts them.  The lanes
-// of the same expert are those whose numbers agree in every bit, by a vote a bit (65536 choices of 128 experts: 8.1 us, and
-// 9.9 with __match_any_sync).
+// of the same expert are those whose numbers agree in every bit, by a vote a bit (65536 choices of 128 experts: 1.8 us less than
+// with __match_any_sync).
 template <int ROUNDS>
 __device__ __forceinline__ void rank_in_warp(const int (&id)[ROUNDS], int (&rank)[ROUNDS], uint16_t* mine, int experts) {
     const unsigned before = (1u << (threadIdx.x & 31)) - 1u;
@@ -106,6 +106,9 @@ __device__ __forceinline__ void clear_counts(uint16_t* count, int experts) {
     for (int i = threadIdx.x; i < SORT_WARPS * experts / 2; i += SORT_THREADS) reinterpret_cast<uint32_t*>(count)[i] = 0u;
 }
 
+// Words of the tables of a CTA (an even number: staged choices of 8 bytes follow).
+__host__ __device__ inline int sort_table_words(int ctas, int experts) { return ((1 + ctas + SORT_WARPS / 2) * experts + 1) & ~1; }
+
 template <int ROUNDS>
 __global__ void __launch_bounds__(SORT_THREADS) moe_sort_kernel(const SortArgs a) {
     extern __shared__ int sm[];
@@ -116,6 +119,7 @@ __global__ void __launch_bounds__(SORT_THREADS) moe_sort_kernel(const SortArgs a
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(me));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(peers));
     uint16_t* count = reinterpret_cast<uint16_t*>(s_total + peers * a.experts);       // [warps][experts]
+    int2* staged = reinterpret_cast<int2*>(sm + sort_table_words(peers, a.experts));  // [choices of the CTA] row and choice, in row order
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");             // this CTA runs
     clear_counts(count, a.experts);
     chain_begin();
@@ -146,19 +150,35 @@ __global__ void __launch_bounds__(SORT_THREADS) moe_sort_kernel(const SortArgs a
             if (p < me) before += v;
         }
     const int start = sum_before(total, s_warp, placed);
+    int here = 0;
     if (tid < G) {
+        here = s_total[me * G + tid];
         s_next[tid] = start + before;
         if (me == 0) a.offsets[tid] = start;
     }
     if (me == 0 && tid == 0) a.offsets[G] = placed;
+    // the choices of this CTA in the order of their rows, so that those of an expert, neighbours in `source`, leave together (one by
+    // one, each with a sector of its own, 65536 of them took 0.7 us more)
+    __syncthreads();                                       // s_warp has been read
+    int staged_choices;
+    const int place = sum_before(here, s_warp, staged_choices);
+    if (tid < G) s_total[me * G + tid] = place;            // (read by this thread alone so far)
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
         const int64_t i = at + r * 32;
         if (i >= last) continue;
-        const int row = id[r] >= 0 ? s_next[id[r]] + count[warp * G + id[r]] + rank[r] : -1;
+        int row = -1;
+        if (id[r] >= 0) {
+            const int nth = count[warp * G + id[r]] + rank[r];
+            row = s_next[id[r]] + nth;
+            if (a.source) staged[s_total[me * G + id[r]] + nth] = make_int2(row, (int)i);
+        }
         a.rows[i] = row;
-        if (a.source && row >= 0) a.source[row] = (int32_t)i;
+    }
+    if (a.source) {
+        __syncthreads();
+        for (int p = tid; p < staged_choices; p += SORT_THREADS) a.source[staged[p].x] = staged[p].y;
     }
     if (a.source)
         for (int64_t r = placed + (int64_t)me * SORT_THREADS + tid; r < a.n; r += (int64_t)peers * SORT_THREADS) a.source[r] = -1;
@@ -226,7 +246,7 @@ __global__ void __launch_bounds__(SORT_THREADS) moe_place_kernel(const SortArgs 
 }
 
 // ------------------------------------------------------------------------------------------------
-// Dispatch: a warp takes 1 KB of a token's row (32 bytes a lane in two coalesced halves) to its top_k rows.  For rows in few
+// Dispatch: a warp takes 1 KB of a token's row (32 bytes a lane) to its top_k rows.  For rows in few
 // bits the first CTAs of the launch move the scale bytes meanwhile, by words of four scale columns: a warp a token, the groups'
 // tables in shared memory, and zeros between the groups.  Bound by HBM: 8192 tokens to 65536 rows of 2048 codes take 27 us, 22 of
 // them the rows (7.0 TB/s); the rest are a million scale words, a sector of their own each, since the rows that share one
@@ -331,7 +351,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) moe_dispatch_kernel(const MoveAr
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)(b - far * a.groups) * (MOVE_WARPS >> a.side) + (warp >> a.side);
     if (t >= a.tokens) return;
-    const int64_t b0 = (((int64_t)far << a.side) + (warp & ((1u << a.side) - 1u))) * MOVE_BYTES + lane * 16, b1 = b0 + 512;
+    const int64_t b0 = (((int64_t)far << a.side) + (warp & ((1u << a.side) - 1u))) * MOVE_BYTES + lane * 32, b1 = b0 + 16;
     const int row = lane < a.top_k ? load_global(a.rows + t * a.top_k + lane) : -1;
     uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
     if (b0 < a.row_bytes) v0 = load_global(reinterpret_cast<const uint4*>(a.x + t * a.pitch + b0));
@@ -339,8 +359,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) moe_dispatch_kernel(const MoveAr
     for (int j = 0; j < a.top_k; ++j) {
         const int r = __shfl_sync(0xFFFFFFFFu, row, j);
         if (r < 0 || r >= a.total_rows) continue;
-        if (b0 < a.row_bytes) *reinterpret_cast<uint4*>(a.y + r * a.y_pitch + b0) = v0;
-        if (b1 < a.row_bytes) *reinterpret_cast<uint4*>(a.y + r * a.y_pitch + b1) = v1;
+        if (b1 < a.row_bytes) stcs_32b(a.y + r * a.y_pitch + b0, v0, v1);
+        else if (b0 < a.row_bytes) *reinterpret_cast<uint4*>(a.y + r * a.y_pitch + b0) = v0;
     }
 }
 
@@ -485,13 +505,14 @@ cudaError_t sort_in_cluster(SortArgs a, cudaStream_t stream) {
     int unused = 0;
     const cudaError_t e = per_device_once(pd, unused, [kernel](int&) {
         const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (1 + SORT_CTAS + SORT_WARPS / 2) * MX_MAX_GROUPS * (int)sizeof(int));
+                                                   sort_table_words(SORT_CTAS, MX_MAX_GROUPS) * 4 + ROUNDS * SORT_THREADS * 8);
         return s != cudaSuccess ? s : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
     if (e != cudaSuccess) return e;
     a.chunk = ROUNDS * SORT_THREADS;
     const unsigned ctas = (unsigned)((a.n + a.chunk - 1) / a.chunk);
-    return launch_chained(kernel, dim3(ctas), dim3(SORT_THREADS), (size_t)(1 + ctas + SORT_WARPS / 2) * a.experts * sizeof(int), ctas, stream, a);
+    const size_t smem = (size_t)sort_table_words((int)ctas, a.experts) * 4 + (size_t)a.chunk * 8;
+    return launch_chained(kernel, dim3(ctas), dim3(SORT_THREADS), smem, ctas, stream, a);
 }
 
 }  // namespace
