@@ -3,13 +3,13 @@
 //   h = BF16(x + residual),  y = BF16(h w r),  r = 1 / sqrt(mean(h^2) + eps),  codes and scales of y in 32-blocks
 //   dx = r (dn - n mean(dn n)) + dsum,  dw = sum over rows of dy n,  with n = h r and dn = dy w
 //
-// Both are bound by HBM: a few operations for the 6 to 10 bytes of an element.  Every row is read once, kept in registers as
-// packed BF16 and written from there.
+// Both are close to HBM's rate and to the issue rate at once: 6 to 10 bytes of an element, and some twenty instructions.  Every
+// element is read once and waits as packed BF16, in registers or shared memory.
 //
 // The sum of squares has one order that depends on the row's width alone, so that a row's values are the same whichever
 // outputs are asked for and in whichever batch it stands (a product in training and one in generation read the same
-// codes): S_i over the 256 elements of segment i, eight elements a lane in a chain and the 32 lanes by a butterfly; then the
-// segments i and i + 32 in pairs and those by a butterfly again.  Where FP32's range does not hold the squares the row is
+// codes): S_i over the 256 elements of segment i, the even and the odd ones of a lane's eight in two chains and the 32 lanes by a
+// butterfly; then the segments i and i + 32 in pairs and those by a butterfly again.  Where FP32's range does not hold the squares the row is
 // summed once more in FP64.
 #include "../../include/mxnum.h"
 #include "../../include/mxnum_layer.h"
