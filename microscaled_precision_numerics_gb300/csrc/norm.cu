@@ -453,46 +453,41 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
             for (int k = first + i % 8; k < last; k += 8)
                 *reinterpret_cast<uint32_t*>(a.s_row + sf_offset(a.rows + i / 8, 4 * k, nct_row)) = 0u;
     }
-    // a warp 64 columns: lane -> chunk of eight columns, quarter of eight rows
-    const int chunk = lane & 7, q = lane >> 3, cc = warp * 64 + chunk * 8, gc = c_cta + cc;
+    // a warp 64 columns, a lane two neighbours: both whole 32-blocks are its own
+    const int cc = warp * 64 + lane * 2, gc = c_cta + cc;
     const int64_t nct = sf_col_tiles(a.rows, 32);
     const int padded_cols = (a.cols + 127) & ~127;
     if (warp * 64 >= C::COLS || c_cta + warp * 64 >= padded_cols) return;
     const bool gin = gc < a.cols;
-    uint32_t t[4][8];                                      // word k holds columns 2 k and 2 k + 1 of eight rows
+    uint32_t t[TILE_ROWS], m = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint4 y = *reinterpret_cast<const uint4*>(sm_tile + ((q * 8 + i) * C::COLS + cc) * 2);
-        t[0][i] = y.x; t[1][i] = y.y; t[2][i] = y.z; t[3][i] = y.w;
+    for (int i = 0; i < TILE_ROWS; ++i) {
+        t[i] = *reinterpret_cast<const uint32_t*>(sm_tile + (i * C::COLS + cc) * 2);
+        m = i == 0 ? t[0] : absmax_bf16x2(m, t[i]);
     }
-    uint8_t* q_col = a.q_col + (int64_t)gc * a.rows + r0 + q * 8;
-    uint8_t* s_col = a.s_col + sf_offset(gc, r0 / 32, nct);               // eight columns of a tile are 16 bytes apart
+    m = abs_halves(m);
+    uint8_t* q_col = a.q_col + (int64_t)gc * a.rows + r0;
+    uint8_t* s_col = a.s_col + sf_offset(gc, r0 / 32, nct);               // the next column's is 16 bytes on
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        uint32_t m = t[k][0];
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t s = e8m0_from_amax_bits(j ? m >> 16 : m & 0xFFFFu);
+        const float inv = inv_scale_from_e8m0(s);
+        uint32_t codes[TILE_ROWS / 4];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) m = absmax_bf16x2(m, t[k][i]);
-        m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-        m = abs_halves(absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16)));
+        for (int k = 0; k < TILE_ROWS / 4; ++k) {
+            float f[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t s = e8m0_from_amax_bits(j ? m >> 16 : m & 0xFFFFu);
-            const float inv = inv_scale_from_e8m0(s);
-            Pairs f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] = j ? f2_pack(bf16_hi(t[k][2 * i]), bf16_hi(t[k][2 * i + 1])) : f2_pack(bf16_lo(t[k][2 * i]), bf16_lo(t[k][2 * i + 1]));
-            times8(f, inv);
-            if (gin)
-                *reinterpret_cast<uint2*>(q_col) = make_uint2(cvt_e4m3_pairs(f[0], f[1]), cvt_e4m3_pairs(f[2], f[3]));
-            q_col += a.rows;
-            if (q == 0) s_col[(2 * k + j) * 16] = gin ? (uint8_t)s : (uint8_t)0;
+            for (int i = 0; i < 4; ++i) f[i] = __fmul_rn(j ? bf16_hi(t[4 * k + i]) : bf16_lo(t[4 * k + i]), inv);
+            codes[k] = cvt_e4m3x4(f[0], f[1], f[2], f[3]);
         }
+        if (gin)
+            stcs_32b(q_col + j * a.rows, make_uint4(codes[0], codes[1], codes[2], codes[3]), make_uint4(codes[4], codes[5], codes[6], codes[7]));
+        s_col[j * 16] = gin ? (uint8_t)s : (uint8_t)0;
     }
     // scale columns from rows / 32 up to a whole word: zeros
-    if (r0 + TILE_ROWS == a.rows && q == 0)
+    if (r0 + TILE_ROWS == a.rows)
         for (int64_t b = a.rows / 32; b < 4 * nct; ++b)
-            for (int j = 0; j < 8; ++j) a.s_col[sf_offset(gc + j, b, nct)] = 0;
+            for (int j = 0; j < 2; ++j) a.s_col[sf_offset(gc + j, b, nct)] = 0;
 }
 
 // ------------------------------------------------------------------------------------------------
