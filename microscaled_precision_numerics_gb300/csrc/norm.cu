@@ -188,10 +188,9 @@ struct NormArgs {
     uint8_t *q_row, *s_row, *q_col, *s_col;
 };
 
-// The codes of eight neighbouring elements of a row, to q, and the scale byte of the 32-block that four lanes hold, from the first
-// of them to s.  in: the elements lie inside the row; scaled: the block lies inside the scale layout, whose padding is zero.  All
-// lanes of the warp call it, with zeros where there are no elements.
-__device__ __forceinline__ void quantize_row8(const uint4& y, uint8_t* q, uint8_t* s, bool in, bool scaled) {
+// The codes of eight neighbouring elements of a row, to q where they lie inside it; returns the scale byte of the 32-block that four
+// lanes hold, 0 beyond the row.  All lanes of the warp call it, with zeros where there are no elements.
+__device__ __forceinline__ uint8_t quantize_row8(const uint4& y, uint8_t* q, bool in) {
     uint32_t m = absmax_bf16x2(absmax_bf16x2(y.x, y.y), absmax_bf16x2(y.z, y.w));
     m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = absmax_bf16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
@@ -201,7 +200,7 @@ __device__ __forceinline__ void quantize_row8(const uint4& y, uint8_t* q, uint8_
     times8(f, inv_scale_from_e8m0(byte));
     const uint2 codes = make_uint2(cvt_e4m3_pairs(f[0], f[1]), cvt_e4m3_pairs(f[2], f[3]));
     if (in) *reinterpret_cast<uint2*>(q) = codes;
-    if (scaled) *s = (uint8_t)byte;
+    return in ? (uint8_t)byte : (uint8_t)0;
 }
 // Offset of (row, 32-block of column c) in the row-wise scale layout, split into the row's and the column's part.
 __device__ __forceinline__ int64_t scale_row_offset(int64_t row, int64_t nct) {
@@ -288,7 +287,10 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
             y = pack8(f);
             if (a.y) *reinterpret_cast<uint4*>(to_y + c) = y;
         }
-        if (a.q_row) quantize_row8(y, q + c, s + scale_col_offset(c), inside(i), (c & 31) == 0 && (FULL || c < 128 * nct));
+        if (a.q_row) {
+            const uint8_t byte = quantize_row8(y, q + c, inside(i));
+            if ((c & 31) == 0 && (FULL || c < 128 * nct)) s[scale_col_offset(c)] = byte;
+        }
     }
 }
 
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
     extern __shared__ __align__(16) uint8_t sm_tile[];
     float* part = reinterpret_cast<float*>(sm_tile + C::TILE);            // [32][PART]
     __shared__ RowNorm s_norm[TILE_ROWS];
+    __shared__ __align__(4) uint8_t s_scales[TILE_ROWS][8 * SEGS];        // the rows' block scales
     cluster_arrive();                                      // this CTA runs: the others may write into its shared memory
     chain_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -421,9 +424,8 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
         slow_rows<SEGS>(a, sm_tile, part, s_norm, gseg, nseg, peers);
     }
     const int64_t nct_row = sf_col_tiles(a.cols, 32);
-    const bool scaled = (c & 31) == 0 && c < 128 * nct_row;
     uint16_t *to_sum = a.sum + (r0 + row0) * a.lds + c, *to_y = a.y + (r0 + row0) * a.ldy + c;
-    uint8_t *to_q = a.q_row + (r0 + row0) * a.cols + c, *to_s = a.s_row + scale_row_offset(r0 + row0, nct_row) + scale_col_offset(c);
+    uint8_t* to_q = a.q_row + (r0 + row0) * a.cols + c;
     Pairs w;
     if (in) weights8<W32>(a.w, c, w);
 #pragma unroll
@@ -441,12 +443,20 @@ __global__ void __launch_bounds__(TileCfg<SEGS>::THREADS, 8 / SEGS) norm_tile_ke
             if (a.y) *reinterpret_cast<uint4*>(to_y) = y;
         }
         *place(i) = y;
-        if (a.q_row) quantize_row8(y, to_q, to_s + 64 * i, in, scaled);   // four rows on: 64 bytes of the tile
+        if (a.q_row) {
+            const uint8_t byte = quantize_row8(y, to_q, in);
+            if ((lane & 3) == 0) s_scales[row0 + 4 * i][seg * 8 + lane / 4] = byte;
+        }
         to_sum += 4 * a.lds;
         to_y += 4 * a.ldy;
         to_q += 4 * (int64_t)a.cols;
     }
     __syncthreads();
+    if (a.q_row && threadIdx.x < TILE_ROWS * 2 * SEGS) {   // words of four blocks, those of a row 512 bytes apart
+        const int r = threadIdx.x / (2 * SEGS), k = threadIdx.x % (2 * SEGS), c4 = c_cta / 128 + k;
+        if (c4 < nct_row)
+            *reinterpret_cast<uint32_t*>(a.s_row + scale_row_offset(r0 + r, nct_row) + c4 * 512) = *reinterpret_cast<const uint32_t*>(&s_scales[r][4 * k]);
+    }
     if (a.q_row && r0 + TILE_ROWS == a.rows) {             // scale rows up to a whole tile: zeros, this CTA's columns
         const int pad = (int)(((a.rows + 127) & ~int64_t(127)) - a.rows), first = c_cta / 128, last = min((int)nct_row, first + C::COLS / 128);
         for (int i = threadIdx.x; i < pad * 8; i += C::THREADS)
