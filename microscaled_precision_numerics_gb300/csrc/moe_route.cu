@@ -4,9 +4,9 @@
 //   dz[id_j] = w_j (dw_j - sum_i w_i dw_i)   or   dz[e] = p_e (dw_j where e = id_j, else 0, - sum_i w_i dw_i)
 //
 // A warp takes a token: its logits stay in registers, expert e in lane e % 32, and are read once.  A choice is a scan of the lane's
-// keys and two warp reductions (the largest key, then the lowest index among the lanes that hold it).  Bound by the integer
-// instructions of the scans: 8 of 128 for 8192 tokens take 8.4 us (2 MB of logits), 8 of 512 28 us.  A lane that remembers its two
-// largest keys scans less often, but costs more at up to 128 experts (9.9 us) and gains 4 % at 512.
+// keys and two warp reductions (the largest key, then the first place among the lanes that hold it).  Bound by the integer
+// instructions of the scans: 8192 tokens, 8 of 128 experts (BF16) take 8.0 us, 8 of 512 (FP32, 17 MB) 12.7, 16 of 1024 24.7 (without
+// thinning out 28 and 79, the loads of a row behind one another).
 #include "../../include/mxnum.h"
 #include "../../include/mxnum_layer.h"
 #include "mx_internal.h"
@@ -22,6 +22,17 @@ template <bool F32>
 __device__ __forceinline__ float logit(const void* p, int64_t i) {
     if (F32) return load_global(static_cast<const float*>(p) + i);
     return __uint_as_float((uint32_t)load_global(static_cast<const uint16_t*>(p) + i) << 16);
+}
+
+// A row's logits, -inf beyond its end.  Every lane loads (its last one again there), so that all loads are on their way at once: behind
+// branches they followed one another (8192 x 1024 took 64 us).
+template <int EPL, bool F32>
+__device__ __forceinline__ void load_row(const void* logits, int64_t at, int experts, float (&z)[EPL]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) z[i] = logit<F32>(logits, at + min(i * 32 + lane, experts - 1));
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) z[i] = i * 32 + lane < experts ? z[i] : -INFINITY;
 }
 
 // Keys in the order of the logits: NaN above all, zeros of both signs alike, 0 for -inf and for what is taken already.
@@ -42,57 +53,95 @@ __device__ __forceinline__ float warp_add(float v) {
     return v;
 }
 
-// EPL: experts a lane.
-template <int EPL, bool F32>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS)
-moe_route_kernel(const void* logits, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize, int32_t* ids, float* weights) {
-    chain_begin();
+// The top_k largest of a warp's keys, key[i] of lane l in place i * 32 + l, of equal ones the first place: number j to lane j
+// (key 0: none left).
+template <int N>
+__device__ __forceinline__ void choose(uint32_t (&key)[N], int top_k, uint32_t& my_key, int& my_place) {
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * ROUTE_WARPS + (threadIdx.x >> 5);
-    if (t >= tokens) return;
-    uint32_t key[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = i * 32 + lane;
-        key[i] = e < experts ? key_of(logit<F32>(logits, t * ldl + e)) : 0u;
-    }
-    float all = 0.0f, top = 0.0f;
-    uint32_t my_key = 0u;                                  // of choice `lane`
-    int my_id = -1;
+    my_key = 0u;
+    my_place = 0;
     for (int j = 0; j < top_k; ++j) {
         uint32_t best = key[0];
         int at = lane;
 #pragma unroll
-        for (int i = 1; i < EPL; ++i)
+        for (int i = 1; i < N; ++i)
             if (key[i] > best) {
                 best = key[i];
                 at = i * 32 + lane;
             }
         const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, best);
-        if (most == 0u) break;                             // none left but -inf
-        const int id = (int)__reduce_min_sync(0xFFFFFFFFu, best == most ? (uint32_t)at : 0xFFFFFFFFu);
-        if (j == 0) {
-            top = value_of(most);
-            if (!normalize) {
-                float s = 0.0f;
+        if (most == 0u) break;
+        const int place = (int)__reduce_min_sync(0xFFFFFFFFu, best == most ? (uint32_t)at : 0xFFFFFFFFu);
 #pragma unroll
-                for (int i = 0; i < EPL; ++i) s += key[i] != 0u ? expf(value_of(key[i]) - top) : 0.0f;
-                all = warp_add(s);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (i * 32 + lane == id) key[i] = 0u;
+        for (int i = 0; i < N; ++i)
+            if (i * 32 + lane == place) key[i] = 0u;
         if (lane == j) {
-            my_id = id;
             my_key = most;
+            my_place = place;
         }
     }
-    const float mine = my_id >= 0 ? expf(value_of(my_key) - top) : 0.0f;
+}
+
+constexpr int ROUTE_FEW = 64;                              // candidates that two keys a lane hold
+
+// EPL: experts a lane.  From 256 experts on (EPL >= 8) the keys are thinned out first: the top_k-th largest of the lanes' maxima is
+// a bound that top_k keys reach, and few others do; those that reach it, in the order of the experts, are the ones to choose
+// from.  Should there be more than 64 (many equal logits), all are.
+template <int EPL, bool F32>
+__global__ void __launch_bounds__(32 * ROUTE_WARPS)
+moe_route_kernel(const void* logits, int64_t ldl, int64_t tokens, int experts, int top_k, int normalize, int32_t* ids, float* weights) {
+    constexpr bool THIN = EPL >= 8;
+    __shared__ uint2 s_few[THIN ? ROUTE_WARPS : 1][THIN ? ROUTE_FEW : 1];
+    chain_begin();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * ROUTE_WARPS + warp;
+    if (t >= tokens) return;
+    float z[EPL];
+    load_row<EPL, F32>(logits, t * ldl, experts, z);
+    uint32_t key[EPL], best = 0u;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+        key[i] = key_of(z[i]);
+        best = max(best, key[i]);
+    }
+    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, best);
+    const float top = value_of(most);                      // (no logit but -inf: not used)
+    float all = 0.0f;
+    if (!normalize) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) all += key[i] != 0u ? expf(value_of(key[i]) - top) : 0.0f;
+        all = warp_add(all);
+    }
+    uint32_t my_key = 0u;                                  // of choice `lane`
+    int my_id = 0, few = ROUTE_FEW + 1;
+    if constexpr (THIN) {
+        uint32_t bound = most, rest = best;
+        for (int j = 0; j < top_k && bound != 0u; ++j) {
+            bound = __reduce_max_sync(0xFFFFFFFFu, rest);
+            if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, rest == bound)) - 1) rest = 0u;
+        }
+        bound = max(bound, 1u);
+        few = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const unsigned reach = __ballot_sync(0xFFFFFFFFu, key[i] >= bound);
+            const int at = few + __popc(reach & ((1u << lane) - 1u));
+            if (key[i] >= bound && at < ROUTE_FEW) s_few[warp][at] = make_uint2(key[i], (uint32_t)(i * 32 + lane));
+            few += __popc(reach);
+        }
+        __syncwarp();
+        if (few <= ROUTE_FEW) {
+            uint32_t two[2] = {lane < few ? s_few[warp][lane].x : 0u, lane + 32 < few ? s_few[warp][lane + 32].x : 0u};
+            choose(two, top_k, my_key, my_id);
+            my_id = (int)s_few[warp][my_id].y;
+        }
+    }
+    if (few > ROUTE_FEW) choose(key, top_k, my_key, my_id);
+    const float mine = my_key != 0u ? expf(value_of(my_key) - top) : 0.0f;
     const float total = normalize ? warp_add(mine) : all;
     if (lane < top_k) {
-        ids[t * top_k + lane] = my_id;
-        weights[t * top_k + lane] = my_id >= 0 ? __fdiv_rn(mine, total) : 0.0f;
+        ids[t * top_k + lane] = my_key != 0u ? my_id : -1;
+        weights[t * top_k + lane] = my_key != 0u ? __fdiv_rn(mine, total) : 0.0f;
     }
 }
 
@@ -115,14 +164,15 @@ moe_route_backward_kernel(const void* logits, int64_t ldl, int64_t tokens, int e
         }
     }
     float p[EPL];                                          // all logits, then the softmax over all, then the gradient
+    if (!normalize) {
+        load_row<EPL, F32>(logits, t * ldl, experts, p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) p[i] = -INFINITY;
+    }
     float top = z;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = i * 32 + lane;
-        p[i] = -INFINITY;
-        if (!normalize && e < experts) p[i] = logit<F32>(logits, t * ldl + e);
-        top = fmaxf(top, p[i]);
-    }
+    for (int i = 0; i < EPL; ++i) top = fmaxf(top, p[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     float sum = 0.0f;

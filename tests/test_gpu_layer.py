@@ -304,6 +304,30 @@ def test_route_rows_that_leave_little_or_are_not_finite(mx, normalize):
     assert not masked.any() and np.isnan(host(dz)[2, 9])
 
 
+@pytest.mark.parametrize("experts,k", [(256, 8), (300, 32), (512, 1), (1024, 20)])
+def test_route_many_experts_with_equal_and_masked_logits(mx, experts, k):
+    """Rows that leave many equal candidates, few or none, or whose largest all lie in one lane's experts."""
+    z = torch.randn((12, experts), generator=torch.Generator().manual_seed(37)).to(DEV)
+    z[0] = 1.0                                             # all equal
+    z[1] = torch.randint(0, 3, (experts,), generator=torch.Generator().manual_seed(38)).float().to(DEV)
+    z[2] = -float("inf")
+    z[3] = -float("inf")
+    z[3, experts // 2] = -1e30
+    z[4, 5::32] += 100.0                                   # the largest in lane 5
+    z[5, ::2] = -float("inf")
+    z[6] = torch.arange(experts, device=DEV).float()
+    z[7] = -torch.arange(experts, device=DEV).float()
+    z[8, 70:90] = float("nan")
+    z[9] = torch.finfo(F32).min
+    for normalize in (False, True):
+        ids, w = run_route(mx, z, k, normalize)
+        want_ids, want_w = ref.route(host(z), k, normalize)
+        assert np.array_equal(host(ids), want_ids)
+        fine = [r for r in range(12) if r != 8]
+        within(w[fine], want_w[fine], np.minimum(weight_bound(host(z)[fine], want_w[fine]), 2e-5) + 2e-6 * want_w[fine])
+        assert np.isnan(host(w)[8]).all()
+
+
 def test_route_gradient_of_ids_given_twice_or_outside(mx):
     z = torch.randn((4, 12), generator=torch.Generator().manual_seed(34)).to(DEV)
     ids = torch.tensor([[3, 3, 1], [-1, 12, 5], [-1, -1, -1], [0, 11, 0]], dtype=I32, device=DEV)
