@@ -533,13 +533,20 @@ struct NormBackwardArgs {
     float *dw, *partial;
 };
 
-constexpr int NB_THREADS = 256;
-// CTAs of an SM by the registers and shared memory that NV vectors a thread take.
-template <int NV>
-constexpr int NB_PER_SM = NV <= 2 ? 3 : NV == 4 ? 2 : 1;
+// Three forms by the row's width.  NARROW, up to 1024: several rows side by side in CTAs of 256 threads, three an SM, weights in
+// registers (65536 x 128 takes 26 us, and 102 with a row a CTA).  MIDDLE, up to 4096: one row of one or two vectors a thread, otherwise
+// as narrow ones.  WIDE: two vectors a thread, up to 1024 threads of 64 registers.
+enum BackwardWidth { NARROW, MIDDLE, WIDE };
+template <int WIDTH>
+struct BackwardCfg {
+    static constexpr int THREADS = WIDTH == WIDE ? 1024 : 256;
+    static constexpr int PER_SM = WIDTH == WIDE ? 1 : 3;   // of full CTAs
+    static constexpr bool KEEP_W = WIDTH != WIDE;
+};
 constexpr int NB_CLUSTER = 2;                              // wider clusters leave SMs idle (four: 72 us where two take 57)
 constexpr int NB_PARTS = 228;                              // most partial sums of a column
 constexpr int NB_STAGES = 2;
+constexpr int NB_ROWS = 8;                                 // most rows side by side
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
@@ -554,19 +561,28 @@ __device__ __forceinline__ void copies_wait() {
 // them) while it works on this one: the loads wait in no registers, and a row's sums do not hold up the next row's.
 // FULL: every vector of every thread lies inside the row (its width is the threads' vectors exactly), which
 // spares the comparisons: 2 of 45 us for 8192 x 4096.
-template <int NV, bool W32, bool FULL>
-__global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kernel(const NormBackwardArgs a) {
+template <int WIDTH, int NV, bool W32, bool FULL>
+__global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH>::PER_SM) norm_backward_kernel(const NormBackwardArgs a) {
     extern __shared__ __align__(16) uint8_t sm_rows[];     // [stage][dy, h, dsum][NV][thread] of 16 bytes
-    __shared__ double sm_all[2][2][MAX_SEGS];
+    __shared__ double sm_all[4 * MAX_SEGS];                // [row side by side][turn][sum][segment]
     chain_begin();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, side = WIDTH == NARROW ? (int)blockDim.y : 1;
+    const int ty = WIDTH == NARROW ? (int)threadIdx.y : 0, tid = ty * blockDim.x + threadIdx.x, threads = blockDim.x * side;
+    // rows side by side have at most MAX_SEGS / NB_ROWS segments each
+    constexpr int sums = WIDTH == NARROW ? MAX_SEGS / NB_ROWS : MAX_SEGS;
+    auto meet = [&]() {                                    // of the threads of a row
+        if constexpr (WIDTH == NARROW) row_sync(ty, blockDim.x);
+        else __syncthreads();
+    };
+    auto sums_of = [&](uint32_t turn, int which) { return sm_all + (ty * 4 + turn * 2 + which) * sums; };
     const int nseg = (a.cols + SEG - 1) / SEG, tensors = a.dsum ? 3 : 2;
-    const uint32_t vector = blockDim.x * 16, tensor = NV * vector, stage_bytes = tensors * tensor;
-    const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm_rows) + threadIdx.x * 16;
+    const uint32_t vector = threads * 16, tensor = NV * vector, stage_bytes = tensors * tensor;
+    const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm_rows) + tid * 16;
     const int c0 = (warp * 32 + lane) * 8, step = warps * SEG;
     auto outside = [&](int i) { return !FULL && c0 + i * step >= a.cols; };
-    const uint16_t *dy = a.dy + blockIdx.x * a.lddy + c0, *from_h = a.h + blockIdx.x * a.ldh + c0, *dsum = a.dsum + blockIdx.x * a.ldds + c0;
-    uint16_t* dx = a.dx + blockIdx.x * a.lddx + c0;
+    const int64_t first = (int64_t)blockIdx.x * side + ty, next = (int64_t)gridDim.x * side;
+    const uint16_t *dy = a.dy + first * a.lddy + c0, *from_h = a.h + first * a.ldh + c0, *dsum = a.dsum + first * a.ldds + c0;
+    uint16_t* dx = a.dx + first * a.lddx + c0;
     auto fetch = [&](int64_t row, uint32_t stage) {        // rows in turn
         if (row < a.rows) {
 #pragma unroll
@@ -577,17 +593,17 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
                 copy16(at + tensor, from_h + i * step);
                 if (a.dsum) copy16(at + 2 * tensor, dsum + i * step);
             }
-            dy += gridDim.x * a.lddy;
-            from_h += gridDim.x * a.ldh;
-            dsum += gridDim.x * a.ldds;
+            dy += next * a.lddy;
+            from_h += next * a.ldh;
+            dsum += next * a.ldds;
         }
         copies_commit();                                   // an empty group where there is no row, so that the count goes on
     };
     auto fetched = [&](uint32_t stage, int which, int i) {
-        return *reinterpret_cast<const uint4*>(sm_rows + stage * stage_bytes + which * tensor + i * vector + threadIdx.x * 16);
+        return *reinterpret_cast<const uint4*>(sm_rows + stage * stage_bytes + which * tensor + i * vector + tid * 16);
     };
-    fetch(blockIdx.x, 0);
-    constexpr bool KEEP_W = NV <= 2;                       // weights in registers
+    fetch(first, 0);
+    constexpr bool KEEP_W = BackwardCfg<WIDTH>::KEEP_W;
     float dw[NV][8] = {}, kept[KEEP_W ? NV : 1][8];
     if (KEEP_W)
 #pragma unroll
@@ -602,8 +618,8 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
         }
     };
     uint32_t turn = 0;
-    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
-        fetch(row + gridDim.x, turn ^ 1);                  // into the stage that this thread read in the turn before
+    for (int64_t row = first; row < a.rows; row += next, turn ^= 1) {
+        fetch(row + next, turn ^ 1);                  // into the stage that this thread read in the turn before
         copies_wait<1>();
         float parts[2 * NV];
 #pragma unroll
@@ -623,12 +639,12 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
             parts[i] = __fadd_rn(s[0], s[1]);
             parts[NV + i] = __fadd_rn(inner[0], inner[1]);
         }
-        float* sm_s = reinterpret_cast<float*>(sm_all[turn][0]);
-        float* sm_c = reinterpret_cast<float*>(sm_all[turn][1]);
+        float* sm_s = reinterpret_cast<float*>(sums_of(turn, 0));
+        float* sm_c = reinterpret_cast<float*>(sums_of(turn, 1));
         const float mine = butterfly_of(parts);
         const int value = value_of_lane<2 * NV>(), my_seg = warp + (value % NV) * warps;
         if (first_of_value<2 * NV>() && my_seg < nseg) (value < NV ? sm_s : sm_c)[my_seg] = mine;
-        __syncthreads();
+        meet();
         float v[2] = {lane < nseg ? sm_s[lane] : 0.0f, lane < nseg ? sm_c[lane] : 0.0f};
         if (lane + 32 < nseg) {
             v[0] += sm_s[lane + 32];
@@ -640,7 +656,7 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
         float mean = __fmul_rn(__fmul_rn(cc, a.inv_cols), n.r);          // mean(dn n)
         // the products dn h likewise: too large, or so small that subnormals would decide (where eps does not)
         if (!fp32_holds(ss, a.eps) || !(fabsf(cc) <= FLT_MAX) || (fabsf(cc) < 7.88860905e-31f && a.eps < 9.09494702e-13f)) {
-            __syncthreads();                                             // the FP32 sums have been read
+            meet();                                                      // the FP32 sums have been read
 #pragma unroll 1
             for (int i = 0; i < NV; ++i) {
                 double inner = 0.0, squares = 0.0;
@@ -656,13 +672,13 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
                 squares = butterfly(squares);
                 inner = butterfly(inner);
                 if (lane == 0 && warp + i * warps < nseg) {
-                    sm_all[turn][0][warp + i * warps] = squares;
-                    sm_all[turn][1][warp + i * warps] = inner;
+                    sums_of(turn, 0)[warp + i * warps] = squares;
+                    sums_of(turn, 1)[warp + i * warps] = inner;
                 }
             }
-            __syncthreads();
-            n = norm_of_wide(segments_sum(sm_all[turn][0], nseg), a.cols, a.eps);
-            mean = (float)(segments_sum(sm_all[turn][1], nseg) / a.cols * n.p * n.r);
+            meet();
+            n = norm_of_wide(segments_sum(sums_of(turn, 0), nseg), a.cols, a.eps);
+            mean = (float)(segments_sum(sums_of(turn, 1), nseg) / a.cols * n.p * n.r);
         }
         // a factor far from 1 is split as a slow row's is, so that dy r keeps its bits where dy n has them
         if (n.r < 9.53674316e-7f || n.r > 1048576.0f) {                  // 2^-20, 2^20; neither for a slow row
@@ -703,10 +719,10 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
         };
         if (n.p != 1.0f) emit(std::true_type{});
         else emit(std::false_type{});
-        dx += gridDim.x * a.lddx;
+        dx += next * a.lddx;
     }
     // the cluster's sums: each CTA's in its shared memory (the ring is free: 8 bytes a column and more), a share of the columns each
-    float* sm_dw = reinterpret_cast<float*>(sm_rows);
+    float *sm_first = reinterpret_cast<float*>(sm_rows), *sm_dw = sm_first + ty * a.cols;
     __syncthreads();                                       // the last row has been read
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -718,14 +734,15 @@ __global__ void __launch_bounds__(NB_THREADS, NB_PER_SM<NV>) norm_backward_kerne
     }
     cluster_sync();
     const int peers = (int)cluster_size();
-    for (int c = ((int)cluster_rank() * blockDim.x + threadIdx.x) * 4; c < a.cols; c += peers * blockDim.x * 4) {
+    for (int c = ((int)cluster_rank() * threads + tid) * 4; c < a.cols; c += peers * threads * 4) {
         uint64_t s0 = 0, s1 = 0;
-        for (int p = 0; p < peers; ++p) {
-            uint64_t v0, v1;
-            asm volatile("ld.shared::cluster.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(peer_address(sm_dw + c, p)) : "memory");
-            s0 = f2_add(s0, v0);
-            s1 = f2_add(s1, v1);
-        }
+        for (int p = 0; p < peers; ++p)
+            for (int g = 0; g < side; ++g) {
+                uint64_t v0, v1;
+                asm volatile("ld.shared::cluster.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(peer_address(sm_first + g * a.cols + c, p)) : "memory");
+                s0 = f2_add(s0, v0);
+                s1 = f2_add(s1, v1);
+            }
         *reinterpret_cast<ulonglong2*>(a.partial + (int64_t)(blockIdx.x / peers) * a.cols + c) = make_ulonglong2(s0, s1);
     }
     cluster_sync();                                        // nobody leaves while the others read its sums
@@ -753,10 +770,10 @@ __global__ void __launch_bounds__(32 * ND_WARPS) norm_dweight_kernel(const float
     if (lane == 0 && blockIdx.x * 32 + warp < cols) dw[blockIdx.x * 32 + warp] = s;
 }
 
-// Vectors of eight elements a thread (1, 2, 4 or 8) such that at most `threads` take a row, and whole warps of threads.
-int row_threads(int64_t cols, int threads, int& nv) {
+// Vectors of eight elements a thread (`least` or a power of two times it) such that at most `threads` take a row, and whole warps of threads.
+int row_threads(int64_t cols, int threads, int& nv, int least = 1) {
     const int64_t vectors = (cols + 7) / 8;
-    nv = 1;
+    nv = least;
     while (nv * threads < vectors) nv *= 2;
     return (int)(((vectors + nv - 1) / nv + 31) / 32 * 32);
 }
@@ -793,19 +810,21 @@ cudaError_t norm_tile(const NormArgs& a, cudaStream_t stream) {
     return launch_chained(kernel, dim3((unsigned)(a.rows / TILE_ROWS) * cluster), dim3(C::THREADS), C::SMEM, cluster, stream, a);
 }
 
-template <int NV, bool W32, bool FULL>
-cudaError_t norm_backward(const NormBackwardArgs& a, int threads, cudaStream_t stream) {
-    auto kernel = norm_backward_kernel<NV, W32, FULL>;
+template <int WIDTH, int NV, bool W32, bool FULL>
+cudaError_t norm_backward(const NormBackwardArgs& a, int threads, int side, cudaStream_t stream) {
+    using C = BackwardCfg<WIDTH>;
+    auto kernel = norm_backward_kernel<WIDTH, NV, W32, FULL>;
     static PerDevice pd;
     int sms = 0;
     const cudaError_t e = per_device_once(pd, sms, [kernel](int& n) {
         n = device_sm_count();
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_STAGES * 3 * NV * NB_THREADS * 16);
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_STAGES * 3 * NV * C::THREADS * 16);
     });
     if (e != cudaSuccess) return e;
-    const int parts = (int)min64((a.rows + NB_CLUSTER - 1) / NB_CLUSTER, min(NB_PARTS, NB_PER_SM<NV> * sms / NB_CLUSTER));
-    const cudaError_t e2 = launch_chained(kernel, dim3(parts * NB_CLUSTER), dim3(threads),
-                                          (size_t)NB_STAGES * (a.dsum ? 3 : 2) * NV * threads * 16, NB_CLUSTER, stream, a);
+    const int per_sm = WIDTH == WIDE ? min(3, C::THREADS / threads) : C::PER_SM;
+    const int parts = (int)min64((a.rows + NB_CLUSTER * side - 1) / (NB_CLUSTER * side), min(NB_PARTS, per_sm * sms / NB_CLUSTER));
+    const cudaError_t e2 = launch_chained(kernel, dim3(parts * NB_CLUSTER), dim3(threads, side),
+                                          (size_t)NB_STAGES * (a.dsum ? 3 : 2) * NV * threads * side * 16, NB_CLUSTER, stream, a);
     if (e2 != cudaSuccess) return e2;
     return launch_chained(norm_dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(32 * ND_WARPS), 0, 0, stream,
                           static_cast<const float*>(a.partial), parts, a.cols, a.dw);
@@ -814,15 +833,21 @@ cudaError_t norm_backward(const NormBackwardArgs& a, int threads, cudaStream_t s
 template <bool W32>
 cudaError_t norm_backward(const NormBackwardArgs& a, cudaStream_t stream) {
     int nv;
-    const int threads = row_threads(a.cols, NB_THREADS, nv);
+    int threads = row_threads(a.cols, 256, nv);
+    if (nv > 2) threads = row_threads(a.cols, 1024, nv, 2);
+    // rows side by side: as many as 256 threads take, but not more than leave a row to every CTA
+    int side = min(NB_ROWS, 256 / threads);
+    while (side > 1 && a.rows < (int64_t)side * NB_CLUSTER * NB_PARTS) side /= 2;
     const bool full = a.cols == nv * threads * 8;
-    auto go = [&](auto n) {
-        return full ? norm_backward<n.value, W32, true>(a, threads, stream) : norm_backward<n.value, W32, false>(a, threads, stream);
+    auto go = [&](auto w, auto n) {
+        return full ? norm_backward<w.value, n.value, W32, true>(a, threads, max(1, side), stream)
+                    : norm_backward<w.value, n.value, W32, false>(a, threads, max(1, side), stream);
     };
-    if (nv == 1) return go(std::integral_constant<int, 1>{});
-    if (nv == 2) return go(std::integral_constant<int, 2>{});
-    if (nv == 4) return go(std::integral_constant<int, 4>{});
-    return go(std::integral_constant<int, 8>{});
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (side > 1) return go(std::integral_constant<int, NARROW>{}, One{});
+    if (a.cols > 4096) return go(std::integral_constant<int, WIDE>{}, Two{});
+    return nv == 1 ? go(std::integral_constant<int, MIDDLE>{}, One{}) : go(std::integral_constant<int, MIDDLE>{}, Two{});
 }
 
 }  // namespace

@@ -163,7 +163,8 @@ def test_norm_zero_rows_and_rows_that_are_not_finite(mx):
     assert torch.isnan(y).all()
 
 
-BACKWARD_SIZES = [(1, 8), (1, 2048), (5, 96), (33, 1000), (700, 256), (3, 8200), (2, 16384), (311, 2048)]
+BACKWARD_SIZES = [(1, 8), (1, 2048), (5, 96), (33, 1000), (700, 256), (3, 8200), (2, 16384), (311, 2048), (2000, 512), (4001, 128), (5, 5120),
+                  (470, 4104), (9, 8192), (1900, 1024), (3700, 72)]
 
 
 @pytest.mark.parametrize("rows,cols", BACKWARD_SIZES)
