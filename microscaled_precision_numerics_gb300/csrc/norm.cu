@@ -296,12 +296,12 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
 
 // With column-wise codes: a cluster takes 32 rows, its CTAs T_SEGS segments of them each.  A warp takes whole segments of rows
 // (eight a thread), so the sums of squares of a segment are one butterfly; the CTAs write theirs into each other's shared memory
-// and meet once.  The tile waits in shared memory, where the output takes its place and a thread then finds the 8 x 8 elements
-// whose columns it quantizes.
-// 8192 x 4096 with residual, sum and both orientations: 56 us, 72 % of the measured copy rate.  The transposed codes leave in
-// pieces of 32 bytes and their scales in single bytes (without them 48 us), and of the rest 7 us are the cluster: eight CTAs
-// start and meet together, and 5 % of the SMs fit no cluster of eight.  No quicker: four CTAs of 1024 columns (57), five CTAs an SM with
-// fewer registers (61), the sums sent asynchronously to a barrier in place of the meeting (57), all loads at once (55 to 56).
+// and meet once.  The tile waits in shared memory, where the output takes its place and a thread then finds the two columns
+// that it quantizes.
+// 8192 x 4096 with residual, sum and both orientations: 53 us, 75 % of the measured copy rate.  Some 7 us are the cluster: eight CTAs
+// start and meet together, and 5 % of the SMs fit no cluster of eight.  The transposed codes leave in pieces of 32 bytes and their
+// scales in single bytes.  No quicker: four CTAs of 1024 columns, five CTAs an SM with 48 registers (59), the sums sent
+// asynchronously to a barrier in place of the meeting, all loads at once.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
