@@ -10,6 +10,8 @@
 #include "mx_internal.h"
 #include "mx_chain.cuh"
 
+#include <type_traits>
+
 namespace mxk {
 
 namespace {
@@ -263,8 +265,9 @@ struct MoveArgs {
     int64_t tokens, row_bytes, total_rows;
     const int32_t* rows;
     int top_k;
-    unsigned groups, scale_ctas;                           // CTAs along the tokens; 0 scale CTAs: rows alone
-    int side;                                              // log2 of the warps side by side on a token
+    unsigned scale_ctas;                                   // 0: rows alone
+    uint32_t pieces;                                       // of MOVE_BYTES in a row
+    DivU32 dv_pieces;
     const uint8_t* s;
     const float* s2;
     int64_t columns;                                       // scale columns
@@ -347,11 +350,11 @@ __global__ void __launch_bounds__(MOVE_THREADS) moe_dispatch_kernel(const MoveAr
         move_scales(a);
         return;
     }
-    const unsigned b = blockIdx.x - a.scale_ctas, far = b / a.groups, warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)(b - far * a.groups) * (MOVE_WARPS >> a.side) + (warp >> a.side);
+    const uint32_t item = (blockIdx.x - a.scale_ctas) * MOVE_WARPS + (threadIdx.x >> 5);
+    const int64_t t = divu32(item, a.dv_pieces);
     if (t >= a.tokens) return;
-    const int64_t b0 = (((int64_t)far << a.side) + (warp & ((1u << a.side) - 1u))) * MOVE_BYTES + lane * 32, b1 = b0 + 16;
+    const int64_t b0 = (int64_t)(item - (uint32_t)t * a.pieces) * MOVE_BYTES + lane * 32, b1 = b0 + 16;
     const int row = lane < a.top_k ? load_global(a.rows + t * a.top_k + lane) : -1;
     uint4 v0 = make_uint4(0u, 0u, 0u, 0u), v1 = v0;
     if (b0 < a.row_bytes) v0 = load_global(reinterpret_cast<const uint4*>(a.x + t * a.pitch + b0));
@@ -365,8 +368,8 @@ __global__ void __launch_bounds__(MOVE_THREADS) moe_dispatch_kernel(const MoveAr
 }
 
 // ------------------------------------------------------------------------------------------------
-// Combine: a warp takes 256 elements of a token, eight rows' loads in flight; the warps of a CTA take the pieces of the same rows
-// (46.5 us for 8192 x 8 rows of 2048, 96 % of the measured copy rate; 51 with the pieces of eight tokens in a CTA).
+// Combine: a warp takes 256 elements of a token, eight rows' loads in flight; neighbouring warps take neighbouring pieces of the
+// same rows (46.5 us for 8192 x 8 rows of 2048, 96 % of the measured copy rate; 51 with the pieces of eight tokens in a CTA).
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -380,16 +383,19 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-constexpr int COMBINE_ROWS = 8;                            // rows fetched side by side
+constexpr int COMBINE_ROWS = 8;                            // most rows fetched side by side
 
-__global__ void __launch_bounds__(32 * MOVE_WARPS)
+// ROWS: top_k up to COMBINE_ROWS, so that no slots without a row are gone through; MANY: top_k is larger, several passes.
+template <int ROWS, bool MANY>
+__global__ void __launch_bounds__(MOVE_THREADS)
 moe_combine_kernel(const uint16_t* z, int64_t ldz, int64_t total_rows, int64_t hidden, const int32_t* rows, const float* weights,
-                   int64_t tokens, int top_k, const uint16_t* residual, int64_t ldr, uint16_t* y, int64_t ldy, int side) {
+                   int64_t tokens, int top_k, const uint16_t* residual, int64_t ldr, uint16_t* y, int64_t ldy, uint32_t pieces, DivU32 dv_pieces) {
     chain_begin();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t = (int64_t)blockIdx.x * (MOVE_WARPS >> side) + (warp >> side);
+    const int lane = threadIdx.x & 31;
+    const uint32_t item = blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
+    const int64_t t = divu32(item, dv_pieces);
     if (t >= tokens) return;
-    const int64_t c = (((int64_t)blockIdx.y << side) + (warp & ((1 << side) - 1))) * 256 + lane * 8;
+    const int64_t c = (int64_t)(item - (uint32_t)t * pieces) * 256 + lane * 8;
     const bool in = c < hidden;
     int row = -1;
     float weight = 0.0f;
@@ -401,19 +407,19 @@ moe_combine_kernel(const uint16_t* z, int64_t ldz, int64_t total_rows, int64_t h
     uint4 res = make_uint4(0u, 0u, 0u, 0u);
     if (residual && in) res = load_global(reinterpret_cast<const uint4*>(residual + t * ldr + c));
     float acc[8] = {};
-    for (int j0 = 0; j0 < top_k; j0 += COMBINE_ROWS) {
-        uint4 v[COMBINE_ROWS];
+    for (int j0 = 0; j0 < (MANY ? top_k : ROWS); j0 += ROWS) {
+        uint4 v[ROWS];
 #pragma unroll
-        for (int j = 0; j < COMBINE_ROWS; ++j) {
-            const int r = j0 + j < 32 ? __shfl_sync(0xFFFFFFFFu, row, j0 + j) : -1;
+        for (int j = 0; j < ROWS; ++j) {
+            const int r = !MANY || j0 + j < top_k ? __shfl_sync(0xFFFFFFFFu, row, j0 + j) : -1;
             v[j] = make_uint4(0u, 0u, 0u, 0u);
             if (r >= 0 && in) v[j] = load_global(reinterpret_cast<const uint4*>(z + r * ldz + c));
         }
 #pragma unroll
-        for (int j = 0; j < COMBINE_ROWS; ++j) {
-            const int r = __shfl_sync(0xFFFFFFFFu, row, (j0 + j) & 31);
+        for (int j = 0; j < ROWS; ++j) {
+            const int r = !MANY || j0 + j < top_k ? __shfl_sync(0xFFFFFFFFu, row, j0 + j) : -1;
             const float w = __shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31);
-            if (r < 0 || j0 + j >= top_k) continue;
+            if (r < 0) continue;
             float f[8];
             unpack8(v[j], f);
 #pragma unroll
@@ -433,6 +439,7 @@ moe_combine_kernel(const uint16_t* z, int64_t ldz, int64_t total_rows, int64_t h
 // A CTA a token; the products of the weights' gradient are summed per thread, by a butterfly and over the warps in order.  8192 x 8
 // rows of 2048 take 84 us, the measured copy rate.
 constexpr int CB_THREADS = 256;
+template <int ROWS, bool MANY>
 __global__ void __launch_bounds__(CB_THREADS)
 moe_combine_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int64_t total_rows, int64_t hidden,
                             const int32_t* rows, const float* weights, int top_k, uint16_t* dz, int64_t lddz, float* dweights) {
@@ -447,24 +454,24 @@ moe_combine_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* z,
         if (row >= total_rows) row = -1;
         weight = load_global(weights + t * top_k + lane);
     }
-    for (int j0 = 0; j0 < top_k; j0 += COMBINE_ROWS) {
-        float dot[COMBINE_ROWS] = {};
+    for (int j0 = 0; j0 < (MANY ? top_k : ROWS); j0 += ROWS) {
+        float dot[ROWS] = {};
         for (int64_t c0 = 0; c0 < hidden; c0 += (int64_t)blockDim.x * 8) {
             const int64_t c = c0 + threadIdx.x * 8;
             const bool in = c < hidden;
-            uint4 v[COMBINE_ROWS], g = make_uint4(0u, 0u, 0u, 0u);
+            uint4 v[ROWS], g = make_uint4(0u, 0u, 0u, 0u);
             if (in) g = load_global(reinterpret_cast<const uint4*>(dy + t * lddy + c));
 #pragma unroll
-            for (int j = 0; j < COMBINE_ROWS; ++j) {
-                const int r = j0 + j < top_k ? __shfl_sync(0xFFFFFFFFu, row, j0 + j) : -1;
+            for (int j = 0; j < ROWS; ++j) {
+                const int r = !MANY || j0 + j < top_k ? __shfl_sync(0xFFFFFFFFu, row, j0 + j) : -1;
                 v[j] = make_uint4(0u, 0u, 0u, 0u);
                 if (r >= 0 && in) v[j] = load_global(reinterpret_cast<const uint4*>(z + r * ldz + c));
             }
             float d[8];
             unpack8(g, d);
 #pragma unroll
-            for (int j = 0; j < COMBINE_ROWS; ++j) {
-                const int r = j0 + j < top_k ? __shfl_sync(0xFFFFFFFFu, row, j0 + j) : -1;
+            for (int j = 0; j < ROWS; ++j) {
+                const int r = !MANY || j0 + j < top_k ? __shfl_sync(0xFFFFFFFFu, row, j0 + j) : -1;
                 const float w = __shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31);
                 if (r < 0) continue;
                 float f[8];
@@ -478,10 +485,10 @@ moe_combine_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* z,
             }
         }
 #pragma unroll
-        for (int j = 0; j < COMBINE_ROWS; ++j) {
+        for (int j = 0; j < ROWS; ++j) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], o);
-            if (lane == 0 && j0 + j < top_k) sm[warp][j0 + j] = dot[j];
+            if (lane == 0 && (!MANY || j0 + j < top_k)) sm[warp][j0 + j] = dot[j];
         }
     }
     __syncthreads();
@@ -545,22 +552,10 @@ cudaError_t launch_moe_sort(const int32_t* ids, int64_t choices, int experts, in
     return launch_chained(moe_place_kernel, dim3(a.chunks), dim3(SORT_THREADS), (size_t)(1 + SORT_WARPS / 2) * experts * sizeof(int), 0, stream, a);
 }
 
-// Warps of a CTA side by side on a token of `pieces` pieces, as a power of two: the pieces of a row are on their way together,
-// which keeps memory pages open.
-static int warps_side_by_side(int64_t pieces) {
-    int side = 0;
-    while (side < 3 && (2 << side) <= pieces) ++side;
-    static_assert(MOVE_WARPS == 8, "eight warps at most");
-    return side;
-}
-
 static cudaError_t move_rows(MoveArgs a, cudaStream_t stream) {
-    const int64_t pieces = (a.row_bytes + MOVE_BYTES - 1) / MOVE_BYTES;
-    a.side = warps_side_by_side(pieces);
-    const int64_t tokens_a_cta = MOVE_WARPS >> a.side, groups = (a.tokens + tokens_a_cta - 1) / tokens_a_cta;
-    a.groups = (unsigned)groups;
-    const int64_t ctas = a.scale_ctas + groups * ((pieces + (1 << a.side) - 1) >> a.side);
-    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    a.pieces = (uint32_t)((a.row_bytes + MOVE_BYTES - 1) / MOVE_BYTES);
+    a.dv_pieces = make_divu32(a.pieces);
+    const int64_t ctas = a.scale_ctas + (a.tokens * a.pieces + MOVE_WARPS - 1) / MOVE_WARPS;
     return launch_chained(moe_dispatch_kernel, dim3((unsigned)ctas), dim3(MOVE_THREADS), a.scale_ctas ? (size_t)12 * (a.G + 1) + 128 : 0, 0,
                           stream, a);
 }
@@ -591,22 +586,41 @@ cudaError_t launch_moe_dispatch_quantized(bool fp4, const uint8_t* q, const uint
     return move_rows(a, stream);
 }
 
+// f of the rows that are fetched side by side and whether there are more, as constants.
+template <typename F>
+static cudaError_t for_rows(int top_k, F&& f) {
+    switch (top_k) {
+        case 1: return f(std::integral_constant<int, 1>{}, std::false_type{});
+        case 2: return f(std::integral_constant<int, 2>{}, std::false_type{});
+        case 3: return f(std::integral_constant<int, 3>{}, std::false_type{});
+        case 4: return f(std::integral_constant<int, 4>{}, std::false_type{});
+        case 5: return f(std::integral_constant<int, 5>{}, std::false_type{});
+        case 6: return f(std::integral_constant<int, 6>{}, std::false_type{});
+        case 7: return f(std::integral_constant<int, 7>{}, std::false_type{});
+        case 8: return f(std::integral_constant<int, 8>{}, std::false_type{});
+        default: return f(std::integral_constant<int, COMBINE_ROWS>{}, std::true_type{});
+    }
+}
+
 cudaError_t launch_moe_combine(const uint16_t* z, int64_t ldz, int64_t total_rows, int64_t hidden, const int32_t* rows,
                                const float* weights, int64_t tokens, int top_k, const uint16_t* residual, int64_t ldr, uint16_t* y,
                                int64_t ldy, cudaStream_t stream) {
-    const int64_t pieces = (hidden + 255) / 256;
-    const int side = warps_side_by_side(pieces), tokens_a_cta = MOVE_WARPS >> side;
-    const dim3 grid((unsigned)((tokens + tokens_a_cta - 1) / tokens_a_cta), (unsigned)((pieces + (1 << side) - 1) >> side));
-    return launch_chained(moe_combine_kernel, grid, dim3(MOVE_THREADS), 0, 0, stream, z, ldz, total_rows, hidden, rows, weights, tokens, top_k,
-                          residual, ldr, y, ldy, side);
+    const uint32_t pieces = (uint32_t)((hidden + 255) / 256);
+    const unsigned ctas = (unsigned)((tokens * pieces + MOVE_WARPS - 1) / MOVE_WARPS);
+    return for_rows(top_k, [&](auto n, auto many) {
+        return launch_chained(moe_combine_kernel<n.value, many.value>, dim3(ctas), dim3(MOVE_THREADS), 0, 0, stream, z, ldz, total_rows, hidden, rows, weights,
+                              tokens, top_k, residual, ldr, y, ldy, pieces, make_divu32(pieces));
+    });
 }
 
 cudaError_t launch_moe_combine_backward(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz, int64_t total_rows,
                                         int64_t hidden, const int32_t* rows, const float* weights, int64_t tokens, int top_k,
                                         uint16_t* dz, int64_t lddz, float* dweights, cudaStream_t stream) {
     const int threads = (int)min64(CB_THREADS, (hidden / 8 + 31) / 32 * 32);
-    return launch_chained(moe_combine_backward_kernel, dim3((unsigned)tokens), dim3(threads), 0, 0, stream, dy, lddy, z, ldz, total_rows,
-                          hidden, rows, weights, top_k, dz, lddz, dweights);
+    return for_rows(top_k, [&](auto n, auto many) {
+        return launch_chained(moe_combine_backward_kernel<n.value, many.value>, dim3((unsigned)tokens), dim3(threads), 0, 0, stream, dy, lddy, z, ldz,
+                              total_rows, hidden, rows, weights, top_k, dz, lddz, dweights);
+    });
 }
 
 }  // namespace mxk

@@ -681,7 +681,9 @@ static mx_status check_moe_rows(const int32_t* rows, int64_t tokens, int64_t top
     if (!aligned4(rows)) return MX_ERR_ALIGNMENT;
     const mx_status st = check_choices(tokens, top_k);
     if (st != MX_OK) return st;
-    return hidden <= (int64_t(1) << 23) && total_rows <= INT32_MAX ? MX_OK : MX_ERR_UNSUPPORTED;
+    // (pieces of 256 elements of all tokens are numbered with 32 bits)
+    return hidden <= (int64_t(1) << 23) && total_rows <= INT32_MAX && tokens <= (int64_t)(UINT32_MAX - 8) / ((hidden + 255) / 256)
+               ? MX_OK : MX_ERR_UNSUPPORTED;
 }
 
 mx_status mx_moe_dispatch(const void* x, int64_t ldx, int64_t tokens, int64_t hidden, const int32_t* rows, int64_t top_k,
