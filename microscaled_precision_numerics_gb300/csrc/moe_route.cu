@@ -188,25 +188,30 @@ moe_route_backward_kernel(const void* logits, int64_t ldl, int64_t tokens, int e
     const bool none = sum == 0.0f;                         // nothing chosen, or nothing but -inf
     w = none || w == 0.0f ? 0.0f : __fdiv_rn(w, sum);
     const float inner = warp_add(__fmul_rn(w, dw));
+    const float share = none ? 0.0f : -__fdiv_rn(inner, sum);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-        p[i] = normalize || none || p[i] == 0.0f ? 0.0f : -__fmul_rn(__fdiv_rn(p[i], sum), inner);
+    for (int i = 0; i < EPL; ++i) p[i] = normalize || p[i] == 0.0f ? 0.0f : __fmul_rn(p[i], share);
     const float part = normalize ? __fmul_rn(w, __fsub_rn(dw, inner)) : __fmul_rn(w, dw);
+    // what a chosen expert has besides, from all of its choices (one, unless an id is given twice); the first of them writes it
+    float chosen = normalize || w == 0.0f ? 0.0f : -__fmul_rn(w, inner);
+    bool mine = id >= 0;
     for (int j = 0; j < top_k; ++j) {
         const int e = __shfl_sync(0xFFFFFFFFu, id, j);
         const float d = __shfl_sync(0xFFFFFFFFu, part, j);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-            if (i * 32 + lane == e) p[i] += d;
-    }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = i * 32 + lane;
-        if (e < experts) {
-            if (F32) static_cast<float*>(dlogits)[t * ldd + e] = p[i];
-            else static_cast<uint16_t*>(dlogits)[t * ldd + e] = (uint16_t)pack_bf16x2(p[i], 0.0f);
+        if (e == id) {
+            chosen += d;
+            mine = mine && j >= lane;
         }
     }
+    auto store = [&](int e, float v) {
+        if (F32) static_cast<float*>(dlogits)[t * ldd + e] = v;
+        else static_cast<uint16_t*>(dlogits)[t * ldd + e] = (uint16_t)pack_bf16x2(v, 0.0f);
+    };
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (i * 32 + lane < experts) store(i * 32 + lane, p[i]);
+    __syncwarp();                                          // the row is written: the chosen ones over it
+    if (mine) store(id, chosen);
 }
 
 }  // namespace
