@@ -544,7 +544,7 @@ struct BackwardCfg {
     static constexpr bool KEEP_W = WIDTH != WIDE;
 };
 constexpr int NB_CLUSTER = 2;                              // wider clusters leave SMs idle (four: 72 us where two take 57)
-constexpr int NB_PARTS = 228;                              // most partial sums of a column
+constexpr int NB_PARTS = 304;                              // most partial sums of a column: pairs of four CTAs an SM
 constexpr int NB_STAGES = 2;
 constexpr int NB_ROWS = 8;                                 // most rows side by side
 
@@ -755,15 +755,15 @@ __global__ void __launch_bounds__(32 * ND_WARPS) norm_dweight_kernel(const float
     chain_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
-    static_assert(NB_PARTS <= 8 * ND_WARPS, "eight loads a thread, side by side");
-    float v[8], s = 0.0f;
+    constexpr int LOADS = (NB_PARTS + ND_WARPS - 1) / ND_WARPS;           // side by side
+    float v[LOADS], s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < LOADS; ++i) {
         const int p = warp + i * ND_WARPS;
         v[i] = p < parts && c < cols ? load_global(partial + (int64_t)p * cols + c) : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += v[i];
+    for (int i = 0; i < LOADS; ++i) s += v[i];
     sm[warp][lane] = s;
     __syncthreads();
     s = butterfly(sm[lane][warp]);                         // a warp a column
@@ -821,7 +821,8 @@ cudaError_t norm_backward(const NormBackwardArgs& a, int threads, int side, cuda
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_STAGES * 3 * NV * C::THREADS * 16);
     });
     if (e != cudaSuccess) return e;
-    const int per_sm = WIDTH == WIDE ? min(3, C::THREADS / threads) : C::PER_SM;
+    // as many CTAs an SM as the registers hold: up to 192 threads four (8192 x 2880 takes 32.7 us, and 41.0 with three)
+    const int per_sm = WIDTH == WIDE ? min(3, C::THREADS / threads) : threads * side <= 192 ? 4 : C::PER_SM;
     const int parts = (int)min64((a.rows + NB_CLUSTER * side - 1) / (NB_CLUSTER * side), min(NB_PARTS, per_sm * sms / NB_CLUSTER));
     const cudaError_t e2 = launch_chained(kernel, dim3(parts * NB_CLUSTER), dim3(threads, side),
                                           (size_t)NB_STAGES * (a.dsum ? 3 : 2) * NV * threads * side * 16, NB_CLUSTER, stream, a);
