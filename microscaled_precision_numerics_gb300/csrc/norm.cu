@@ -224,9 +224,11 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
     if (a.q_row) {                                         // scale rows from a.rows up to a whole tile: zeros
         const int words = (int)((((a.rows + 127) & ~int64_t(127)) - a.rows) * nct);
         const int64_t me = ((int64_t)blockIdx.x * blockDim.y + ty) * blockDim.x + threadIdx.x;
-        if (me < words)
-            for (int i = (int)me; i < words; i += gridDim.x * blockDim.x * blockDim.y)
-                *reinterpret_cast<uint32_t*>(a.s_row + sf_offset(a.rows + i / (int)nct, 4 * (i % (int)nct), nct)) = 0u;
+        const int64_t all = (int64_t)gridDim.x * blockDim.y * blockDim.x;             // (2^32 threads and more, with narrow rows)
+        for (int64_t at = me; at < words; at += all) {
+            const int i = (int)at;
+            *reinterpret_cast<uint32_t*>(a.s_row + sf_offset(a.rows + i / (int)nct, 4 * (i % (int)nct), nct)) = 0u;
+        }
     }
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + ty;
     if (row >= a.rows) return;

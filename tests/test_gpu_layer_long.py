@@ -101,3 +101,19 @@ def test_choice_of_many_tokens(mx):
     assert torch.equal(ids, order.indices[:, :8].int())
     want = torch.softmax(order.values[:, :8].double(), -1)
     assert ((w.double() - want).abs() <= want * 2.0 ** -24 * 80).all()
+
+
+def test_norm_of_more_threads_than_32_bits(mx):
+    """2^27 - 1 narrow rows, 32 threads each: the last rows, and the scale row that fills up the last tile, which is cleared."""
+    rows, cols, tail = (1 << 27) - 1, 32, 127
+    x = torch.randn((1 << 20, cols), device=DEV, dtype=BF).repeat(128, 1)[:rows]
+    w = torch.randn(cols, device=DEV, dtype=BF)
+    out, few = mx.alloc_mxfp8(rows, cols, DEV, colwise=False), mx.alloc_mxfp8(tail, cols, DEV, colwise=False)
+    for o in (out, few):
+        o["s_row"].fill_(255)
+    mx.mx_rmsnorm_mxfp8(x, w, 1e-6, **out)
+    mx.mx_rmsnorm_mxfp8(x[rows - tail:], w, 1e-6, **few)
+    assert torch.equal(out["q_row"][rows - tail:], few["q_row"])
+    assert torch.equal(out["s_row"].view(-1)[-512:], few["s_row"].view(-1))
+    scales = few["s_row"].view(32, 4, 4)                   # row 32 q + r of the tile at [r, q], its columns 1 to 3 padding
+    assert scales[31, 3].eq(0).all() and scales[:, :, 0].eq(0).sum() == 1 and scales[:, :, 1:].eq(0).all()
