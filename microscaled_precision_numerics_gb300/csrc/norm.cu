@@ -57,10 +57,11 @@ __device__ __forceinline__ uint32_t cvt_e4m3_pairs(uint64_t a, uint64_t b) {
     return cvt_e4m3x4(a0, a1, b0, b1);
 }
 
-template <typename T>
+// The sum over the LANES neighbouring lanes of a group.
+template <int LANES = 32, typename T>
 __device__ __forceinline__ T butterfly(T v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
 
@@ -208,6 +209,81 @@ __device__ __forceinline__ int64_t scale_row_offset(int64_t row, int64_t nct) {
 }
 __device__ __forceinline__ int scale_col_offset(int c) { return (c >> 7 << 9) + (c >> 5 & 3); }
 
+// Clears the scale rows from a.rows up to a whole tile; thread `me` of `all`.
+__device__ __forceinline__ void clear_scale_rows(const NormArgs& a, int64_t nct, int64_t me, int64_t all) {
+    const int words = (int)((((a.rows + 127) & ~int64_t(127)) - a.rows) * nct);
+    for (int64_t at = me; at < words; at += all) {         // (2^32 threads and more, with narrow rows)
+        const int i = (int)at;
+        *reinterpret_cast<uint32_t*>(a.s_row + sf_offset(a.rows + i / (int)nct, 4 * (i % (int)nct), nct)) = 0u;
+    }
+}
+
+// Rows of up to 256 elements, without column-wise codes: LANES lanes a row (8, 16 or 32), eight elements each, ROWS rows a lane with
+// their loads side by side, the weights in registers.  The sums are those of a segment whose other lanes hold zeros.  With a residual
+// and codes 262144 x 128 take 38.9 us, 90 % of the measured copy rate (a warp a row with eight rows a CTA: 102.8).
+constexpr int NN_THREADS = 256;
+// CTAs with a row a lane from which on a lane takes four (262144 x 256 71.5 us, and 90.4 with one; below, 65536 x 64 5.6 with one and 6.2
+// with four).
+constexpr int NN_MANY = 2432;
+template <int LANES, int ROWS, bool W32>
+__global__ void __launch_bounds__(NN_THREADS) norm_narrow_kernel(const NormArgs a) {
+    constexpr int SIDE = 32 / LANES;
+    chain_begin();
+    const int lane = threadIdx.x & 31, c = lane % LANES * 8;
+    const int64_t nct = sf_col_tiles(a.cols, 32), thread = (int64_t)blockIdx.x * NN_THREADS + threadIdx.x;
+    if (a.q_row) clear_scale_rows(a, nct, thread, (int64_t)gridDim.x * NN_THREADS);
+    const int64_t first = (thread >> 5) * (SIDE * ROWS) + lane / LANES;
+    auto inside = [&](int i) { return c < a.cols && first + i * SIDE < a.rows; };
+    uint4 h[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        h[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (inside(i)) h[i] = load_global(reinterpret_cast<const uint4*>(a.x + (first + i * SIDE) * a.ldx + c));
+    }
+    if (a.residual) {
+        uint4 r[ROWS];
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (inside(i)) r[i] = load_global(reinterpret_cast<const uint4*>(a.residual + (first + i * SIDE) * a.ldr + c));
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (inside(i)) {
+                h[i] = add8(h[i], r[i]);
+                if (a.sum) *reinterpret_cast<uint4*>(a.sum + (first + i * SIDE) * a.lds + c) = h[i];
+            }
+    }
+    Pairs w = {};
+    if (c < a.cols) weights8<W32>(a.w, c, w);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t row = first + i * SIDE;
+        const float ss = butterfly<LANES>(squares8(h[i]));
+        RowNorm n = norm_of(ss, a.inv_cols, a.eps);
+        const bool fine = fp32_holds(ss, a.eps);
+        if (__any_sync(0xFFFFFFFFu, !fine)) {
+            const double wide = butterfly<LANES>(squares8_wide(h[i]));
+            if (!fine) n = norm_of_wide(wide, a.cols, a.eps);
+        }
+        uint4 y = make_uint4(0u, 0u, 0u, 0u);
+        if (inside(i)) {
+            Pairs f;
+            unpack8(h[i], f);
+            normed8(f, w, n);
+            y = pack8(f);
+            if (a.y) *reinterpret_cast<uint4*>(a.y + row * a.ldy + c) = y;
+        }
+        if (a.q_row) {
+            uint32_t s = quantize_row8(y, a.q_row + row * a.cols + c, inside(i));
+            // the scales of 128 columns (0 beyond the row), a word
+            const uint32_t s1 = __shfl_down_sync(0xFFFFFFFFu, s, 4), s2 = __shfl_down_sync(0xFFFFFFFFu, s, 8), s3 = __shfl_down_sync(0xFFFFFFFFu, s, 12);
+            s |= s1 << 8;
+            if (LANES > 8) s |= s2 << 16 | s3 << 24;
+            if (c % 128 == 0 && c < 128 * nct && row < a.rows)
+                *reinterpret_cast<uint32_t*>(a.s_row + scale_row_offset(row, nct) + scale_col_offset(c)) = s;
+        }
+    }
+}
+
 // Without column-wise codes: one row a group of blockDim.x threads, blockDim.y rows a CTA; NV vectors of eight elements a thread.
 // At most four a thread and 64 registers: with eight, one CTA an SM ran through 32 KB of straight-line code for every row
 // (1003 x 14336 took 54 us, now 17: three turns of two CTAs an SM, each a row's loads, meeting and stores after one another).
@@ -221,15 +297,8 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, ty = threadIdx.y;
     const int nseg = (a.cols + SEG - 1) / SEG;
     const int64_t nct = sf_col_tiles(a.cols, 32);
-    if (a.q_row) {                                         // scale rows from a.rows up to a whole tile: zeros
-        const int words = (int)((((a.rows + 127) & ~int64_t(127)) - a.rows) * nct);
-        const int64_t me = ((int64_t)blockIdx.x * blockDim.y + ty) * blockDim.x + threadIdx.x;
-        const int64_t all = (int64_t)gridDim.x * blockDim.y * blockDim.x;             // (2^32 threads and more, with narrow rows)
-        for (int64_t at = me; at < words; at += all) {
-            const int i = (int)at;
-            *reinterpret_cast<uint32_t*>(a.s_row + sf_offset(a.rows + i / (int)nct, 4 * (i % (int)nct), nct)) = 0u;
-        }
-    }
+    if (a.q_row)
+        clear_scale_rows(a, nct, ((int64_t)blockIdx.x * blockDim.y + ty) * blockDim.x + threadIdx.x, (int64_t)gridDim.x * blockDim.y * blockDim.x);
     const int64_t row = (int64_t)blockIdx.x * blockDim.y + ty;
     if (row >= a.rows) return;
     const int c0 = (warp * 32 + lane) * 8, step = warps * SEG;
@@ -780,8 +849,21 @@ int row_threads(int64_t cols, int threads, int& nv, int least = 1) {
     return (int)(((vectors + nv - 1) / nv + 31) / 32 * 32);
 }
 
+template <int LANES, bool W32>
+cudaError_t norm_narrow(const NormArgs& a, cudaStream_t stream) {
+    auto go = [&](auto kernel, int rows_a_cta) {
+        return launch_chained(kernel, dim3((unsigned)((a.rows + rows_a_cta - 1) / rows_a_cta)), dim3(NN_THREADS), 0, 0, stream, a);
+    };
+    constexpr int side = NN_THREADS / LANES;
+    if (a.rows >= (int64_t)NN_MANY * side) return go(norm_narrow_kernel<LANES, 4, W32>, 4 * side);
+    return go(norm_narrow_kernel<LANES, 1, W32>, side);
+}
+
 template <bool W32>
 cudaError_t norm_rows(const NormArgs& a, cudaStream_t stream) {
+    if (a.cols <= 64) return norm_narrow<8, W32>(a, stream);
+    if (a.cols <= 128) return norm_narrow<16, W32>(a, stream);
+    if (a.cols <= 256) return norm_narrow<32, W32>(a, stream);
     // many rows: four vectors a thread, so that more bytes are on their way for every row's meeting of its warps; few rows: as
     // many threads a row as have work
     const bool many = a.rows >= 512;

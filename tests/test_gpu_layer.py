@@ -163,6 +163,34 @@ def test_norm_zero_rows_and_rows_that_are_not_finite(mx):
     assert torch.isnan(y).all()
 
 
+@pytest.mark.parametrize("rows,cols", [(61, 8), (100, 64), (1001, 136), (77901, 40), (78001, 64), (39000, 96), (39001, 128), (19501, 224), (19499, 256)])
+def test_norm_of_narrow_rows(mx, rows, cols):
+    """Rows that share a warp: ordinary ones, ones that FP32 does not hold and ones that are not finite side by side."""
+    x, w = rand(13, rows, cols), rand(14, cols, scale=0.2).float() + 1.0
+    x[1::7] *= 2.0 ** 70                                   # (exact: a power of two)
+    x[2::7] *= 2.0 ** -80
+    x[3::7, cols - 1], x[5::14, 3] = float("inf"), float("nan")
+    fine = torch.ones(rows, dtype=torch.bool, device=DEV)
+    fine[3::7] = fine[5::14] = False
+    codes = cols % 32 == 0
+    _, y, out = run_norm(mx, x, w, 0.0, row=codes)
+    _, _, want = ref.norm(host(x[fine]), host(w), 0.0)
+    within(y[fine], want, y_bound(want))
+    assert torch.isnan(y[5::14]).all() and torch.isnan(y[3::7, -1]).all() and not y[3::7, :-1].any()
+    if codes:
+        same(out, codes_of(mx, y, True, False))
+    # with a residual, in views with other strides, and column-wise codes too: the same rows
+    half = x * 0.5
+    ys, ss = strided(torch.zeros_like(x)), strided(torch.zeros_like(x))
+    mx.mx_rmsnorm_mxfp8(strided(half), w, 0.0, residual=strided(half, extra=40), sum_out=ss, y=ys)
+    assert torch.equal(ss.nan_to_num(7.0), x.nan_to_num(7.0)) and torch.equal(ys.nan_to_num(7.0), y.nan_to_num(7.0))
+    around = ys.as_strided((rows, cols + 24), (cols + 24, 1), ys.storage_offset() - 8)
+    assert (around[:, :8] == 7.0).all() and (around[:, cols + 8:] == 7.0).all()
+    some = rows // 32 * 32
+    _, both, _ = run_norm(mx, x[:some], w, 0.0, row=codes, col=True)
+    assert torch.equal(both.nan_to_num(7.0), y[:some].nan_to_num(7.0))
+
+
 BACKWARD_SIZES = [(1, 8), (1, 2048), (5, 96), (33, 1000), (700, 256), (3, 8200), (2, 16384), (311, 2048), (2000, 512), (4001, 128), (5, 5120),
                   (470, 4104), (9, 8192), (1900, 1024), (3700, 72)]
 
