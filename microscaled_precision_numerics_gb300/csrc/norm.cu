@@ -604,9 +604,9 @@ struct NormBackwardArgs {
     float *dw, *partial;
 };
 
-// Three forms by the row's width.  NARROW, up to 1024: several rows side by side in CTAs of 256 threads, three an SM, weights in
-// registers (65536 x 128 takes 26 us, and 102 with a row a CTA).  MIDDLE, up to 4096: one row of one or two vectors a thread, otherwise
-// as narrow ones.  WIDE: two vectors a thread, up to 1024 threads of 64 registers.
+// Three forms by the row's width (and one of its own, below, up to 256).  NARROW, up to 1024: several rows side by side in CTAs of 256
+// threads, three an SM, weights in registers (32768 x 512 takes 26 us, and 59 with a row a CTA).  MIDDLE, up to 4096: one row of one or
+// two vectors a thread, otherwise as narrow ones.  WIDE: two vectors a thread, up to 1024 threads of 64 registers.
 enum BackwardWidth { NARROW, MIDDLE, WIDE };
 template <int WIDTH>
 struct BackwardCfg {
@@ -617,7 +617,7 @@ struct BackwardCfg {
 constexpr int NB_CLUSTER = 2;                              // wider clusters leave SMs idle (four: 72 us where two take 57)
 constexpr int NB_PARTS = 304;                              // most partial sums of a column: pairs of four CTAs an SM
 constexpr int NB_STAGES = 2;
-constexpr int NB_ROWS = 8;                                 // most rows side by side
+constexpr int NB_ROWS = 4;                                 // most rows side by side
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
@@ -626,6 +626,56 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int LEFT>
 __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" :: "n"(LEFT) : "memory");
+}
+
+// A lane's sums of h^2 and dn h over eight elements, even and odd ones apart as in the forward's sums.
+__device__ __forceinline__ void products8(const float (&x)[8], const float (&d)[8], const float (&w)[8], float& squares, float& inner) {
+    float s[2] = {0.0f, 0.0f}, c[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        s[j & 1] = __fmaf_rn(x[j], x[j], s[j & 1]);
+        c[j & 1] = __fmaf_rn(__fmul_rn(d[j], w[j]), x[j], c[j & 1]);
+    }
+    squares = __fadd_rn(s[0], s[1]);
+    inner = __fadd_rn(c[0], c[1]);
+}
+__device__ __forceinline__ double inner8_wide(const float (&x)[8], const float (&d)[8], const float (&w)[8]) {
+    double s = 0.0;
+    for (int j = 0; j < 8; ++j) s = __fma_rn((double)d[j] * (double)w[j], (double)x[j], s);
+    return s;
+}
+// Whether FP32 held both sums of a row: dn h likewise neither too large, nor so small that subnormals would decide (where eps
+// does not).
+__device__ __forceinline__ bool fp32_holds_both(float ss, float cc, float eps) {
+    return fp32_holds(ss, eps) && fabsf(cc) <= FLT_MAX && (fabsf(cc) >= 7.88860905e-31f || eps >= 9.09494702e-13f);
+}
+// A factor far from 1 is split as a slow row's is, so that dy r keeps its bits where dy n has them.
+__device__ __forceinline__ void split_far(RowNorm& n) {
+    if (n.r < 9.53674316e-7f || n.r > 1048576.0f) {        // 2^-20, 2^20; neither for a slow row
+        n.p = __uint_as_float(__float_as_uint(n.r) & 0x7F800000u);
+        n.r = __uint_as_float((__float_as_uint(n.r) & 0x007FFFFFu) | 0x3F800000u);
+    }
+}
+// With x = h p: o = p (r dy w - x r^2 mean), dw += (r dy) x.  SCALED false: p is 1 (its products would take a tenth of the
+// instructions).
+template <bool SCALED>
+__device__ __forceinline__ void gradient8(float (&x)[8], float (&d)[8], const float (&w)[8], const RowNorm& n, float by_x, float (&dw)[8],
+                                          float (&o)[8]) {
+    if (SCALED)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], n.p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        d[j] = __fmul_rn(d[j], n.r);
+        o[j] = __fmaf_rn(x[j], by_x, __fmul_rn(d[j], w[j]));
+        dw[j] = __fmaf_rn(d[j], x[j], dw[j]);
+    }
+    if (SCALED)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(o[j], n.p);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
 // A thread fetches its own vectors of the next row into shared memory (nobody else reads them there, so no barrier guards
@@ -701,14 +751,7 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
             unpack8(fetched(turn, 1, i), x);
             unpack8(fetched(turn, 0, i), d);
             weights(i, w);
-            float s[2] = {0.0f, 0.0f}, inner[2] = {0.0f, 0.0f};           // even and odd elements, as in the forward's sums
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s[j & 1] = __fmaf_rn(x[j], x[j], s[j & 1]);
-                inner[j & 1] = __fmaf_rn(__fmul_rn(d[j], w[j]), x[j], inner[j & 1]);
-            }
-            parts[i] = __fadd_rn(s[0], s[1]);
-            parts[NV + i] = __fadd_rn(inner[0], inner[1]);
+            products8(x, d, w, parts[i], parts[NV + i]);
         }
         float* sm_s = reinterpret_cast<float*>(sums_of(turn, 0));
         float* sm_c = reinterpret_cast<float*>(sums_of(turn, 1));
@@ -725,8 +768,7 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
         const float ss = __shfl_sync(0xFFFFFFFFu, both, 0), cc = __shfl_sync(0xFFFFFFFFu, both, 16);
         RowNorm n = norm_of(ss, a.inv_cols, a.eps);
         float mean = __fmul_rn(__fmul_rn(cc, a.inv_cols), n.r);          // mean(dn n)
-        // the products dn h likewise: too large, or so small that subnormals would decide (where eps does not)
-        if (!fp32_holds(ss, a.eps) || !(fabsf(cc) <= FLT_MAX) || (fabsf(cc) < 7.88860905e-31f && a.eps < 9.09494702e-13f)) {
+        if (!fp32_holds_both(ss, cc, a.eps)) {
             meet();                                                      // the FP32 sums have been read
 #pragma unroll 1
             for (int i = 0; i < NV; ++i) {
@@ -737,7 +779,7 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
                     unpack8(h, x);
                     unpack8(fetched(turn, 0, i), d);
                     weights8<W32>(a.w, c0 + i * step, w);
-                    for (int j = 0; j < 8; ++j) inner = __fma_rn((double)d[j] * (double)w[j], (double)x[j], inner);
+                    inner = inner8_wide(x, d, w);
                     squares = squares8_wide(h);
                 }
                 squares = butterfly(squares);
@@ -751,14 +793,8 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
             n = norm_of_wide(segments_sum(sums_of(turn, 0), nseg), a.cols, a.eps);
             mean = (float)(segments_sum(sums_of(turn, 1), nseg) / a.cols * n.p * n.r);
         }
-        // a factor far from 1 is split as a slow row's is, so that dy r keeps its bits where dy n has them
-        if (n.r < 9.53674316e-7f || n.r > 1048576.0f) {                  // 2^-20, 2^20; neither for a slow row
-            n.p = __uint_as_float(__float_as_uint(n.r) & 0x7F800000u);
-            n.r = __uint_as_float((__float_as_uint(n.r) & 0x007FFFFFu) | 0x3F800000u);
-        }
-        // with x = h p: dx = p (r dy w - x r^2 mean) + dsum, dw += (r dy) x
+        split_far(n);
         const float by_x = -__fmul_rn(__fmul_rn(mean, n.r), n.r);
-        // in two forms, as the products with p would take a tenth of the instructions where it is 1
         auto emit = [&](auto scaled) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -767,25 +803,13 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
                 unpack8(fetched(turn, 1, i), x);
                 unpack8(fetched(turn, 0, i), d);
                 weights(i, w);
-                if constexpr (decltype(scaled)::value)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], n.p);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    d[j] = __fmul_rn(d[j], n.r);
-                    o[j] = __fmaf_rn(x[j], by_x, __fmul_rn(d[j], w[j]));
-                    dw[i][j] = __fmaf_rn(d[j], x[j], dw[i][j]);
-                }
-                if constexpr (decltype(scaled)::value)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(o[j], n.p);
+                gradient8<decltype(scaled)::value>(x, d, w, n, by_x, dw[i], o);
                 if (a.dsum) {
                     unpack8(fetched(turn, 2, i), x);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[j] = __fadd_rn(o[j], x[j]);
                 }
-                *reinterpret_cast<uint4*>(dx + i * step) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                                                                      pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+                *reinterpret_cast<uint4*>(dx + i * step) = pack8(o);
             }
         };
         if (n.p != 1.0f) emit(std::true_type{});
@@ -817,6 +841,118 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
         *reinterpret_cast<ulonglong2*>(a.partial + (int64_t)(blockIdx.x / peers) * a.cols + c) = make_ulonglong2(s0, s1);
     }
     cluster_sync();                                        // nobody leaves while the others read its sums
+}
+
+// Rows of up to 256 elements: LANES lanes a row (8, 16 or 32).  The warps walk the rows, each lane with a ring of its own vectors in
+// shared memory, and a CTA adds its sums of dw up there at the end.  262144 x 128 with dsum take 39.9 us, the measured copy rate (89.5 in
+// NARROW's form); two CTAs of 256 threads an SM: with 384 (80 registers) 42.4, with 512 (64, which spill) 52.3.
+constexpr int NBN_THREADS = 256, NBN_STAGES = 4;
+
+// p, r and mean(dn n) of the warp's rows, summed in FP64 (out of line, so that it costs the others no registers).
+template <int LANES, bool W32>
+__device__ __noinline__ float3 slow_narrow_row(uint4 h, uint4 dy, const void* weight, int c, int cols, float eps) {
+    float x[8], d[8], w[8] = {};
+    unpack8(h, x);
+    unpack8(dy, d);
+    if (c < cols) weights8<W32>(weight, c, w);
+    const double squares = butterfly<LANES>(squares8_wide(h)), inner = butterfly<LANES>(inner8_wide(x, d, w));
+    const RowNorm n = norm_of_wide(squares, cols, eps);
+    return make_float3(n.p, n.r, (float)(inner / cols * n.p * n.r));
+}
+
+template <int LANES, bool W32>
+__global__ void __launch_bounds__(NBN_THREADS, 2) norm_backward_narrow_kernel(const NormBackwardArgs a) {
+    constexpr int SIDE = 32 / LANES, WARPS = NBN_THREADS / 32;
+    constexpr uint32_t TENSOR = NBN_THREADS * 16;
+    extern __shared__ __align__(16) uint8_t sm_rows[];     // [stage][dy, h, dsum][thread] of 16 bytes; then [warp][column] sums
+    chain_begin();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % LANES * 8;
+    const uint32_t stage_bytes = (a.dsum ? 3 : 2) * TENSOR, sm0 = (uint32_t)__cvta_generic_to_shared(sm_rows) + threadIdx.x * 16;
+    const int64_t next = (int64_t)gridDim.x * (WARPS * SIDE), first = ((int64_t)blockIdx.x * WARPS + warp) * SIDE + lane / LANES;
+    // the group's first row decides for the warp (its lanes stay together), the lane's own whether it has one
+    const int64_t turns = first - lane / LANES < a.rows ? (a.rows - (first - lane / LANES) + next - 1) / next : 0;
+    auto inside = [&](int64_t t) { return c < a.cols && first + t * next < a.rows; };
+    const uint16_t *dy = a.dy + first * a.lddy + c, *from_h = a.h + first * a.ldh + c, *dsum = a.dsum + first * a.ldds + c;
+    uint16_t* dx = a.dx + first * a.lddx + c;
+    auto fetch = [&](int64_t t, uint32_t stage) {          // turns in order
+        if (inside(t)) {
+            const uint32_t at = sm0 + stage * stage_bytes;
+            copy16(at, dy);
+            copy16(at + TENSOR, from_h);
+            if (a.dsum) copy16(at + 2 * TENSOR, dsum);
+            dy += next * a.lddy;
+            from_h += next * a.ldh;
+            dsum += next * a.ldds;
+        }
+        copies_commit();                                   // an empty group where there is no row, so that the count goes on
+    };
+#pragma unroll
+    for (int t = 0; t < NBN_STAGES - 1; ++t) fetch(t, t);
+    float w[8] = {}, dw[8] = {};
+    if (c < a.cols) weights8<W32>(a.w, c, w);
+    uint32_t stage = 0;
+    for (int64_t t = 0; t < turns; ++t) {
+        fetch(t + NBN_STAGES - 1, stage == 0 ? NBN_STAGES - 1 : stage - 1);           // into the stage that this lane read in the turn before
+        copies_wait<NBN_STAGES - 1>();
+        auto fetched = [&](int which) { return *reinterpret_cast<const uint4*>(sm_rows + stage * stage_bytes + which * TENSOR + threadIdx.x * 16); };
+        const bool in = inside(t);
+        uint4 h = make_uint4(0u, 0u, 0u, 0u), g = h;
+        if (in) {
+            g = fetched(0);
+            h = fetched(1);
+        }
+        float x[8], d[8], ss, cc;
+        unpack8(h, x);
+        unpack8(g, d);
+        products8(x, d, w, ss, cc);
+        ss = butterfly<LANES>(ss);
+        cc = butterfly<LANES>(cc);
+        RowNorm n = norm_of(ss, a.inv_cols, a.eps);
+        float mean = __fmul_rn(__fmul_rn(cc, a.inv_cols), n.r);          // mean(dn n)
+        const bool fine = fp32_holds_both(ss, cc, a.eps);
+        if (__any_sync(0xFFFFFFFFu, !fine)) {
+            const float3 wide = slow_narrow_row<LANES, W32>(h, g, a.w, c, a.cols, a.eps);
+            if (!fine) {
+                n = RowNorm{wide.x, wide.y};
+                mean = wide.z;
+            }
+        }
+        split_far(n);
+        if (in) {
+            const float by_x = -__fmul_rn(__fmul_rn(mean, n.r), n.r);
+            float o[8];
+            unpack8(h, x);
+            unpack8(g, d);
+            if (n.p != 1.0f) gradient8<true>(x, d, w, n, by_x, dw, o);
+            else gradient8<false>(x, d, w, n, by_x, dw, o);
+            if (a.dsum) {
+                unpack8(fetched(2), x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = __fadd_rn(o[j], x[j]);
+            }
+            *reinterpret_cast<uint4*>(dx) = pack8(o);
+        }
+        dx += next * a.lddx;
+        stage = stage == NBN_STAGES - 1 ? 0 : stage + 1;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int o = 16; o >= LANES; o >>= 1) dw[j] += __shfl_xor_sync(0xFFFFFFFFu, dw[j], o);
+    float* sm_dw = reinterpret_cast<float*>(sm_rows);      // (the ring's copies have all arrived, but other warps may still read theirs)
+    __syncthreads();
+    if (lane < LANES) {
+        float4* at = reinterpret_cast<float4*>(sm_dw + warp * (LANES * 8) + c);
+        at[0] = make_float4(dw[0], dw[1], dw[2], dw[3]);
+        at[1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
+    }
+    __syncthreads();
+    for (int at = threadIdx.x; at < a.cols; at += NBN_THREADS) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < WARPS; ++k) s += sm_dw[k * (LANES * 8) + at];
+        a.partial[(int64_t)blockIdx.x * a.cols + at] = s;
+    }
 }
 
 // dw[c] = the sum of `parts` partial sums: 32 columns a CTA, 32 warps a share of the parts each.
@@ -894,6 +1030,11 @@ cudaError_t norm_tile(const NormArgs& a, cudaStream_t stream) {
     return launch_chained(kernel, dim3((unsigned)(a.rows / TILE_ROWS) * cluster), dim3(C::THREADS), C::SMEM, cluster, stream, a);
 }
 
+cudaError_t add_parts(const NormBackwardArgs& a, int parts, cudaStream_t stream) {
+    return launch_chained(norm_dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(32 * ND_WARPS), 0, 0, stream,
+                          static_cast<const float*>(a.partial), parts, a.cols, a.dw);
+}
+
 template <int WIDTH, int NV, bool W32, bool FULL>
 cudaError_t norm_backward(const NormBackwardArgs& a, int threads, int side, cudaStream_t stream) {
     using C = BackwardCfg<WIDTH>;
@@ -910,13 +1051,31 @@ cudaError_t norm_backward(const NormBackwardArgs& a, int threads, int side, cuda
     const int parts = (int)min64((a.rows + NB_CLUSTER * side - 1) / (NB_CLUSTER * side), min(NB_PARTS, per_sm * sms / NB_CLUSTER));
     const cudaError_t e2 = launch_chained(kernel, dim3(parts * NB_CLUSTER), dim3(threads, side),
                                           (size_t)NB_STAGES * (a.dsum ? 3 : 2) * NV * threads * side * 16, NB_CLUSTER, stream, a);
-    if (e2 != cudaSuccess) return e2;
-    return launch_chained(norm_dweight_kernel, dim3((unsigned)((a.cols + 31) / 32)), dim3(32 * ND_WARPS), 0, 0, stream,
-                          static_cast<const float*>(a.partial), parts, a.cols, a.dw);
+    return e2 != cudaSuccess ? e2 : add_parts(a, parts, stream);
+}
+
+template <int LANES, bool W32>
+cudaError_t norm_backward_narrow(const NormBackwardArgs& a, cudaStream_t stream) {
+    auto kernel = norm_backward_narrow_kernel<LANES, W32>;
+    constexpr int tensor = NBN_STAGES * NBN_THREADS * 16;
+    static PerDevice pd;
+    int sms = 0;
+    const cudaError_t e = per_device_once(pd, sms, [kernel](int& n) {
+        n = device_sm_count();
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * tensor);
+    });
+    if (e != cudaSuccess) return e;
+    constexpr int rows_a_cta = NBN_THREADS / LANES;
+    const int parts = (int)min64((a.rows + rows_a_cta - 1) / rows_a_cta, min(NB_PARTS, 2 * sms));
+    const cudaError_t e2 = launch_chained(kernel, dim3(parts), dim3(NBN_THREADS), (size_t)(a.dsum ? 3 : 2) * tensor, 0, stream, a);
+    return e2 != cudaSuccess ? e2 : add_parts(a, parts, stream);
 }
 
 template <bool W32>
 cudaError_t norm_backward(const NormBackwardArgs& a, cudaStream_t stream) {
+    if (a.cols <= 64) return norm_backward_narrow<8, W32>(a, stream);
+    if (a.cols <= 128) return norm_backward_narrow<16, W32>(a, stream);
+    if (a.cols <= 256) return norm_backward_narrow<32, W32>(a, stream);
     int nv;
     int threads = row_threads(a.cols, 256, nv);
     if (nv > 2) threads = row_threads(a.cols, 1024, nv, 2);

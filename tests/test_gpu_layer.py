@@ -216,6 +216,30 @@ def test_norm_backward(mx, rows, cols, weight, with_dsum):
         assert torch.equal(a[alias], dx) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("rows,cols", [(9001, 64), (77901, 40), (39001, 128), (40000, 72), (19501, 224), (40011, 256)])
+def test_norm_backward_of_narrow_rows(mx, rows, cols):
+    """Many rows to a warp, ordinary ones and ones that FP32 does not hold side by side, in views with other strides."""
+    h, dy, dsum = rand(30, rows, cols), rand(31, rows, cols, scale=0.01), rand(32, rows, cols, scale=0.01)
+    w = rand(33, cols, scale=0.2).float() + 1.0
+    h[1::7] *= 2.0 ** 70                                   # (exact: powers of two)
+    h[2::7] *= 2.0 ** -80
+    dy[3::5] *= 2.0 ** -40
+    dx, dw = torch.empty_like(h), torch.full((cols,), 9.0, device=DEV)
+    ws = torch.full((mx.rmsnorm_workspace_bytes(rows, cols),), 255, dtype=U8, device=DEV)
+    mx.mx_rmsnorm_backward(dy, h, w, 0.0, dx, dw, ws, dsum=dsum)
+    want, wdw, bound, size = ref.norm_backward(host(dy), host(h), host(w), 0.0, host(dsum))
+    within(dx, want, bound)
+    within(dw, wdw, (rows + 32) * ref.EPS32 * size + 1e-30)
+    views, dw2 = [strided(t, extra) for t, extra in ((dy, 24), (h, 40), (dsum, 32), (torch.zeros_like(h), 24))], torch.empty_like(dw)
+    mx.mx_rmsnorm_backward(views[0], views[1], w, 0.0, views[3], dw2, ws, dsum=views[2])
+    assert torch.equal(views[3], dx) and torch.equal(dw, dw2)
+    around = views[3].as_strided((rows, cols + 24), (cols + 24, 1), views[3].storage_offset() - 8)
+    assert (around[:, :8] == 7.0).all() and (around[:, cols + 8:] == 7.0).all()
+    few = torch.empty((37, cols), dtype=BF, device=DEV)
+    mx.mx_rmsnorm_backward(dy[-37:], h[-37:], w, 0.0, few, dw2, ws, dsum=dsum[-37:])
+    assert torch.equal(few, dx[-37:])
+
+
 def test_norm_backward_against_differences(mx):
     """The directional derivative of sum(dy * y) by central differences in 64 bits.  The step leaves an error of its square."""
     h, dy, w = rand(25, 9, 352), rand(26, 9, 352), rand(27, 352).float() + 1.0
