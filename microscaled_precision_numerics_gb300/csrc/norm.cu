@@ -209,12 +209,21 @@ __device__ __forceinline__ int64_t scale_row_offset(int64_t row, int64_t nct) {
 }
 __device__ __forceinline__ int scale_col_offset(int c) { return (c >> 7 << 9) + (c >> 5 & 3); }
 
-// Clears the scale rows from a.rows up to a whole tile; thread `me` of `all`.
+// Clears the scale rows from a.rows up to a whole tile; thread `me` of `all`.  16 bytes hold the rows l, l + 32, l + 64 and l + 96 of a
+// tile (one row of 11840 takes 4.3 us, and 10.5 with a word at a time).
 __device__ __forceinline__ void clear_scale_rows(const NormArgs& a, int64_t nct, int64_t me, int64_t all) {
-    const int words = (int)((((a.rows + 127) & ~int64_t(127)) - a.rows) * nct);
-    for (int64_t at = me; at < words; at += all) {         // (2^32 threads and more, with narrow rows)
-        const int i = (int)at;
-        *reinterpret_cast<uint32_t*>(a.s_row + sf_offset(a.rows + i / (int)nct, 4 * (i % (int)nct), nct)) = 0u;
+    const int used = (int)(a.rows & 127);
+    if (used == 0) return;
+    for (int64_t i = me; i < nct * 32; i += all) {         // (in 64 bits: narrow rows take 2^32 threads and more)
+        const int l = (int)i & 31;
+        uint32_t* at = reinterpret_cast<uint32_t*>(a.s_row + ((a.rows >> 7) * nct + (i >> 5)) * 512 + l * 16);
+        if (l >= used) {
+            *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+                if (l + 32 * q >= used) at[q] = 0u;
+        }
     }
 }
 
