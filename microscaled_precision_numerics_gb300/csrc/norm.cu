@@ -613,15 +613,12 @@ struct NormBackwardArgs {
     float *dw, *partial;
 };
 
-// Three forms by the row's width (and one of its own, below, up to 256).  NARROW, up to 1024: several rows side by side in CTAs of 256
-// threads, three an SM, weights in registers (32768 x 512 takes 26 us, and 59 with a row a CTA).  MIDDLE, up to 4096: one row of one or
-// two vectors a thread, otherwise as narrow ones.  WIDE: two vectors a thread, up to 1024 threads of 64 registers.
-enum BackwardWidth { NARROW, MIDDLE, WIDE };
-template <int WIDTH>
-struct BackwardCfg {
-    static constexpr int THREADS = WIDTH == WIDE ? 1024 : 256;
-    static constexpr int PER_SM = WIDTH == WIDE ? 1 : 3;   // of full CTAs
-    static constexpr bool KEEP_W = WIDTH != WIDE;
+// A form of the kernel: CTAs of up to THREADS threads, PER_SM of those an SM (which sets the registers of a thread), NV vectors of eight
+// elements a thread; SIDE: several rows side by side in a CTA.  Every form keeps the weights in registers.
+template <int THREADS_, int PER_SM_, int NV_, bool SIDE_ = false>
+struct BackwardForm {
+    static constexpr int THREADS = THREADS_, PER_SM = PER_SM_, NV = NV_;
+    static constexpr bool SIDE = SIDE_;
 };
 constexpr int NB_CLUSTER = 2;                              // wider clusters leave SMs idle (four: 72 us where two take 57)
 constexpr int NB_PARTS = 304;                              // most partial sums of a column: pairs of four CTAs an SM
@@ -691,17 +688,18 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // them) while it works on this one: the loads wait in no registers, and a row's sums do not hold up the next row's.
 // FULL: every vector of every thread lies inside the row (its width is the threads' vectors exactly), which
 // spares the comparisons: 2 of 45 us for 8192 x 4096.
-template <int WIDTH, int NV, bool W32, bool FULL>
-__global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH>::PER_SM) norm_backward_kernel(const NormBackwardArgs a) {
+template <typename F, bool W32, bool FULL>
+__global__ void __launch_bounds__(F::THREADS, F::PER_SM) norm_backward_kernel(const NormBackwardArgs a) {
+    constexpr int NV = F::NV;
     extern __shared__ __align__(16) uint8_t sm_rows[];     // [stage][dy, h, dsum][NV][thread] of 16 bytes
     __shared__ double sm_all[4 * MAX_SEGS];                // [row side by side][turn][sum][segment]
     chain_begin();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, side = WIDTH == NARROW ? (int)blockDim.y : 1;
-    const int ty = WIDTH == NARROW ? (int)threadIdx.y : 0, tid = ty * blockDim.x + threadIdx.x, threads = blockDim.x * side;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, side = F::SIDE ? (int)blockDim.y : 1;
+    const int ty = F::SIDE ? (int)threadIdx.y : 0, tid = ty * blockDim.x + threadIdx.x, threads = blockDim.x * side;
     // rows side by side have at most MAX_SEGS / NB_ROWS segments each
-    constexpr int sums = WIDTH == NARROW ? MAX_SEGS / NB_ROWS : MAX_SEGS;
+    constexpr int sums = F::SIDE ? MAX_SEGS / NB_ROWS : MAX_SEGS;
     auto meet = [&]() {                                    // of the threads of a row
-        if constexpr (WIDTH == NARROW) row_sync(ty, blockDim.x);
+        if constexpr (F::SIDE) row_sync(ty, blockDim.x);
         else __syncthreads();
     };
     auto sums_of = [&](uint32_t turn, int which) { return sm_all + (ty * 4 + turn * 2 + which) * sums; };
@@ -733,20 +731,10 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
         return *reinterpret_cast<const uint4*>(sm_rows + stage * stage_bytes + which * tensor + i * vector + tid * 16);
     };
     fetch(first, 0);
-    constexpr bool KEEP_W = BackwardCfg<WIDTH>::KEEP_W;
-    float dw[NV][8] = {}, kept[KEEP_W ? NV : 1][8];
-    if (KEEP_W)
+    float dw[NV][8] = {}, weight[NV][8];
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (!outside(i)) weights8<W32>(a.w, c0 + i * step, kept[i]);
-    auto weights = [&](int i, float (&w)[8]) {
-        if (KEEP_W) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = kept[KEEP_W ? i : 0][j];
-        } else {
-            weights8<W32>(a.w, c0 + i * step, w);
-        }
-    };
+    for (int i = 0; i < NV; ++i)
+        if (!outside(i)) weights8<W32>(a.w, c0 + i * step, weight[i]);
     uint32_t turn = 0;
     for (int64_t row = first; row < a.rows; row += next, turn ^= 1) {
         fetch(row + next, turn ^ 1);                  // into the stage that this thread read in the turn before
@@ -756,11 +744,10 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
         for (int i = 0; i < NV; ++i) {
             parts[i] = parts[NV + i] = 0.0f;
             if (outside(i)) continue;
-            float x[8], d[8], w[8];
+            float x[8], d[8];
             unpack8(fetched(turn, 1, i), x);
             unpack8(fetched(turn, 0, i), d);
-            weights(i, w);
-            products8(x, d, w, parts[i], parts[NV + i]);
+            products8(x, d, weight[i], parts[i], parts[NV + i]);
         }
         float* sm_s = reinterpret_cast<float*>(sums_of(turn, 0));
         float* sm_c = reinterpret_cast<float*>(sums_of(turn, 1));
@@ -808,11 +795,10 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 if (outside(i)) continue;
-                float x[8], d[8], w[8], o[8];
+                float x[8], d[8], o[8];
                 unpack8(fetched(turn, 1, i), x);
                 unpack8(fetched(turn, 0, i), d);
-                weights(i, w);
-                gradient8<decltype(scaled)::value>(x, d, w, n, by_x, dw[i], o);
+                gradient8<decltype(scaled)::value>(x, d, weight[i], n, by_x, dw[i], o);
                 if (a.dsum) {
                     unpack8(fetched(turn, 2, i), x);
 #pragma unroll
@@ -854,7 +840,7 @@ __global__ void __launch_bounds__(BackwardCfg<WIDTH>::THREADS, BackwardCfg<WIDTH
 
 // Rows of up to 256 elements: LANES lanes a row (8, 16 or 32).  The warps walk the rows, each lane with a ring of its own vectors in
 // shared memory, and a CTA adds its sums of dw up there at the end.  262144 x 128 with dsum take 39.9 us, the measured copy rate (89.5 in
-// NARROW's form); two CTAs of 256 threads an SM: with 384 (80 registers) 42.4, with 512 (64, which spill) 52.3.
+// the form for wider rows); two CTAs of 256 threads an SM: with 384 (80 registers) 42.4, with 512 (64, which spill) 52.3.
 constexpr int NBN_THREADS = 256, NBN_STAGES = 4;
 
 // p, r and mean(dn n) of the warp's rows, summed in FP64 (out of line, so that it costs the others no registers).
@@ -986,10 +972,10 @@ __global__ void __launch_bounds__(32 * ND_WARPS) norm_dweight_kernel(const float
     if (lane == 0 && blockIdx.x * 32 + warp < cols) dw[blockIdx.x * 32 + warp] = s;
 }
 
-// Vectors of eight elements a thread (`least` or a power of two times it) such that at most `threads` take a row, and whole warps of threads.
-int row_threads(int64_t cols, int threads, int& nv, int least = 1) {
+// Vectors of eight elements a thread (a power of two) such that at most `threads` take a row, and whole warps of threads.
+int row_threads(int64_t cols, int threads, int& nv) {
     const int64_t vectors = (cols + 7) / 8;
-    nv = least;
+    nv = 1;
     while (nv * threads < vectors) nv *= 2;
     return (int)(((vectors + nv - 1) / nv + 31) / 32 * 32);
 }
@@ -1044,22 +1030,21 @@ cudaError_t add_parts(const NormBackwardArgs& a, int parts, cudaStream_t stream)
                           static_cast<const float*>(a.partial), parts, a.cols, a.dw);
 }
 
-template <int WIDTH, int NV, bool W32, bool FULL>
+template <typename F, bool W32, bool FULL>
 cudaError_t norm_backward(const NormBackwardArgs& a, int threads, int side, cudaStream_t stream) {
-    using C = BackwardCfg<WIDTH>;
-    auto kernel = norm_backward_kernel<WIDTH, NV, W32, FULL>;
+    auto kernel = norm_backward_kernel<F, W32, FULL>;
     static PerDevice pd;
     int sms = 0;
     const cudaError_t e = per_device_once(pd, sms, [kernel](int& n) {
         n = device_sm_count();
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_STAGES * 3 * NV * C::THREADS * 16);
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, NB_STAGES * 3 * F::NV * F::THREADS * 16);
     });
     if (e != cudaSuccess) return e;
-    // as many CTAs an SM as the registers hold: up to 192 threads four (8192 x 2880 takes 32.7 us, and 41.0 with three)
-    const int per_sm = WIDTH == WIDE ? min(3, C::THREADS / threads) : threads * side <= 192 ? 4 : C::PER_SM;
+    // as many CTAs an SM as the registers hold, up to four (8192 x 2880, 192 threads, takes 32.7 us, and 41.0 with three)
+    const int per_sm = min(4, F::THREADS * F::PER_SM / (threads * side));
     const int parts = (int)min64((a.rows + NB_CLUSTER * side - 1) / (NB_CLUSTER * side), min(NB_PARTS, per_sm * sms / NB_CLUSTER));
     const cudaError_t e2 = launch_chained(kernel, dim3(parts * NB_CLUSTER), dim3(threads, side),
-                                          (size_t)NB_STAGES * (a.dsum ? 3 : 2) * NV * threads * side * 16, NB_CLUSTER, stream, a);
+                                          (size_t)NB_STAGES * (a.dsum ? 3 : 2) * F::NV * threads * side * 16, NB_CLUSTER, stream, a);
     return e2 != cudaSuccess ? e2 : add_parts(a, parts, stream);
 }
 
@@ -1085,22 +1070,26 @@ cudaError_t norm_backward(const NormBackwardArgs& a, cudaStream_t stream) {
     if (a.cols <= 64) return norm_backward_narrow<8, W32>(a, stream);
     if (a.cols <= 128) return norm_backward_narrow<16, W32>(a, stream);
     if (a.cols <= 256) return norm_backward_narrow<32, W32>(a, stream);
-    int nv;
-    int threads = row_threads(a.cols, 256, nv);
-    if (nv > 2) threads = row_threads(a.cols, 1024, nv, 2);
-    // rows side by side: as many as 256 threads take, but not more than leave a row to every CTA
-    int side = min(NB_ROWS, 256 / threads);
-    while (side > 1 && a.rows < (int64_t)side * NB_CLUSTER * NB_PARTS) side /= 2;
-    const bool full = a.cols == nv * threads * 8;
-    auto go = [&](auto w, auto n) {
-        return full ? norm_backward<w.value, n.value, W32, true>(a, threads, max(1, side), stream)
-                    : norm_backward<w.value, n.value, W32, false>(a, threads, max(1, side), stream);
+    auto go = [&](auto form, int side) {
+        using F = decltype(form);
+        const int threads = (int)(((a.cols + 8 * F::NV - 1) / (8 * F::NV) + 31) / 32 * 32);
+        return a.cols == F::NV * threads * 8 ? norm_backward<F, W32, true>(a, threads, side, stream)
+                                             : norm_backward<F, W32, false>(a, threads, side, stream);
     };
-    using One = std::integral_constant<int, 1>;
-    using Two = std::integral_constant<int, 2>;
-    if (side > 1) return go(std::integral_constant<int, NARROW>{}, One{});
-    if (a.cols > 4096) return go(std::integral_constant<int, WIDE>{}, Two{});
-    return nv == 1 ? go(std::integral_constant<int, MIDDLE>{}, One{}) : go(std::integral_constant<int, MIDDLE>{}, Two{});
+    // rows side by side: as many as 256 threads take, but not more than leave a row to every CTA (32768 x 512 takes 26 us, and 59 with
+    // a row a CTA)
+    int side = (int)min64(NB_ROWS, 256 / ((a.cols / 8 + 31) / 32 * 32));
+    while (side > 1 && a.rows < (int64_t)side * NB_CLUSTER * NB_PARTS) side /= 2;
+    if (side > 1) return go(BackwardForm<256, 3, 1, true>{}, side);
+    // 768 threads an SM with 80 registers as long as a row's threads come near them with two vectors each, else 512 with 128 and four:
+    // 8192 x 5120 takes 47.3 us, 2000 x 12288 31.8, 3421 x 8192 32.6 and 2000 x 16384 38.7, where 1024 threads with 64 registers,
+    // which do not hold the weights, took 56.4, 40.1, 42.7 and 53.9
+    if (a.cols <= 2048) return go(BackwardForm<256, 3, 1>{}, 1);
+    if (a.cols <= 4096) return go(BackwardForm<256, 3, 2>{}, 1);
+    if (a.cols <= 6144) return go(BackwardForm<384, 2, 2>{}, 1);
+    if (a.cols <= 8192) return go(BackwardForm<256, 2, 4>{}, 1);
+    if (a.cols <= 12288) return go(BackwardForm<768, 1, 2>{}, 1);
+    return go(BackwardForm<512, 1, 4>{}, 1);
 }
 
 }  // namespace
