@@ -249,8 +249,9 @@ __global__ void __launch_bounds__(SORT_THREADS) moe_place_kernel(const SortArgs 
 
 // ------------------------------------------------------------------------------------------------
 // Dispatch: a warp takes 1 KB of a token's row (32 bytes a lane) to its top_k rows.  For rows in few
-// bits the first CTAs of the launch move the scale bytes meanwhile, by words of four scale columns: a warp a token, the groups'
-// tables in shared memory, and zeros between the groups.  Bound by HBM: 8192 tokens to 65536 rows of 2048 codes take 27 us, 22 of
+// bits the first CTAs of the launch move the scale bytes meanwhile, by words of four scale columns: a warp a token or several
+// (one look-up for the choices of all: 5166 tokens to 3 of 256 experts 9.8 to 6.6 us), the groups' tables in shared memory, and zeros
+// between the groups.  Bound by HBM: 8192 tokens to 65536 rows of 2048 codes take 27 us, 22 of
 // them the rows (7.0 TB/s); the rest are a million scale words, a sector of their own each, since the rows that share one
 // belong to different tokens.
 // ------------------------------------------------------------------------------------------------
@@ -258,6 +259,9 @@ constexpr int MOVE_WARPS = 8, MOVE_THREADS = 32 * MOVE_WARPS;
 constexpr int MOVE_BYTES = 1024;
 // Most CTAs for the scales (8192 tokens: 33 us with 152, 27 with 304 to 1024; the rows alone take 22).
 constexpr int MOVE_SCALE_CTAS = 304;
+// With five CTAs an SM (48 registers) the scales of 869 tokens of 6528 to 7 of 8 experts take 9.4 us, with six 13.4, with four those of
+// 8192 tokens 28.1 in place of 27.0.
+constexpr int MOVE_PER_SM = 5;
 
 struct MoveArgs {
     const uint8_t* x; int64_t pitch;
@@ -266,6 +270,8 @@ struct MoveArgs {
     const int32_t* rows;
     int top_k;
     unsigned scale_ctas;                                   // 0: rows alone
+    DivU32 dv_top_k;
+    int scale_tokens;                                      // of a warp in turn, whose choices are looked up at once
     uint32_t pieces;                                       // of MOVE_BYTES in a row
     DivU32 dv_pieces;
     const uint8_t* s;
@@ -311,40 +317,53 @@ __device__ __forceinline__ void move_scales(const MoveArgs& a) {
     const uint32_t last_mask = (a.columns & 3) ? (1u << (8 * (a.columns & 3))) - 1u : 0xFFFFFFFFu;
     // `width` lanes (a power of two) a choice, 32 / width choices side by side
     const int width = nct >= 32 ? 32 : 1 << (32 - __clz((int)nct - 1)), mine = lane & (width - 1), j0 = lane / width, js = 32 / width;
-    auto row_of = [&](int64_t t) { return t < a.tokens && lane < a.top_k ? load_global(a.rows + t * a.top_k + lane) : -1; };
+    // `n` tokens in turn, whose choices are neighbours in `rows`, a lane each: one search for all of them
+    const int n = a.scale_tokens, my_token = (int)divu32((uint32_t)lane, a.dv_top_k);
+    auto row_of = [&](int64_t t) { return lane < n * a.top_k && t + my_token < a.tokens ? load_global(a.rows + t * a.top_k + lane) : -1; };
     auto word_of = [&](int64_t t, int64_t c) {
         return t < a.tokens && c < nct ? load_global(reinterpret_cast<const uint32_t*>(a.s + sf_offset(t, 4 * c, nct))) : 0u;
     };
-    int row = row_of(me);                                  // on their way while the tables are made
-    uint32_t word = word_of(me, mine);
+    int row = row_of(me * n);                              // on their way while the tables are made
+    uint32_t word = word_of(me * n, mine), word2 = word_of(me * n, mine + 32);        // (none beyond 32 where `width` is less)
     for (int i = threadIdx.x; i <= a.G; i += MOVE_THREADS) s_off[i] = load_global(a.offsets + i);
     __syncthreads();
     scan_group_tiles(s_off, a.G, s_ptile, s_scratch);
-    for (int64_t t = me; t < a.tokens; t += warps) {
+    for (int64_t t0 = me * n; t0 < a.tokens; t0 += warps * n) {
         const int r = row;
-        uint32_t first = word;
-        row = row_of(t + warps);                           // the next token's, on their way meanwhile
-        word = word_of(t + warps, mine);
-        int64_t place = -1;                                // row in the grouped layout of choice `lane`
+        row = row_of(t0 + warps * n);                      // the next tokens', on their way meanwhile
+        int64_t place = -1;                                // row in the grouped layout of this lane's choice
         if (r >= 0 && r < a.total_rows) {
             const int64_t p = grouped_scale_row(s_off, s_ptile, a.G, r);
             if (p >= 0 && p < tile_bound * 128) place = p;
-            if (a.s2_out) a.s2_out[r] = load_global(a.s2 + t);
+            if (a.s2_out) a.s2_out[r] = load_global(a.s2 + t0 + my_token);
         }
-        for (int64_t c0 = 0; c0 < nct; c0 += width) {
-            const int64_t c = c0 + mine;
-            uint32_t w = c0 == 0 ? first : word_of(t, c);
-            if (c == nct - 1) w &= last_mask;
-            for (int j = 0; j < a.top_k; j += js) {
-                const int64_t p = __shfl_sync(0xFFFFFFFFu, place, min(31, j + j0));
-                if (c < nct && j + j0 < a.top_k && p >= 0) *reinterpret_cast<uint32_t*>(a.s_out + sf_offset(p, 4 * c, nct)) = w;
+        for (int i = 0; i < n && t0 + i < a.tokens; ++i) {
+            const int64_t t = t0 + i;
+            uint32_t w = word, w2 = word2;
+            const int64_t then = i + 1 < n ? t + 1 : t0 + warps * n;
+            word = word_of(then, mine);
+            word2 = word_of(then, mine + 32);
+            for (int64_t c = mine; c - mine < nct; c += 64) {
+                if (c - mine > 0) {
+                    w = word_of(t, c);
+                    w2 = word_of(t, c + 32);
+                }
+                if (c == nct - 1) w &= last_mask;
+                if (c + 32 == nct - 1) w2 &= last_mask;
+                for (int j = 0; j < a.top_k; j += js) {
+                    const int64_t p = __shfl_sync(0xFFFFFFFFu, place, min(31, i * a.top_k + j + j0));
+                    if (j + j0 >= a.top_k || p < 0) continue;
+                    uint32_t* to = reinterpret_cast<uint32_t*>(a.s_out + sf_offset(p, 4 * c, nct));
+                    if (c < nct) to[0] = w;
+                    if (c + 32 < nct) to[32 * 128] = w2;
+                }
             }
         }
     }
     zero_between_groups(a.s_out, s_off, s_ptile, a.G, (int)nct, tile_bound, me, warps);
 }
 
-__global__ void __launch_bounds__(MOVE_THREADS) moe_dispatch_kernel(const MoveArgs a) {
+__global__ void __launch_bounds__(MOVE_THREADS, MOVE_PER_SM) moe_dispatch_kernel(const MoveArgs a) {
     chain_begin();
     if (blockIdx.x < a.scale_ctas) {
         move_scales(a);
@@ -580,9 +599,12 @@ cudaError_t launch_moe_dispatch_quantized(bool fp4, const uint8_t* q, const uint
     a.rows = rows; a.top_k = top_k;
     a.s = s; a.s2 = s2; a.columns = hidden / (fp4 ? 16 : 32);
     a.G = G; a.offsets = offsets; a.s_out = s_out; a.s2_out = s2_out;
-    // a warp a token and four of the pieces between groups, up to two CTAs an SM
+    // a warp a token and four of the pieces between groups, up to two CTAs an SM; with more tokens each has several
     const int64_t pieces = (int64_t)G * ((a.columns + 3) / 4);
     a.scale_ctas = (unsigned)min64(MOVE_SCALE_CTAS, (max64(tokens, pieces / 4) + MOVE_WARPS - 1) / MOVE_WARPS);
+    const int64_t warps = (int64_t)a.scale_ctas * MOVE_WARPS;
+    a.dv_top_k = make_divu32(top_k);
+    a.scale_tokens = (int)min64(max(1, 32 / top_k), (tokens + warps - 1) / warps);
     return move_rows(a, stream);
 }
 

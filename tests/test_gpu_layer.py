@@ -468,7 +468,9 @@ def test_dispatch(mx, tokens, k, experts, hidden, view):
 
 
 @pytest.mark.parametrize("tokens,k,experts,hidden", [(1, 1, 4, 32), (1, 8, 128, 2048), (61, 8, 128, 256), (37, 6, 60, 992), (300, 4, 9, 160),
-                                                     (40, 32, 64, 288), (5, 3, 8, 16384), (1000, 2, 3, 512), (900, 8, 1024, 64)])
+                                                     (40, 32, 64, 288), (5, 3, 8, 16384), (1000, 2, 3, 512), (900, 8, 1024, 64),
+                                                     (30, 3, 5, 8480), (2500, 1, 9, 96), (5000, 3, 40, 160), (20000, 5, 300, 32), (2600, 20, 64, 96),
+                                                     (2433, 32, 40, 64), (4867, 2, 7, 2112)])
 @pytest.mark.parametrize("idle", [0.0, 0.4])
 def test_dispatch_quantized_is_the_grouped_quantizer_of_the_dispatched_rows(mx, tokens, k, experts, hidden, idle):
     ids = some_ids(44, tokens, k, experts, idle)
