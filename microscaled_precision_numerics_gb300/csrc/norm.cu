@@ -614,16 +614,14 @@ struct NormBackwardArgs {
 };
 
 // A form of the kernel: CTAs of up to THREADS threads, PER_SM of those an SM (which sets the registers of a thread), NV vectors of eight
-// elements a thread; SIDE: several rows side by side in a CTA.  Every form keeps the weights in registers.
-template <int THREADS_, int PER_SM_, int NV_, bool SIDE_ = false>
+// elements a thread.  Every form keeps the weights in registers.
+template <int THREADS_, int PER_SM_, int NV_>
 struct BackwardForm {
     static constexpr int THREADS = THREADS_, PER_SM = PER_SM_, NV = NV_;
-    static constexpr bool SIDE = SIDE_;
 };
 constexpr int NB_CLUSTER = 2;                              // wider clusters leave SMs idle (four: 72 us where two take 57)
 constexpr int NB_PARTS = 304;                              // most partial sums of a column: pairs of four CTAs an SM
 constexpr int NB_STAGES = 2;
-constexpr int NB_ROWS = 4;                                 // most rows side by side
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
@@ -692,23 +690,15 @@ template <typename F, bool W32, bool FULL>
 __global__ void __launch_bounds__(F::THREADS, F::PER_SM) norm_backward_kernel(const NormBackwardArgs a) {
     constexpr int NV = F::NV;
     extern __shared__ __align__(16) uint8_t sm_rows[];     // [stage][dy, h, dsum][NV][thread] of 16 bytes
-    __shared__ double sm_all[4 * MAX_SEGS];                // [row side by side][turn][sum][segment]
+    __shared__ double sm_all[2][2][MAX_SEGS];              // [turn][sum][segment]
     chain_begin();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, side = F::SIDE ? (int)blockDim.y : 1;
-    const int ty = F::SIDE ? (int)threadIdx.y : 0, tid = ty * blockDim.x + threadIdx.x, threads = blockDim.x * side;
-    // rows side by side have at most MAX_SEGS / NB_ROWS segments each
-    constexpr int sums = F::SIDE ? MAX_SEGS / NB_ROWS : MAX_SEGS;
-    auto meet = [&]() {                                    // of the threads of a row
-        if constexpr (F::SIDE) row_sync(ty, blockDim.x);
-        else __syncthreads();
-    };
-    auto sums_of = [&](uint32_t turn, int which) { return sm_all + (ty * 4 + turn * 2 + which) * sums; };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, tid = threadIdx.x, threads = blockDim.x;
     const int nseg = (a.cols + SEG - 1) / SEG, tensors = a.dsum ? 3 : 2;
     const uint32_t vector = threads * 16, tensor = NV * vector, stage_bytes = tensors * tensor;
     const uint32_t sm0 = (uint32_t)__cvta_generic_to_shared(sm_rows) + tid * 16;
     const int c0 = (warp * 32 + lane) * 8, step = warps * SEG;
     auto outside = [&](int i) { return !FULL && c0 + i * step >= a.cols; };
-    const int64_t first = (int64_t)blockIdx.x * side + ty, next = (int64_t)gridDim.x * side;
+    const int64_t first = blockIdx.x, next = gridDim.x;
     const uint16_t *dy = a.dy + first * a.lddy + c0, *from_h = a.h + first * a.ldh + c0, *dsum = a.dsum + first * a.ldds + c0;
     uint16_t* dx = a.dx + first * a.lddx + c0;
     auto fetch = [&](int64_t row, uint32_t stage) {        // rows in turn
@@ -749,12 +739,12 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_SM) norm_backward_kernel(co
             unpack8(fetched(turn, 0, i), d);
             products8(x, d, weight[i], parts[i], parts[NV + i]);
         }
-        float* sm_s = reinterpret_cast<float*>(sums_of(turn, 0));
-        float* sm_c = reinterpret_cast<float*>(sums_of(turn, 1));
+        float* sm_s = reinterpret_cast<float*>(sm_all[turn][0]);
+        float* sm_c = reinterpret_cast<float*>(sm_all[turn][1]);
         const float mine = butterfly_of(parts);
         const int value = value_of_lane<2 * NV>(), my_seg = warp + (value % NV) * warps;
         if (first_of_value<2 * NV>() && my_seg < nseg) (value < NV ? sm_s : sm_c)[my_seg] = mine;
-        meet();
+        __syncthreads();
         float v[2] = {lane < nseg ? sm_s[lane] : 0.0f, lane < nseg ? sm_c[lane] : 0.0f};
         if (lane + 32 < nseg) {
             v[0] += sm_s[lane + 32];
@@ -765,7 +755,7 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_SM) norm_backward_kernel(co
         RowNorm n = norm_of(ss, a.inv_cols, a.eps);
         float mean = __fmul_rn(__fmul_rn(cc, a.inv_cols), n.r);          // mean(dn n)
         if (!fp32_holds_both(ss, cc, a.eps)) {
-            meet();                                                      // the FP32 sums have been read
+            __syncthreads();                                                   // the FP32 sums have been read
 #pragma unroll 1
             for (int i = 0; i < NV; ++i) {
                 double inner = 0.0, squares = 0.0;
@@ -781,13 +771,13 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_SM) norm_backward_kernel(co
                 squares = butterfly(squares);
                 inner = butterfly(inner);
                 if (lane == 0 && warp + i * warps < nseg) {
-                    sums_of(turn, 0)[warp + i * warps] = squares;
-                    sums_of(turn, 1)[warp + i * warps] = inner;
+                    sm_all[turn][0][warp + i * warps] = squares;
+                    sm_all[turn][1][warp + i * warps] = inner;
                 }
             }
-            meet();
-            n = norm_of_wide(segments_sum(sums_of(turn, 0), nseg), a.cols, a.eps);
-            mean = (float)(segments_sum(sums_of(turn, 1), nseg) / a.cols * n.p * n.r);
+            __syncthreads();
+            n = norm_of_wide(segments_sum(sm_all[turn][0], nseg), a.cols, a.eps);
+            mean = (float)(segments_sum(sm_all[turn][1], nseg) / a.cols * n.p * n.r);
         }
         split_far(n);
         const float by_x = -__fmul_rn(__fmul_rn(mean, n.r), n.r);
@@ -812,7 +802,7 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_SM) norm_backward_kernel(co
         dx += next * a.lddx;
     }
     // the cluster's sums: each CTA's in its shared memory (the ring is free: 8 bytes a column and more), a share of the columns each
-    float *sm_first = reinterpret_cast<float*>(sm_rows), *sm_dw = sm_first + ty * a.cols;
+    float* sm_dw = reinterpret_cast<float*>(sm_rows);
     __syncthreads();                                       // the last row has been read
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -826,55 +816,81 @@ __global__ void __launch_bounds__(F::THREADS, F::PER_SM) norm_backward_kernel(co
     const int peers = (int)cluster_size();
     for (int c = ((int)cluster_rank() * threads + tid) * 4; c < a.cols; c += peers * threads * 4) {
         uint64_t s0 = 0, s1 = 0;
-        for (int p = 0; p < peers; ++p)
-            for (int g = 0; g < side; ++g) {
-                uint64_t v0, v1;
-                asm volatile("ld.shared::cluster.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(peer_address(sm_first + g * a.cols + c, p)) : "memory");
-                s0 = f2_add(s0, v0);
-                s1 = f2_add(s1, v1);
-            }
+        for (int p = 0; p < peers; ++p) {
+            uint64_t v0, v1;
+            asm volatile("ld.shared::cluster.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(peer_address(sm_dw + c, p)) : "memory");
+            s0 = f2_add(s0, v0);
+            s1 = f2_add(s1, v1);
+        }
         *reinterpret_cast<ulonglong2*>(a.partial + (int64_t)(blockIdx.x / peers) * a.cols + c) = make_ulonglong2(s0, s1);
     }
     cluster_sync();                                        // nobody leaves while the others read its sums
 }
 
-// Rows of up to 256 elements: LANES lanes a row (8, 16 or 32).  The warps walk the rows, each lane with a ring of its own vectors in
-// shared memory, and a CTA adds its sums of dw up there at the end.  262144 x 128 with dsum take 39.9 us, the measured copy rate (89.5 in
-// the form for wider rows); two CTAs of 256 threads an SM: with 384 (80 registers) 42.4, with 512 (64, which spill) 52.3.
-constexpr int NBN_THREADS = 256, NBN_STAGES = 4;
+// Rows of up to 1024 elements, a warp or part of one each: LANES lanes (8, 16 or 32), NV vectors of eight elements a lane (more than one
+// with 32 lanes only).  The warps walk the rows, each lane with a ring of its own vectors in shared memory, and a CTA adds its sums of dw
+// up there at the end.  262144 x 128 with dsum take 39.7 us, the measured copy rate, and 32768 x 512 20.3 (89.5 and 25.9 with rows side by side in the
+// form for wider rows); two CTAs of 256 threads an SM: with 384 (80 registers) 42.4, with 512 (64, which spill) 52.3.
+constexpr int NBN_THREADS = 256;
+template <int NV>
+constexpr int NBN_STAGES = NV == 4 ? 2 : 4;
 
-// p, r and mean(dn n) of the warp's rows, summed in FP64 (out of line, so that it costs the others no registers).
-template <int LANES, bool W32>
-__device__ __noinline__ float3 slow_narrow_row(uint4 h, uint4 dy, const void* weight, int c, int cols, float eps) {
-    float x[8], d[8], w[8] = {};
-    unpack8(h, x);
-    unpack8(dy, d);
-    if (c < cols) weights8<W32>(weight, c, w);
-    const double squares = butterfly<LANES>(squares8_wide(h)), inner = butterfly<LANES>(inner8_wide(x, d, w));
-    const RowNorm n = norm_of_wide(squares, cols, eps);
-    return make_float3(n.p, n.r, (float)(inner / cols * n.p * n.r));
+// The sum over a row's segments, whose sums are v, in the fixed order.
+template <typename T, int NV>
+__device__ __forceinline__ T few_segments_sum(const T (&v)[NV]) {
+    if constexpr (NV == 1) return v[0];
+    else if constexpr (NV == 2) return v[0] + v[1];
+    else return (v[0] + v[2]) + (v[1] + v[3]);
 }
 
-template <int LANES, bool W32>
+// p, r and mean(dn n) of the warp's rows, summed in FP64 (out of line, so that it costs the others no registers).  dy and h: the lane's
+// vectors, NBN_THREADS apart.
+template <int LANES, int NV, bool W32>
+__device__ __noinline__ float3 slow_narrow_row(const uint4* dy, const uint4* h, bool in, const void* weight, int c, int cols, float eps) {
+    double squares[NV], inner[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        squares[i] = inner[i] = 0.0;
+        if (in && c + i * SEG < cols) {
+            float x[8], d[8], w[8];
+            unpack8(h[i * NBN_THREADS], x);
+            unpack8(dy[i * NBN_THREADS], d);
+            weights8<W32>(weight, c + i * SEG, w);
+            squares[i] = squares8_wide(h[i * NBN_THREADS]);
+            inner[i] = inner8_wide(x, d, w);
+        }
+        squares[i] = butterfly<LANES>(squares[i]);
+        inner[i] = butterfly<LANES>(inner[i]);
+    }
+    const RowNorm n = norm_of_wide(few_segments_sum(squares), cols, eps);
+    return make_float3(n.p, n.r, (float)(few_segments_sum(inner) / cols * n.p * n.r));
+}
+
+template <int LANES, int NV, bool W32>
 __global__ void __launch_bounds__(NBN_THREADS, 2) norm_backward_narrow_kernel(const NormBackwardArgs a) {
-    constexpr int SIDE = 32 / LANES, WARPS = NBN_THREADS / 32;
-    constexpr uint32_t TENSOR = NBN_THREADS * 16;
-    extern __shared__ __align__(16) uint8_t sm_rows[];     // [stage][dy, h, dsum][thread] of 16 bytes; then [warp][column] sums
+    static_assert(NV == 1 || LANES == 32, "several vectors a lane: a segment each");
+    constexpr int SIDE = 32 / LANES, WARPS = NBN_THREADS / 32, STAGES = NBN_STAGES<NV>;
+    constexpr uint32_t TENSOR = NV * NBN_THREADS * 16;
+    extern __shared__ __align__(16) uint8_t sm_rows[];     // [stage][dy, h, dsum][NV][thread] of 16 bytes; then [warp][column] sums
     chain_begin();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane % LANES * 8;
     const uint32_t stage_bytes = (a.dsum ? 3 : 2) * TENSOR, sm0 = (uint32_t)__cvta_generic_to_shared(sm_rows) + threadIdx.x * 16;
     const int64_t next = (int64_t)gridDim.x * (WARPS * SIDE), first = ((int64_t)blockIdx.x * WARPS + warp) * SIDE + lane / LANES;
     // the group's first row decides for the warp (its lanes stay together), the lane's own whether it has one
     const int64_t turns = first - lane / LANES < a.rows ? (a.rows - (first - lane / LANES) + next - 1) / next : 0;
-    auto inside = [&](int64_t t) { return c < a.cols && first + t * next < a.rows; };
+    auto has = [&](int i) { return c + i * SEG < a.cols; };
     const uint16_t *dy = a.dy + first * a.lddy + c, *from_h = a.h + first * a.ldh + c, *dsum = a.dsum + first * a.ldds + c;
     uint16_t* dx = a.dx + first * a.lddx + c;
     auto fetch = [&](int64_t t, uint32_t stage) {          // turns in order
-        if (inside(t)) {
-            const uint32_t at = sm0 + stage * stage_bytes;
-            copy16(at, dy);
-            copy16(at + TENSOR, from_h);
-            if (a.dsum) copy16(at + 2 * TENSOR, dsum);
+        if (first + t * next < a.rows) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                if (!has(i)) continue;
+                const uint32_t at = sm0 + stage * stage_bytes + i * (NBN_THREADS * 16);
+                copy16(at, dy + i * SEG);
+                copy16(at + TENSOR, from_h + i * SEG);
+                if (a.dsum) copy16(at + 2 * TENSOR, dsum + i * SEG);
+            }
             dy += next * a.lddy;
             from_h += next * a.ldh;
             dsum += next * a.ldds;
@@ -882,70 +898,97 @@ __global__ void __launch_bounds__(NBN_THREADS, 2) norm_backward_narrow_kernel(co
         copies_commit();                                   // an empty group where there is no row, so that the count goes on
     };
 #pragma unroll
-    for (int t = 0; t < NBN_STAGES - 1; ++t) fetch(t, t);
-    float w[8] = {}, dw[8] = {};
-    if (c < a.cols) weights8<W32>(a.w, c, w);
+    for (int t = 0; t < STAGES - 1; ++t) fetch(t, t);
+    float w[NV][8] = {}, dw[NV][8] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if (has(i)) weights8<W32>(a.w, c + i * SEG, w[i]);
     uint32_t stage = 0;
     for (int64_t t = 0; t < turns; ++t) {
-        fetch(t + NBN_STAGES - 1, stage == 0 ? NBN_STAGES - 1 : stage - 1);           // into the stage that this lane read in the turn before
-        copies_wait<NBN_STAGES - 1>();
-        auto fetched = [&](int which) { return *reinterpret_cast<const uint4*>(sm_rows + stage * stage_bytes + which * TENSOR + threadIdx.x * 16); };
-        const bool in = inside(t);
-        uint4 h = make_uint4(0u, 0u, 0u, 0u), g = h;
-        if (in) {
-            g = fetched(0);
-            h = fetched(1);
+        fetch(t + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);      // into the stage that this lane read in the turn before
+        copies_wait<STAGES - 1>();
+        auto fetched = [&](int which) { return reinterpret_cast<const uint4*>(sm_rows + stage * stage_bytes + which * TENSOR) + threadIdx.x; };
+        const bool row_in = first + t * next < a.rows;
+        float parts[2 * NV];
+        uint4 held[2];                                     // of one vector a lane, which need not be read again (2 of 41 us)
+        auto vector = [&](int which, int i) { return NV == 1 ? held[which] : fetched(which)[i * NBN_THREADS]; };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            parts[i] = parts[NV + i] = 0.0f;
+            if (!row_in || !has(i)) continue;
+            if (NV == 1)
+                for (int k = 0; k < 2; ++k) held[k] = fetched(k)[0];
+            float x[8], d[8];
+            unpack8(vector(1, i), x);
+            unpack8(vector(0, i), d);
+            products8(x, d, w[i], parts[i], parts[NV + i]);
         }
-        float x[8], d[8], ss, cc;
-        unpack8(h, x);
-        unpack8(g, d);
-        products8(x, d, w, ss, cc);
-        ss = butterfly<LANES>(ss);
-        cc = butterfly<LANES>(cc);
+        float ss, cc;
+        if constexpr (NV == 1) {
+            ss = butterfly<LANES>(parts[0]);
+            cc = butterfly<LANES>(parts[1]);
+        } else {                                           // value v to the lanes from v * 32 / (2 NV) on; then the segments in pairs
+            float both = butterfly_of(parts);
+#pragma unroll
+            for (int o = 8; o >= 16 / NV; o >>= 1) both += __shfl_xor_sync(0xFFFFFFFFu, both, o);
+            ss = __shfl_sync(0xFFFFFFFFu, both, 0);
+            cc = __shfl_sync(0xFFFFFFFFu, both, 16);
+        }
         RowNorm n = norm_of(ss, a.inv_cols, a.eps);
         float mean = __fmul_rn(__fmul_rn(cc, a.inv_cols), n.r);          // mean(dn n)
         const bool fine = fp32_holds_both(ss, cc, a.eps);
         if (__any_sync(0xFFFFFFFFu, !fine)) {
-            const float3 wide = slow_narrow_row<LANES, W32>(h, g, a.w, c, a.cols, a.eps);
+            const float3 wide = slow_narrow_row<LANES, NV, W32>(fetched(0), fetched(1), row_in, a.w, c, a.cols, a.eps);
             if (!fine) {
                 n = RowNorm{wide.x, wide.y};
                 mean = wide.z;
             }
         }
         split_far(n);
-        if (in) {
-            const float by_x = -__fmul_rn(__fmul_rn(mean, n.r), n.r);
-            float o[8];
-            unpack8(h, x);
-            unpack8(g, d);
-            if (n.p != 1.0f) gradient8<true>(x, d, w, n, by_x, dw, o);
-            else gradient8<false>(x, d, w, n, by_x, dw, o);
-            if (a.dsum) {
-                unpack8(fetched(2), x);
+        const float by_x = -__fmul_rn(__fmul_rn(mean, n.r), n.r);
+        auto emit = [&](auto scaled) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = __fadd_rn(o[j], x[j]);
+            for (int i = 0; i < NV; ++i) {
+                if (!has(i)) continue;
+                float x[8], d[8], o[8];
+                unpack8(vector(1, i), x);
+                unpack8(vector(0, i), d);
+                gradient8<decltype(scaled)::value>(x, d, w[i], n, by_x, dw[i], o);
+                if (a.dsum) {
+                    unpack8(fetched(2)[i * NBN_THREADS], x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = __fadd_rn(o[j], x[j]);
+                }
+                *reinterpret_cast<uint4*>(dx + i * SEG) = pack8(o);
             }
-            *reinterpret_cast<uint4*>(dx) = pack8(o);
+        };
+        if (row_in) {
+            if (n.p != 1.0f) emit(std::true_type{});
+            else emit(std::false_type{});
         }
         dx += next * a.lddx;
-        stage = stage == NBN_STAGES - 1 ? 0 : stage + 1;
+        stage = stage == STAGES - 1 ? 0 : stage + 1;
     }
+    if (LANES < 32)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int o = 16; o >= LANES; o >>= 1) dw[j] += __shfl_xor_sync(0xFFFFFFFFu, dw[j], o);
-    float* sm_dw = reinterpret_cast<float*>(sm_rows);      // (the ring's copies have all arrived, but other warps may still read theirs)
-    __syncthreads();
-    if (lane < LANES) {
-        float4* at = reinterpret_cast<float4*>(sm_dw + warp * (LANES * 8) + c);
-        at[0] = make_float4(dw[0], dw[1], dw[2], dw[3]);
-        at[1] = make_float4(dw[4], dw[5], dw[6], dw[7]);
-    }
+            for (int o = 16; o >= LANES; o >>= 1) dw[0][j] += __shfl_xor_sync(0xFFFFFFFFu, dw[0][j], o);
+    constexpr int WIDTH = NV * LANES * 8;                  // 32 KB at most: the ring has 48 and more
+    float* sm_dw = reinterpret_cast<float*>(sm_rows);
+    __syncthreads();                                       // the last rows have been read
+    if (lane < LANES)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float4* at = reinterpret_cast<float4*>(sm_dw + warp * WIDTH + c + i * SEG);
+            at[0] = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+            at[1] = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+        }
     __syncthreads();
     for (int at = threadIdx.x; at < a.cols; at += NBN_THREADS) {
         float s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < WARPS; ++k) s += sm_dw[k * (LANES * 8) + at];
+        for (int k = 0; k < WARPS; ++k) s += sm_dw[k * WIDTH + at];
         a.partial[(int64_t)blockIdx.x * a.cols + at] = s;
     }
 }
@@ -1031,7 +1074,7 @@ cudaError_t add_parts(const NormBackwardArgs& a, int parts, cudaStream_t stream)
 }
 
 template <typename F, bool W32, bool FULL>
-cudaError_t norm_backward(const NormBackwardArgs& a, int threads, int side, cudaStream_t stream) {
+cudaError_t norm_backward(const NormBackwardArgs& a, int threads, cudaStream_t stream) {
     auto kernel = norm_backward_kernel<F, W32, FULL>;
     static PerDevice pd;
     int sms = 0;
@@ -1041,17 +1084,17 @@ cudaError_t norm_backward(const NormBackwardArgs& a, int threads, int side, cuda
     });
     if (e != cudaSuccess) return e;
     // as many CTAs an SM as the registers hold, up to four (8192 x 2880, 192 threads, takes 32.7 us, and 41.0 with three)
-    const int per_sm = min(4, F::THREADS * F::PER_SM / (threads * side));
-    const int parts = (int)min64((a.rows + NB_CLUSTER * side - 1) / (NB_CLUSTER * side), min(NB_PARTS, per_sm * sms / NB_CLUSTER));
-    const cudaError_t e2 = launch_chained(kernel, dim3(parts * NB_CLUSTER), dim3(threads, side),
-                                          (size_t)NB_STAGES * (a.dsum ? 3 : 2) * F::NV * threads * side * 16, NB_CLUSTER, stream, a);
+    const int per_sm = min(4, F::THREADS * F::PER_SM / threads);
+    const int parts = (int)min64((a.rows + NB_CLUSTER - 1) / NB_CLUSTER, min(NB_PARTS, per_sm * sms / NB_CLUSTER));
+    const cudaError_t e2 = launch_chained(kernel, dim3(parts * NB_CLUSTER), dim3(threads),
+                                          (size_t)NB_STAGES * (a.dsum ? 3 : 2) * F::NV * threads * 16, NB_CLUSTER, stream, a);
     return e2 != cudaSuccess ? e2 : add_parts(a, parts, stream);
 }
 
-template <int LANES, bool W32>
+template <int LANES, int NV, bool W32>
 cudaError_t norm_backward_narrow(const NormBackwardArgs& a, cudaStream_t stream) {
-    auto kernel = norm_backward_narrow_kernel<LANES, W32>;
-    constexpr int tensor = NBN_STAGES * NBN_THREADS * 16;
+    auto kernel = norm_backward_narrow_kernel<LANES, NV, W32>;
+    constexpr int tensor = NBN_STAGES<NV> * NV * NBN_THREADS * 16;
     static PerDevice pd;
     int sms = 0;
     const cudaError_t e = per_device_once(pd, sms, [kernel](int& n) {
@@ -1067,29 +1110,25 @@ cudaError_t norm_backward_narrow(const NormBackwardArgs& a, cudaStream_t stream)
 
 template <bool W32>
 cudaError_t norm_backward(const NormBackwardArgs& a, cudaStream_t stream) {
-    if (a.cols <= 64) return norm_backward_narrow<8, W32>(a, stream);
-    if (a.cols <= 128) return norm_backward_narrow<16, W32>(a, stream);
-    if (a.cols <= 256) return norm_backward_narrow<32, W32>(a, stream);
-    auto go = [&](auto form, int side) {
+    if (a.cols <= 64) return norm_backward_narrow<8, 1, W32>(a, stream);
+    if (a.cols <= 128) return norm_backward_narrow<16, 1, W32>(a, stream);
+    if (a.cols <= 256) return norm_backward_narrow<32, 1, W32>(a, stream);
+    if (a.cols <= 512) return norm_backward_narrow<32, 2, W32>(a, stream);
+    if (a.cols <= 1024) return norm_backward_narrow<32, 4, W32>(a, stream);
+    auto go = [&](auto form) {
         using F = decltype(form);
         const int threads = (int)(((a.cols + 8 * F::NV - 1) / (8 * F::NV) + 31) / 32 * 32);
-        return a.cols == F::NV * threads * 8 ? norm_backward<F, W32, true>(a, threads, side, stream)
-                                             : norm_backward<F, W32, false>(a, threads, side, stream);
+        return a.cols == F::NV * threads * 8 ? norm_backward<F, W32, true>(a, threads, stream) : norm_backward<F, W32, false>(a, threads, stream);
     };
-    // rows side by side: as many as 256 threads take, but not more than leave a row to every CTA (32768 x 512 takes 26 us, and 59 with
-    // a row a CTA)
-    int side = (int)min64(NB_ROWS, 256 / ((a.cols / 8 + 31) / 32 * 32));
-    while (side > 1 && a.rows < (int64_t)side * NB_CLUSTER * NB_PARTS) side /= 2;
-    if (side > 1) return go(BackwardForm<256, 3, 1, true>{}, side);
     // 768 threads an SM with 80 registers as long as a row's threads come near them with two vectors each, else 512 with 128 and four:
     // 8192 x 5120 takes 47.3 us, 2000 x 12288 31.8, 3421 x 8192 32.6 and 2000 x 16384 38.7, where 1024 threads with 64 registers,
     // which do not hold the weights, took 56.4, 40.1, 42.7 and 53.9
-    if (a.cols <= 2048) return go(BackwardForm<256, 3, 1>{}, 1);
-    if (a.cols <= 4096) return go(BackwardForm<256, 3, 2>{}, 1);
-    if (a.cols <= 6144) return go(BackwardForm<384, 2, 2>{}, 1);
-    if (a.cols <= 8192) return go(BackwardForm<256, 2, 4>{}, 1);
-    if (a.cols <= 12288) return go(BackwardForm<768, 1, 2>{}, 1);
-    return go(BackwardForm<512, 1, 4>{}, 1);
+    if (a.cols <= 2048) return go(BackwardForm<256, 3, 1>{});
+    if (a.cols <= 4096) return go(BackwardForm<256, 3, 2>{});
+    if (a.cols <= 6144) return go(BackwardForm<384, 2, 2>{});
+    if (a.cols <= 8192) return go(BackwardForm<256, 2, 4>{});
+    if (a.cols <= 12288) return go(BackwardForm<768, 1, 2>{});
+    return go(BackwardForm<512, 1, 4>{});
 }
 
 }  // namespace

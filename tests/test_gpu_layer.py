@@ -216,7 +216,8 @@ def test_norm_backward(mx, rows, cols, weight, with_dsum):
         assert torch.equal(a[alias], dx) and torch.equal(dw, dw2)
 
 
-@pytest.mark.parametrize("rows,cols", [(9001, 64), (77901, 40), (39001, 128), (40000, 72), (19501, 224), (40011, 256)])
+@pytest.mark.parametrize("rows,cols", [(9001, 64), (77901, 40), (39001, 128), (40000, 72), (19501, 224), (40011, 256),
+                                       (20001, 384), (9001, 512), (9003, 776), (5000, 1000), (4999, 1024)])
 def test_norm_backward_of_narrow_rows(mx, rows, cols):
     """Many rows to a warp, ordinary ones and ones that FP32 does not hold side by side, in views with other strides."""
     h, dy, dsum = rand(30, rows, cols), rand(31, rows, cols, scale=0.01), rand(32, rows, cols, scale=0.01)
