@@ -974,7 +974,7 @@ __global__ void __launch_bounds__(NBN_THREADS, 2) norm_backward_narrow_kernel(co
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int o = 16; o >= LANES; o >>= 1) dw[0][j] += __shfl_xor_sync(0xFFFFFFFFu, dw[0][j], o);
-    constexpr int WIDTH = NV * LANES * 8;                  // 32 KB at most: the ring has 48 and more
+    constexpr int WIDTH = NV * LANES * 8;                  // (half of the ring at most)
     float* sm_dw = reinterpret_cast<float*>(sm_rows);
     __syncthreads();                                       // the last rows have been read
     if (lane < LANES)
