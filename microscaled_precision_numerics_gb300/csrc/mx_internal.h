@@ -196,6 +196,22 @@ struct MatvecArgs {
 cudaError_t launch_matvec_nvfp4(const MatvecArgs& a, cudaStream_t stream);
 
 // Norm with residual and MXFP8 output, and its gradient (norm.cu).
+
+// How the norm without column-wise codes takes rows of more than 256 columns: `threads` of a row (whole warps, up to
+// NORM_ROWS_THREADS), nv vectors of eight elements each (1, 2 or 4), which cover the row.
+struct NormRowsForm {
+    int threads, nv;
+};
+constexpr int NORM_ROWS_THREADS = 512;
+inline NormRowsForm norm_rows_form(int64_t rows, int64_t cols) {
+    // many rows: four vectors a thread (the warps that hold cols / 32 of them, rounded up), so that more bytes are on their way for every
+    // row's meeting of its warps; few rows: as many threads a row as have work
+    const int64_t vectors = (cols + 7) / 8, four = (vectors + 127) / 128 * 32;
+    const int64_t most = rows >= 512 && four < NORM_ROWS_THREADS ? four : NORM_ROWS_THREADS;
+    int nv = 1;
+    while (nv * most < vectors) nv *= 2;
+    return {(int)(((vectors + nv - 1) / nv + 31) / 32 * 32), nv};
+}
 cudaError_t launch_rmsnorm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, const void* w, bool w32,
                            float eps, int64_t rows, int64_t cols, uint16_t* sum, int64_t lds, uint16_t* y, int64_t ldy,
                            uint8_t* q_row, uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, cudaStream_t stream);

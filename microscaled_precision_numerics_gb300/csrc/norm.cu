@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(NN_THREADS) norm_narrow_kernel(const NormArgs 
 // (1003 x 14336 took 54 us, now 17: three turns of two CTAs an SM, each a row's loads, meeting and stores after one another).
 // FULL: the threads' vectors are the row exactly, no comparisons (8192 x 4096 to codes 29.8 to 27.3 us).  With residual, sum and codes
 // 8192 x 4096 takes 36 us, 97 % of the measured copy rate.
-constexpr int NR_THREADS = 512;
+constexpr int NR_THREADS = NORM_ROWS_THREADS;
 template <int NV, bool W32, bool FULL>
 __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs a) {
     __shared__ double sm_all[8][MAX_SEGS];
@@ -1015,14 +1015,6 @@ __global__ void __launch_bounds__(32 * ND_WARPS) norm_dweight_kernel(const float
     if (lane == 0 && blockIdx.x * 32 + warp < cols) dw[blockIdx.x * 32 + warp] = s;
 }
 
-// Vectors of eight elements a thread (a power of two) such that at most `threads` take a row, and whole warps of threads.
-int row_threads(int64_t cols, int threads, int& nv) {
-    const int64_t vectors = (cols + 7) / 8;
-    nv = 1;
-    while (nv * threads < vectors) nv *= 2;
-    return (int)(((vectors + nv - 1) / nv + 31) / 32 * 32);
-}
-
 template <int LANES, bool W32>
 cudaError_t norm_narrow(const NormArgs& a, cudaStream_t stream) {
     auto go = [&](auto kernel, int rows_a_cta) {
@@ -1038,11 +1030,9 @@ cudaError_t norm_rows(const NormArgs& a, cudaStream_t stream) {
     if (a.cols <= 64) return norm_narrow<8, W32>(a, stream);
     if (a.cols <= 128) return norm_narrow<16, W32>(a, stream);
     if (a.cols <= 256) return norm_narrow<32, W32>(a, stream);
-    // many rows: four vectors a thread, so that more bytes are on their way for every row's meeting of its warps; few rows: as
-    // many threads a row as have work
-    const bool many = a.rows >= 512;
-    int nv;
-    const int threads = row_threads(a.cols, many ? (int)min64(NR_THREADS, max64(32, (a.cols / 32 + 31) / 32 * 32)) : NR_THREADS, nv);
+    const NormRowsForm form = norm_rows_form(a.rows, a.cols);
+    const int threads = form.threads, nv = form.nv;
+    if (nv > 4 || (int64_t)nv * threads * 8 < a.cols) return cudaErrorInvalidConfiguration;       // no form covers the row
     const int per = max(1, 256 / threads);
     auto go = [&](auto kernel) {
         return launch_chained(kernel, dim3((unsigned)((a.rows + per - 1) / per)), dim3(threads, per), 0, 0, stream, a);

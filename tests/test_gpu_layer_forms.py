@@ -1,0 +1,76 @@
+"""The forms that the operators between a layer's products take by their sizes: every kind of width of the norm from 512 rows on, and
+wide rows that FP32 does not hold.  Against the 64-bit forms of layer_ref.py and against the same rows in another form."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+from test_gpu_layer import codes_of, host, mx, rand, run_norm, same, within, y_bound      # noqa: F401
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def norm_into_marked(mx, x, w, eps, res):
+    """(sum, y) of a call without codes, into buffers that held a mark."""
+    y, s = torch.full_like(x, 77.0), None if res is None else torch.full_like(x, 77.0)
+    mx.mx_rmsnorm_mxfp8(x, w, eps, residual=res, sum_out=s, y=y)
+    return s, y
+
+
+# 8, 16 and 24 columns beyond each multiple of 1024
+RAGGED = [1024 * k + r for k in range(1, 16) for r in (8, 16, 24)]
+
+
+@pytest.mark.parametrize("cols", RAGGED + [264, 520, 1016, 1000, 2040, 4096, 5120, 8184, 12288, 16376, 16384])
+def test_norm_of_512_rows_and_more_at_every_kind_of_width(mx, cols):
+    """The same rows in a call of 512 and in calls of fewer, which take another form, and some of them against 64 bits."""
+    x, res = rand(101, 512, cols), rand(102, 512, cols, scale=3.0)
+    w = rand(103, cols, scale=0.2).float() + 1.0
+    for r in (None, res):
+        s, y = norm_into_marked(mx, x, w, 1e-6, r)
+        for part in (slice(0, 300), slice(300, 512)):
+            s2, y2 = norm_into_marked(mx, x[part], w, 1e-6, None if r is None else r[part])
+            assert torch.equal(y[part], y2) and (r is None or torch.equal(s[part], s2))
+        some = slice(0, 512, 73)
+        h, _, want = ref.norm(host(x[some]), host(w), 1e-6, None if r is None else host(r[some]))
+        within(y[some], want, y_bound(want))
+        assert r is None or np.array_equal(host(s[some]), h)
+
+
+@pytest.mark.parametrize("rows,cols", [(513, 288), (600, 1032), (777, 2056), (512, 3080), (1003, 14336), (520, 15384), (2000, 1056), (801, 4096),
+                                       (515, 992)])
+@pytest.mark.parametrize("weight", [BF, F32])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_norm_of_many_rows(mx, rows, cols, weight, with_residual):
+    x, res = rand(104, rows, cols), rand(105, rows, cols, scale=3.0) if with_residual else None
+    w = (1.0 + 0.2 * torch.randn(cols, generator=torch.Generator().manual_seed(106))).to(weight).to(DEV)
+    codes = cols % 32 == 0
+    y = torch.full_like(x, 77.0)
+    s, y, out = run_norm(mx, x, w, 1e-6, res, row=codes, sum_out=None if res is None else torch.full_like(x, 77.0), y=y)
+    h, _, want = ref.norm(host(x), host(w), 1e-6, None if res is None else host(res))
+    if res is not None:
+        assert np.array_equal(host(s), h)
+    within(y, want, y_bound(want))
+    if codes:
+        same(out, codes_of(mx, y, True, False))
+
+
+@pytest.mark.parametrize("rows,cols,col", [(7, 4096, False), (7, 8192, False), (5, 16384, False), (700, 1056, False), (601, 2048, False),
+                                           (520, 1032, False), (64, 1536, True), (32, 5120, True), (64, 8224, True), (32, 16384, True)])
+def test_norm_of_wide_rows_beyond_the_range_of_squares(mx, rows, cols, col):
+    """Ordinary rows, rows whose squares pass FP32's range on either side and rows that are not finite, in one call."""
+    x, w = rand(107, rows, cols), rand(108, cols, scale=0.2).float() + 1.0
+    x[1::7] *= 2.0 ** 70                                   # (exact: powers of two)
+    x[2::7] *= 2.0 ** -80
+    x[3::14, cols - 1], x[4::14, 3] = float("inf"), float("nan")
+    fine = torch.ones(rows, dtype=torch.bool, device=DEV)
+    fine[3::14] = fine[4::14] = False
+    codes = cols % 32 == 0
+    _, y, out = run_norm(mx, x, w, 0.0, row=codes, col=col)
+    _, _, want = ref.norm(host(x[fine]), host(w), 0.0)
+    within(y[fine], want, y_bound(want))
+    assert torch.isnan(y[4::14]).all() and torch.isnan(y[3::14, -1]).all() and not y[3::14, :-1].any()
+    if codes or col:
+        same(out, codes_of(mx, y, codes, col))
