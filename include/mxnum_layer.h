@@ -72,7 +72,8 @@ mx_status mx_moe_route(const void* logits, mx_dtype logits_type, int64_t ldl, in
 /* Gradient of the logits from that of the weights, with w recomputed from logits and ids (ids outside [0, experts) are skipped):
  *   normalize = 1: dlogits[id_j] = w_j (dw_j - sum_i w_i dw_i), zero elsewhere
  *   normalize = 0: dlogits[e] = p_e (dw_j where e = id_j - sum_i w_i dw_i), p the softmax over all
- * dlogits [tokens, ldd] of the logits' type. */
+ * dlogits [tokens, ldd] of the logits' type.  Where w or p is NaN (a NaN or +inf among the logits that it is made of) these are NaN:
+ * the chosen ones' (1) or the whole row (0). */
 mx_status mx_moe_route_backward(const void* logits, mx_dtype logits_type, int64_t ldl, int64_t tokens, int64_t experts,
                                 int64_t top_k, int normalize, const int32_t* ids, const float* dweights, void* dlogits,
                                 int64_t ldd, cudaStream_t stream);

@@ -186,11 +186,12 @@ moe_route_backward_kernel(const void* logits, int64_t ldl, int64_t tokens, int e
         }
     sum = warp_add(sum);                                   // a NaN passes the maximum and reaches the sum
     const bool none = sum == 0.0f;                         // nothing chosen, or nothing but -inf
-    w = none || w == 0.0f ? 0.0f : __fdiv_rn(w, sum);
+    const bool is_nan = sum != sum;                        // a NaN or +inf: the softmax is NaN everywhere, where a term is 0 too
+    w = none ? 0.0f : __fdiv_rn(w, sum);
     const float inner = warp_add(__fmul_rn(w, dw));
     const float share = none ? 0.0f : -__fdiv_rn(inner, sum);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) p[i] = normalize || p[i] == 0.0f ? 0.0f : __fmul_rn(p[i], share);
+    for (int i = 0; i < EPL; ++i) p[i] = normalize || (p[i] == 0.0f && !is_nan) ? 0.0f : __fmul_rn(p[i], share);
     const float part = normalize ? __fmul_rn(w, __fsub_rn(dw, inner)) : __fmul_rn(w, dw);
     // what a chosen expert has besides, from all of its choices (one, unless an id is given twice); the first of them writes it
     float chosen = normalize || w == 0.0f ? 0.0f : -__fmul_rn(w, inner);

@@ -74,3 +74,32 @@ def test_norm_of_wide_rows_beyond_the_range_of_squares(mx, rows, cols, col):
     assert torch.isnan(y[4::14]).all() and torch.isnan(y[3::14, -1]).all() and not y[3::14, :-1].any()
     if codes or col:
         same(out, codes_of(mx, y, codes, col))
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("experts,k", [(12, 3), (100, 8), (300, 5), (1024, 32)])
+def test_route_gradient_of_rows_that_are_not_finite(mx, normalize, dtype, experts, k):
+    """Such a row's softmax is NaN everywhere, and so is what it passes on: all of the row, or (over the chosen) the chosen ones."""
+    inf, nan = float("inf"), float("nan")
+    z = torch.randn((6, experts), generator=torch.Generator().manual_seed(120)).to(dtype).to(DEV)
+    z[0, 7] = inf
+    z[1, 2], z[1, 9] = nan, -inf
+    z[2, 4], z[2, 5] = inf, nan
+    z[3, 6], z[3, 7:] = inf, -inf                          # fewer than k may be left
+    z[4, 3] = -inf                                         # an ordinary row
+    z[5] = -inf
+    ids = torch.empty((6, k), dtype=torch.int32, device=DEV)
+    w, dw = torch.empty((6, k), device=DEV), torch.randn((6, k), generator=torch.Generator().manual_seed(121)).to(DEV)
+    mx.mx_moe_route(z, ids, w, normalize=normalize)
+    dz = torch.full_like(z, 99.0)
+    mx.mx_moe_route_backward(z, ids, dw, dz, normalize=normalize)
+    got, chosen = host(dz), np.zeros((6, experts), bool)
+    for t in range(6):
+        chosen[t, host(ids)[t][host(ids)[t] >= 0]] = True
+    for t in range(4):
+        if normalize:
+            assert np.isnan(got[t, chosen[t]]).all() and not got[t, ~chosen[t]].any()
+        else:
+            assert np.isnan(got[t]).all()
+    assert np.isfinite(got[4:]).all() and got[4, 3] == 0 and not got[5].any()
