@@ -746,6 +746,14 @@ def _ids2d(fn: str, name: str, t):
     return t.shape
 
 
+def _choices(fn: str, name: str, t, dtype, tokens: int, k: int, cur: int) -> int:
+    """The pointer of what each choice has, [tokens, k] (or as many values in one dimension).  Another last dimension is another order
+    of the same values, [k, tokens] above all, and is refused."""
+    if isinstance(t, torch.Tensor) and t.dim() != 1 and (t.dim() != 2 or t.shape[1] != k):
+        raise ValueError(f"{fn}: {name} must be [{tokens}, {k}], got {tuple(t.shape)}")
+    return _array(fn, name, t, dtype, tokens * k, cur)
+
+
 def _workspace(fn: str, t, cur: int):
     """(pointer, bytes) of a contiguous workspace."""
     if not isinstance(t, torch.Tensor) or not t.is_contiguous() or t.get_device() != cur:
@@ -765,6 +773,8 @@ def moe_sort_workspace_bytes(choices: int, experts: int) -> int:
 def _norm_weight(fn: str, weight, cols: int, cur: int):
     if not isinstance(weight, torch.Tensor) or weight.dtype not in _DTYPES:
         raise TypeError(f"{fn}: weight must be a bfloat16 or float32 tensor")
+    if weight.numel() != cols:                             # (a longer one belongs to a norm of another width)
+        raise ValueError(f"{fn}: weight must be [{cols}], got {tuple(weight.shape)}")
     return _array(fn, "weight", weight, weight.dtype, cols, cur), _DTYPES[weight.dtype]
 
 
@@ -815,7 +825,7 @@ def mx_moe_route(logits, ids, weights, normalize: bool = True, stream=None):
     T, k = _ids2d(fn, "ids", ids)
     lp, ldl, _, E = _rows2d(fn, "logits", logits, logits.dtype, T, None, cur)
     _check(fn, lib().mx_moe_route(lp, kind, ldl, T, E, k, 1 if normalize else 0, _array(fn, "ids", ids, torch.int32, T * k, cur),
-                                  _array(fn, "weights", weights, torch.float32, T * k, cur), _stream_on(cur, stream)))
+                                  _choices(fn, "weights", weights, torch.float32, T, k, cur), _stream_on(cur, stream)))
 
 
 def mx_moe_route_backward(logits, ids, dweights, dlogits, normalize: bool = True, stream=None):
@@ -826,7 +836,7 @@ def mx_moe_route_backward(logits, ids, dweights, dlogits, normalize: bool = True
     dp, ldd, _, _ = _rows2d(fn, "dlogits", dlogits, logits.dtype, T, E, cur)
     _check(fn, lib().mx_moe_route_backward(
         lp, kind, ldl, T, E, k, 1 if normalize else 0, _array(fn, "ids", ids, torch.int32, T * k, cur),
-        _array(fn, "dweights", dweights, torch.float32, T * k, cur), dp, ldd, _stream_on(cur, stream)))
+        _choices(fn, "dweights", dweights, torch.float32, T, k, cur), dp, ldd, _stream_on(cur, stream)))
 
 
 def mx_moe_sort(ids, group_offsets, rows, source, workspace, stream=None):
@@ -838,7 +848,7 @@ def mx_moe_sort(ids, group_offsets, rows, source, workspace, stream=None):
     ws, ws_bytes = _workspace(fn, workspace, cur)
     _check(fn, lib().mx_moe_sort(
         _array(fn, "ids", ids, i32, n, cur), T, k, G, _array(fn, "group_offsets", group_offsets, torch.int64, G + 1, cur),
-        _array(fn, "rows", rows, i32, n, cur), None if source is None else _array(fn, "source", source, i32, n, cur), ws, ws_bytes,
+        _choices(fn, "rows", rows, i32, T, k, cur), None if source is None else _array(fn, "source", source, i32, n, cur), ws, ws_bytes,
         _stream_on(cur, stream)))
 
 
@@ -879,7 +889,7 @@ def mx_moe_combine(z, rows, y, weights=None, residual=None, stream=None):
     rp, ldr = _like(fn, "residual", residual, bf, y.shape, cur)
     _check(fn, lib().mx_moe_combine(
         zp, ldz, R, H, _array(fn, "rows", rows, torch.int32, T * k, cur),
-        None if weights is None else _array(fn, "weights", weights, torch.float32, T * k, cur), T, k, rp, ldr, yp, ldy,
+        None if weights is None else _choices(fn, "weights", weights, torch.float32, T, k, cur), T, k, rp, ldr, yp, ldy,
         _stream_on(cur, stream)))
 
 
@@ -891,8 +901,8 @@ def mx_moe_combine_backward(dy, z, rows, weights, dz, dweights, stream=None):
     gp, ldg, _, _ = _rows2d(fn, "dy", dy, bf, T, H, cur)
     dp, ldd, _, _ = _rows2d(fn, "dz", dz, bf, R, H, cur)
     _check(fn, lib().mx_moe_combine_backward(
-        gp, ldg, zp, ldz, R, H, _array(fn, "rows", rows, torch.int32, T * k, cur), _array(fn, "weights", weights, f32, T * k, cur), T, k,
-        dp, ldd, _array(fn, "dweights", dweights, f32, T * k, cur), _stream_on(cur, stream)))
+        gp, ldg, zp, ldz, R, H, _array(fn, "rows", rows, torch.int32, T * k, cur), _choices(fn, "weights", weights, f32, T, k, cur), T, k,
+        dp, ldd, _choices(fn, "dweights", dweights, f32, T, k, cur), _stream_on(cur, stream)))
 
 
 def mx_count_mismatch(x, y, count, stream=None):
