@@ -1,15 +1,17 @@
-"""The forms that the operators between a layer's products take by their sizes: every kind of width of the norm from 512 rows on, and
-wide rows that FP32 does not hold.  Against the 64-bit forms of layer_ref.py and against the same rows in another form."""
+"""The forms that the operators between a layer's products take by their sizes: every kind of width of the norm from 512 rows on,
+wide rows that FP32 does not hold, rows of logits that are not finite, long runs of the norm gradient's rings with what each turn
+adds, and the sort on both sides of its switches.  Against the 64-bit forms of layer_ref.py and against the same rows in another
+form."""
 import numpy as np
 import pytest
 import torch
 
 import layer_ref as ref
-from test_gpu_layer import codes_of, host, mx, rand, run_norm, same, within, y_bound      # noqa: F401
+from test_gpu_layer import codes_of, host, mx, rand, run_norm, run_sort, same, some_ids, within, y_bound      # noqa: F401
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
-BF, F32 = torch.bfloat16, torch.float32
+BF, F32, U8 = torch.bfloat16, torch.float32, torch.uint8
 
 
 def norm_into_marked(mx, x, w, eps, res):
@@ -103,3 +105,62 @@ def test_route_gradient_of_rows_that_are_not_finite(mx, normalize, dtype, expert
         else:
             assert np.isnan(got[t]).all()
     assert np.isfinite(got[4:]).all() and got[4, 3] == 0 and not got[5].any()
+
+
+# Sizes of which every CTA of the gradient has at least three turns on 152 SMs: (rows, cols, most turns of a CTA's row or lane's).
+# Rows that share a warp: 304 CTAs of 8 warps with 4, 2 or 1 rows each.  A CTA a row: up to four CTAs an SM.
+LONG = [(30000, 64), (15001, 128), (7600, 256), (7501, 512), (7400, 1000), (2000, 1032), (1501, 2048), (1400, 4096), (1001, 5120), (960, 8192),
+        (520, 8200), (500, 16384)]
+
+
+def longest_chain(rows, cols):
+    """Additions that one summand of dweight may pass: the turns of a lane or thread, then at most 2 in the butterfly, 8 warps or 2 CTAs,
+    10 loads of the second kernel and 5 levels of its butterfly."""
+    side = 4 if cols <= 64 else 2 if cols <= 128 else 1
+    turns = -(-rows // (304 * 8 * side)) if cols <= 1024 else -(-rows // 152)        # (a CTA an SM at least, whatever the form)
+    return turns + 25
+
+
+@pytest.mark.parametrize("rows,cols", LONG)
+def test_norm_gradient_over_many_turns(mx, rows, cols):
+    """Ordinary rows and ones that FP32 does not hold side by side.  n has 24 roundings beside the sums'."""
+    h, dy, dsum = rand(109, rows, cols), rand(110, rows, cols, scale=0.01), rand(111, rows, cols, scale=0.01)
+    w = rand(112, cols, scale=0.2).float() + 1.0
+    h[1::7] *= 2.0 ** 70                                   # (exact: powers of two)
+    h[2::7] *= 2.0 ** -80
+    dy[3::5] *= 2.0 ** -40
+    dx, dw = torch.empty_like(h), torch.full((cols,), 9.0, device=DEV)
+    ws = torch.full((mx.rmsnorm_workspace_bytes(rows, cols),), 255, dtype=U8, device=DEV)
+    mx.mx_rmsnorm_backward(dy, h, w, 0.0, dx, dw, ws, dsum=dsum)
+    want, wdw, bound, size = ref.norm_backward(host(dy), host(h), host(w), 0.0, host(dsum))
+    within(dx, want, bound)
+    within(dw, wdw, (longest_chain(rows, cols) + 24) * ref.EPS32 * size)
+
+
+@pytest.mark.parametrize("rows,cols", LONG)
+def test_norm_gradient_takes_every_row_into_dweight(mx, rows, cols):
+    """dy is zero but in a few rows, so that a row left out shows whole."""
+    h, w = rand(113, rows, cols), torch.ones(cols, dtype=BF, device=DEV)
+    ws = torch.full((mx.rmsnorm_workspace_bytes(rows, cols),), 255, dtype=U8, device=DEV)
+    n = host(h)
+    n = n / np.sqrt((n * n).mean(-1, keepdims=True) + 1e-6)
+    for picked in ([0], [rows - 1], [rows - 2, rows // 2, 1], list(range(5, rows, 101))):
+        dy = torch.zeros_like(h)
+        dy[picked] = rand(114, len(picked), cols)
+        dx, dw = torch.empty_like(h), torch.full((cols,), 9.0, device=DEV)
+        mx.mx_rmsnorm_backward(dy, h, w, 1e-6, dx, dw, ws)
+        each = host(dy[picked]) * n[picked]
+        within(dw, each.sum(0), (len(picked) + 24 + 25) * ref.EPS32 * np.abs(each).sum(0))
+
+
+# choices on both sides of 16384, 32768, 65536 and 131072
+@pytest.mark.parametrize("tokens,k,experts", [(2048, 8, 128), (2731, 6, 33), (4096, 8, 1000), (10923, 3, 128), (65537, 1, 7), (8193, 8, 60),
+                                              (16384, 8, 1024), (12000, 9, 513), (43691, 3, 1024)])
+@pytest.mark.parametrize("idle", [0.0, 0.3])
+def test_sort_on_both_sides_of_its_switches(mx, tokens, k, experts, idle):
+    ids = some_ids(115, tokens, k, experts, idle, distinct=False)
+    got = run_sort(mx, ids, experts)
+    for a, b, name in zip(got, ref.sort(host(ids), experts), ("group_offsets", "rows", "source")):
+        assert np.array_equal(host(a), b), name
+    a, b, _ = run_sort(mx, ids, experts, source=False)
+    assert torch.equal(a, got[0]) and torch.equal(b, got[1])
