@@ -30,7 +30,8 @@ typedef enum { MX_DTYPE_BF16 = 0, MX_DTYPE_FP32 = 1 } mx_dtype;
 
 /* Root-mean-square norm with the residual's addition, and its output in MXFP8.  Per row:
  *   h = BF16(x + residual)                            (h = x without a residual)
- *   y = BF16(h * weight / sqrt(mean(h^2) + eps))      (FP32: the product with weight, exact where that is BF16, times 1 / sqrt)
+ *   y = BF16(h * weight / sqrt(mean(h^2) + eps))      (FP32: the product with weight, exact where that is BF16 and
+ *                                                      the product a normal number, times 1 / sqrt)
  *   codes and scales: those of mx_quantize_mxfp8(y), byte for byte, in either orientation
  *   x, residual [rows, cols] BF16, rows ldx and ldr elements apart;  residual NULL: none
  *   weight   [cols], BF16 or FP32 by weight_type

@@ -295,9 +295,10 @@ __global__ void __launch_bounds__(NN_THREADS) norm_narrow_kernel(const NormArgs 
 
 // Without column-wise codes: one row a group of blockDim.x threads, blockDim.y rows a CTA; NV vectors of eight elements a thread.
 // At most four a thread and 64 registers: with eight, one CTA an SM ran through 32 KB of straight-line code for every row
-// (1003 x 14336 took 54 us, now 17: three turns of two CTAs an SM, each a row's loads, meeting and stores after one another).
+// (1003 x 14336 took 54 us, now 17: four turns of two CTAs an SM, each a row's loads, meeting and stores after one another, which wait for
+// memory most of the time: half of the issue slots are taken).
 // FULL: the threads' vectors are the row exactly, no comparisons (8192 x 4096 to codes 29.8 to 27.3 us).  With residual, sum and codes
-// 8192 x 4096 takes 36 us, 97 % of the measured copy rate.
+// 8192 x 4096 takes 36.5 us on the same tensors again and again, 96 % of the measured copy rate, and 40.3 where they change.
 constexpr int NR_THREADS = NORM_ROWS_THREADS;
 template <int NV, bool W32, bool FULL>
 __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs a) {
@@ -378,7 +379,7 @@ __global__ void __launch_bounds__(NR_THREADS, 2) norm_rows_kernel(const NormArgs
 // (eight a thread), so the sums of squares of a segment are one butterfly; the CTAs write theirs into each other's shared memory
 // and meet once.  The tile waits in shared memory, where the output takes its place and a thread then finds the two columns
 // that it quantizes.
-// 8192 x 4096 with residual, sum and both orientations: 53 us, 75 % of the measured copy rate.  Some 7 us are the cluster: eight CTAs
+// 8192 x 4096 with residual, sum and both orientations: 53 us, 76 % of the measured copy rate; 8192 x 8192 112, 72 %.  Some 7 us are the cluster: eight CTAs
 // start and meet together, and 5 % of the SMs fit no cluster of eight.  The transposed codes leave in pieces of 32 bytes and their
 // scales in single bytes.  No quicker: four CTAs of 1024 columns, five CTAs an SM with 48 registers (59), the sums sent
 // asynchronously to a barrier in place of the meeting, all loads at once.
@@ -619,8 +620,9 @@ template <int THREADS_, int PER_SM_, int NV_>
 struct BackwardForm {
     static constexpr int THREADS = THREADS_, PER_SM = PER_SM_, NV = NV_;
 };
-constexpr int NB_CLUSTER = 2;                              // wider clusters leave SMs idle (four: 72 us where two take 57)
-constexpr int NB_PARTS = 304;                              // most partial sums of a column: pairs of four CTAs an SM
+constexpr int NB_CLUSTER = 2;                              // wider clusters leave SMs idle (8192 x 4096 47 us, with four 63, with eight 65; 777 x 2048
+                                                           // 8.7, 10.6 and 11.8)
+constexpr int NB_PARTS = 304;                              // most partial sums of a column: two an SM of 152 (a pair of CTAs has one, four fit an SM)
 constexpr int NB_STAGES = 2;
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
