@@ -749,9 +749,16 @@ def _ids2d(fn: str, name: str, t):
 def _choices(fn: str, name: str, t, dtype, tokens: int, k: int, cur: int) -> int:
     """The pointer of what each choice has, [tokens, k] (or as many values in one dimension).  Another last dimension is another order
     of the same values, [k, tokens] above all, and is refused."""
-    if isinstance(t, torch.Tensor) and t.dim() != 1 and (t.dim() != 2 or t.shape[1] != k):
-        raise ValueError(f"{fn}: {name} must be [{tokens}, {k}], got {tuple(t.shape)}")
-    return _array(fn, name, t, dtype, tokens * k, cur)
+    shape = t.shape
+    if len(shape) == 2 and shape[1] == k:
+        n = shape[0] * k
+    elif len(shape) == 1:
+        n = shape[0]
+    else:
+        raise ValueError(f"{fn}: {name} must be [{tokens}, {k}], got {tuple(shape)}")
+    if t.dtype is not dtype or n < tokens * k or t.get_device() != cur or not t.is_contiguous():
+        _refuse(fn, name, t, dtype, tokens * k)
+    return t.data_ptr()
 
 
 def _workspace(fn: str, t, cur: int):
@@ -775,7 +782,9 @@ def _norm_weight(fn: str, weight, cols: int, cur: int):
         raise TypeError(f"{fn}: weight must be a bfloat16 or float32 tensor")
     if weight.numel() != cols:                             # (a longer one belongs to a norm of another width)
         raise ValueError(f"{fn}: weight must be [{cols}], got {tuple(weight.shape)}")
-    return _array(fn, "weight", weight, weight.dtype, cols, cur), _DTYPES[weight.dtype]
+    if weight.get_device() != cur or not weight.is_contiguous():
+        _refuse(fn, "weight", weight, weight.dtype, cols)
+    return weight.data_ptr(), _DTYPES[weight.dtype]
 
 
 def mx_rmsnorm_mxfp8(x, weight, eps: float, residual=None, sum_out=None, y=None, q_row=None, s_row=None, q_col=None, s_col=None,
